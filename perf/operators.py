@@ -169,7 +169,7 @@ def prepare(case, seed):
     # Keys and values are the two parts of one up-projection's output; the rotary part is one row for all heads.
     up = randn(tk, heads, NOPE + VDIM, dtype=dtype)
     s.update(q=randn(tq, heads, NOPE + ROPE, dtype=dtype), k_nope=up[..., :NOPE], k_rope=randn(tk, ROPE, dtype=dtype), v=up[..., NOPE:],
-             cu_q=cu_q.to(dev), cu_k=cu_k.to(dev), max_q=int(new.max()), scale=(NOPE + ROPE) ** -0.5, causal=case["causal"],
+             cu_q=cu_q.to(dev), cu_k=cu_k.to(dev), scale=(NOPE + ROPE) ** -0.5, causal=case["causal"],
              out=torch.empty(tq, heads, VDIM, dtype=dtype, device=dev), lse=torch.empty(tq, heads, dtype=torch.float32, device=dev))
     return s
 
@@ -196,7 +196,7 @@ def _run_own(s):
         out, lse, s["workspace"] = api.attend_paged(s["q"], s["cache"], s["lens"], s["table"], s["page"], s["scale"],
                                                     out=s["out"], lse=s["lse"], workspace=s["workspace"])
     else:
-        out, lse = api.attend_prompt(s["q"], s["k_nope"], s["k_rope"], s["v"], s["cu_q"], s["cu_k"], s["max_q"], s["scale"],
+        out, lse = api.attend_prompt(s["q"], s["k_nope"], s["k_rope"], s["v"], s["cu_q"], s["cu_k"], s["scale"],
                                      causal=s["causal"], out=s["out"], lse=s["lse"])
     return {"out": out, "lse": lse}
 
