@@ -207,6 +207,185 @@ topk_status_t topk_transform_noalloc(const float* scores, int64_t row_stride, co
                                      int64_t page_table_stride, int32_t page_size, int32_t k,
                                      int32_t* out_indices, int32_t* out_raw_indices_or_null, topk_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around the selection: block tables, the paged latent cache, and attention
+ * over it.
+ *
+ * A latent row has TOPK_LATENT_DIM values shared by all heads followed by
+ * TOPK_ROPE_DIM rotary ones, in bf16 or fp16.  The cache holds one row per
+ * slot; slot = page * page_size + offset, as topk_transform writes them.
+ * Strides are in elements.  Two-byte tensors that are read or written in
+ * rows have bases and strides that are multiples of 16 bytes (TOPK_EALIGN
+ * otherwise).  Sums, softmax statistics and norms are kept in fp32; outputs
+ * are rounded once.
+ */
+#define TOPK_LATENT_DIM 512
+#define TOPK_ROPE_DIM 64
+#define TOPK_NOPE_DIM 128 /* unrotated values per head of the expanded form */
+#define TOPK_VALUE_DIM 128 /* values per value head of the expanded form    */
+
+typedef enum {
+    TOPK_BF16 = 0,
+    TOPK_FP16 = 1
+} topk_dtype_t;
+
+/* Bits of status[1] of topk_block_tables. */
+#define TOPK_TABLES_NEGATIVE 0x1u  /* a negative length was treated as 0                 */
+#define TOPK_TABLES_ROW_FULL 0x2u  /* a request is longer than its page-table row holds  */
+#define TOPK_TABLES_NO_PAGES 0x4u  /* the free list ended before every request had pages */
+#define TOPK_TABLES_NO_TOKENS 0x8u /* the step has more new tokens than max_tokens       */
+
+/*
+ * Block tables and slot maps of one step, from request lengths on the device
+ * (one launch, no host read).  Request b holds context_lens[b] tokens and
+ * gets new_lens[b] more.  With P(n) = ceil(n / page_size), it needs the pages
+ * P(context)..P(context + new) - 1; the requests take them from free_pages in
+ * order, request 0 first.  New token j of request b, number
+ * t = cu_new[b] + j of the step, has position p = context_lens[b] + j and slot
+ * page_table[b][p / page_size] * page_size + p % page_size.
+ *
+ *   context_lens, new_lens  device int32[batch]; negative ones count as 0.
+ *   batch             >= 1; batch * pages_per_row < 2^31.
+ *   page_size         power of two, 1 <= page_size <= 2^30.
+ *   free_pages        device int32[num_free]; num_free >= 0.
+ *   page_table        device int32[batch][page_table_stride], pages_per_row
+ *                     (>= 1, <= page_table_stride) of them used per row;
+ *                     only the entries of new pages are written: the next
+ *                     page of the list, or -1 once it has ended.
+ *   max_tokens        >= 0, the room of slots, positions and rows; tokens past
+ *                     it are dropped, their pages are not.
+ *   seq_lens          device int32[batch]: min(context + new,
+ *                     pages_per_row * page_size, 2^31 - 1).
+ *   cu_new            device int32[batch + 1]: 0, then the running sums of
+ *                     new_lens (at most 2^31 - 1).
+ *   slots             device int32[max_tokens]: -1 for a token whose page is
+ *                     negative or outside its row, and past the last token.
+ *   positions_or_null, rows_or_null  device int32[max_tokens]: each token's
+ *                     position and request, -1 past the last token.
+ *   status            device int32[2]: pages taken, TOPK_TABLES_* bits.
+ * Outputs other than page_table overlap no input.
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+topk_status_t topk_block_tables(const int32_t* context_lens, const int32_t* new_lens, int32_t batch,
+                                int32_t page_size, const int32_t* free_pages, int32_t num_free,
+                                int32_t* page_table, int64_t page_table_stride, int32_t pages_per_row,
+                                int32_t max_tokens, int32_t* seq_lens, int32_t* cu_new, int32_t* slots,
+                                int32_t* positions_or_null, int32_t* rows_or_null, int32_t* status,
+                                topk_stream_t stream);
+
+/*
+ * Writes latent rows to their slots of the cache: the root-mean-square norm
+ * of the 512 latent values, the rotation of the 64 rotary ones, and the store
+ * in one pass.
+ *   c' = c / sqrt(mean(c^2) + eps) * norm_weight      (norm_weight NULL: c' = c)
+ *   (a, b)' = (a cos - b sin, a sin + b cos)          (cos_sin NULL: unchanged)
+ * for pair i = 0..31 of the rotary values: (2i, 2i + 1) if interleaved, else
+ * (i, i + 32).
+ *   rows              device [tokens][row_stride], 576 values used per row.
+ *   norm_weight_or_null  device [512], the rows' type.
+ *   cos_sin_or_null   device float[num_positions][64]: 32 cosines, 32 sines.
+ *   positions         device int32[tokens]; needed with cos_sin.
+ *   slots             device int32[tokens]; a row whose slot is outside
+ *                     [0, num_slots), or whose position is outside
+ *                     [0, num_positions), is not written.  Which of two rows
+ *                     with one slot stays is not specified.
+ *   cache             device [num_slots][slot_stride].
+ *   tokens            >= 0 (0: nothing is enqueued).
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+topk_status_t topk_cache_append(const void* rows, int64_t row_stride, int32_t tokens, const void* norm_weight_or_null,
+                                float eps, const float* cos_sin_or_null, int32_t num_positions,
+                                const int32_t* positions_or_null, int32_t interleaved, const int32_t* slots,
+                                void* cache, int64_t slot_stride, int32_t num_slots, topk_dtype_t dtype,
+                                topk_stream_t stream);
+
+/*
+ * Bytes of device workspace (16-byte aligned, contents free) that
+ * topk_attend_selected and topk_attend_paged need for batch rows of `queries`
+ * queries (selected: 1) and `heads` heads: the partial sums of rows that
+ * several blocks share.  0 for arguments out of range.
+ */
+size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
+
+/*
+ * Latent attention over selected slots (absorbed form; one query per row):
+ *   s[b][h][j] = scale * q[b][h][:] . cache[indices[b][j]][:]       (576 terms)
+ *   p = softmax of s over the j that are seen
+ *   out[b][h][:] = sum_j p[b][h][j] cache[indices[b][j]][:512]
+ *   lse[b][h]    = log sum_j exp(s[b][h][j])
+ * Index j of row b is seen if it is in [0, num_slots) and, where seq_lens is
+ * given, j < seq_lens[b] (topk_transform's rows: -1 in the slots past
+ * min(k, seq_len)).  A slot that is listed twice counts twice; rows of the
+ * cache that are not seen are never used, whatever they hold.  A row that
+ * sees nothing gets zeros and an lse of -inf.  Products of two-byte values
+ * are exact and summed in fp32; the weights p are rounded to the cache's type
+ * before the second product.
+ *   q                 device [rows][q_row_stride], head h at h * q_head_stride.
+ *   cache             device [num_slots][slot_stride], 576 values used.
+ *   indices           device int32[rows][indices_stride], k used per row.
+ *   rows, heads, k    >= 1; rows * heads <= 2^30.
+ *   out               device [rows][heads][512], contiguous.
+ *   lse_or_null       device float[rows][heads].
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_ENOSPACE, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+topk_status_t topk_attend_selected(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* cache,
+                                   int64_t slot_stride, int32_t num_slots, const int32_t* indices,
+                                   int64_t indices_stride, const int32_t* seq_lens_or_null, int32_t rows,
+                                   int32_t heads, int32_t k, float scale, topk_dtype_t dtype, void* out,
+                                   float* lse_or_null, void* workspace, size_t workspace_bytes,
+                                   topk_stream_t stream);
+
+/*
+ * The same over whole rows through the page table, for `queries` >= 1 newest
+ * tokens per request: query i of request b sees the positions
+ * t < seq_lens[b] - (queries - 1 - i) whose slot
+ * page_table[b][t / page_size] * page_size + t % page_size is in
+ * [0, num_slots) (seq_lens counts the new tokens; values above max_seq_len
+ * count as max_seq_len, negative ones as 0).
+ *   q                 device [batch][q_row_stride], query i at
+ *                     i * q_query_stride, head h at h * q_head_stride.
+ *   page_table        as in topk_transform; page_table_stride >=
+ *                     ceil(max_seq_len / page_size).
+ *   out               device [batch][queries][heads][512], contiguous.
+ *   lse_or_null       device float[batch][queries][heads].
+ */
+topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_query_stride, int64_t q_head_stride,
+                                const void* cache, int64_t slot_stride, int32_t num_slots, const int32_t* seq_lens,
+                                const int32_t* page_table, int64_t page_table_stride, int32_t page_size,
+                                int32_t max_seq_len, int32_t batch, int32_t queries, int32_t heads, float scale,
+                                topk_dtype_t dtype, void* out, float* lse_or_null, void* workspace,
+                                size_t workspace_bytes, topk_stream_t stream);
+
+/*
+ * Latent attention in its expanded form, for prompts (ragged, one launch):
+ * queries and keys of 128 + 64 values, the keys' 64 rotary ones shared by the
+ * heads, values of 128:
+ *   s[i][h][j] = scale * (q[i][h][:128] . k_nope[j][h][:] + q[i][h][128:] . k_rope[j][:])
+ * Request b has the queries cu_q[b]..cu_q[b+1]-1 and the keys
+ * cu_k[b]..cu_k[b+1]-1.  A query sees its request's keys; with causal != 0
+ * the request's last query sees all of them and each one before it one key
+ * less.  A query that sees nothing gets zeros and an lse of -inf; tokens that
+ * are in no request are not written.  Keys and values of other requests, or
+ * of none, are never used, whatever they hold; values of one request that a
+ * query does not see (causal) must be finite.
+ *   q                 device [total_q][q_token_stride], head h at h * q_head_stride
+ *   k_nope            device [total_k][k_token_stride], head h at h * k_head_stride
+ *   k_rope            device [total_k][k_rope_stride]
+ *   v                 device [total_k][v_token_stride], head h at h * v_head_stride
+ *   cu_q, cu_k        device int32[batch + 1], not decreasing; values outside
+ *                     [0, total] are clamped to it.
+ *   total_q, total_k  >= 0 (total_q 0: nothing is enqueued).
+ *   out               device [total_q][heads][128], contiguous.
+ *   lse_or_null       device float[total_q][heads].
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,
+                                 int64_t k_token_stride, int64_t k_head_stride, const void* k_rope,
+                                 int64_t k_rope_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                 const int32_t* cu_q, const int32_t* cu_k, int32_t batch, int32_t total_q,
+                                 int32_t total_k, int32_t heads, float scale, int32_t causal, topk_dtype_t dtype,
+                                 void* out, float* lse_or_null, topk_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* topk_status_string(topk_status_t status);
 

@@ -30,6 +30,19 @@ TOPK_FLAG_INTERNAL = 0x10
 
 TOPK_NOALLOC_MAX_BATCH = 16384
 
+TOPK_LATENT_DIM = 512
+TOPK_ROPE_DIM = 64
+TOPK_NOPE_DIM = 128
+TOPK_VALUE_DIM = 128
+
+TOPK_BF16 = 0
+TOPK_FP16 = 1
+
+TOPK_TABLES_NEGATIVE = 0x1
+TOPK_TABLES_ROW_FULL = 0x2
+TOPK_TABLES_NO_PAGES = 0x4
+TOPK_TABLES_NO_TOKENS = 0x8
+
 EXPORTED = (
     "topk_plan_workspace_bytes",
     "topk_plan",
@@ -38,6 +51,12 @@ EXPORTED = (
     "topk_transform_launches",
     "topk_page_transform",
     "topk_key_map",
+    "topk_block_tables",
+    "topk_cache_append",
+    "topk_attend_workspace_bytes",
+    "topk_attend_selected",
+    "topk_attend_paged",
+    "topk_attend_prompt",
     "topk_read_flags",
     "topk_status_string",
     "topk_last_error_string",
@@ -105,6 +124,22 @@ def _load() -> ctypes.CDLL:
     lib.topk_page_transform.restype = ctypes.c_int
     lib.topk_key_map.argtypes = [p, i64, p, p]
     lib.topk_key_map.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.topk_block_tables.argtypes = [p, p, i32, i32, p, i32, p, i64, i32, i32, p, p, p, p, p, p, p]
+    lib.topk_block_tables.restype = ctypes.c_int
+    lib.topk_cache_append.argtypes = [p, i64, i32, p, f32, p, i32, p, i32, p, p, i64, i32, ctypes.c_int, p]
+    lib.topk_cache_append.restype = ctypes.c_int
+    lib.topk_attend_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.topk_attend_workspace_bytes.restype = sz
+    lib.topk_attend_selected.argtypes = [p, i64, i64, p, i64, i32, p, i64, p, i32, i32, i32, f32, ctypes.c_int, p, p,
+                                         p, sz, p]
+    lib.topk_attend_selected.restype = ctypes.c_int
+    lib.topk_attend_paged.argtypes = [p, i64, i64, i64, p, i64, i32, p, p, i64, i32, i32, i32, i32, i32, f32,
+                                      ctypes.c_int, p, p, p, sz, p]
+    lib.topk_attend_paged.restype = ctypes.c_int
+    lib.topk_attend_prompt.argtypes = [p, i64, i64, p, i64, i64, p, i64, p, i64, i64, p, p, i32, i32, i32, i32, f32,
+                                       i32, ctypes.c_int, p, p, p]
+    lib.topk_attend_prompt.restype = ctypes.c_int
     lib.topk_read_flags.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), i32, p]
     lib.topk_read_flags.restype = ctypes.c_int
     lib.topk_status_string.argtypes = [ctypes.c_int]
@@ -206,6 +241,70 @@ def topk_page_transform(raw_indices: torch.Tensor, batch: int, k: int, page_tabl
 
 def topk_key_map(x: torch.Tensor, n: int, keys: torch.Tensor, stream=None) -> None:
     _check("topk_key_map", _lib.topk_key_map(_ptr(x), n, _ptr(keys), _stream(stream, x.device)))
+
+
+def topk_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, batch: int, page_size: int,
+                      free_pages: torch.Tensor | None, num_free: int, page_table: torch.Tensor,
+                      page_table_stride: int, pages_per_row: int, max_tokens: int, seq_lens: torch.Tensor,
+                      cu_new: torch.Tensor, slots: torch.Tensor, positions_or_null: torch.Tensor | None,
+                      rows_or_null: torch.Tensor | None, status: torch.Tensor, stream=None) -> None:
+    """Page-table entries, lengths and slot map of one step, from request lengths."""
+    _check("topk_block_tables", _lib.topk_block_tables(
+        _ptr(context_lens), _ptr(new_lens), batch, page_size, _ptr(free_pages), num_free, _ptr(page_table),
+        page_table_stride, pages_per_row, max_tokens, _ptr(seq_lens), _ptr(cu_new), _ptr(slots),
+        _ptr(positions_or_null), _ptr(rows_or_null), _ptr(status), _stream(stream, context_lens.device)))
+
+
+def topk_cache_append(rows: torch.Tensor, row_stride: int, tokens: int, norm_weight_or_null: torch.Tensor | None,
+                      eps: float, cos_sin_or_null: torch.Tensor | None, num_positions: int,
+                      positions_or_null: torch.Tensor | None, interleaved: bool, slots: torch.Tensor,
+                      cache: torch.Tensor, slot_stride: int, num_slots: int, dtype: int, stream=None) -> None:
+    """Norm, rotation and paged store of latent rows."""
+    _check("topk_cache_append", _lib.topk_cache_append(
+        _ptr(rows), row_stride, tokens, _ptr(norm_weight_or_null), eps, _ptr(cos_sin_or_null), num_positions,
+        _ptr(positions_or_null), int(interleaved), _ptr(slots), _ptr(cache), slot_stride, num_slots, dtype,
+        _stream(stream, cache.device)))
+
+
+def topk_attend_workspace_bytes(batch: int, queries: int, heads: int) -> int:
+    return int(_lib.topk_attend_workspace_bytes(batch, queries, heads))
+
+
+def topk_attend_selected(q: torch.Tensor, q_row_stride: int, q_head_stride: int, cache: torch.Tensor,
+                         slot_stride: int, num_slots: int, indices: torch.Tensor, indices_stride: int,
+                         seq_lens_or_null: torch.Tensor | None, rows: int, heads: int, k: int, scale: float,
+                         dtype: int, out: torch.Tensor, lse_or_null: torch.Tensor | None, workspace: torch.Tensor,
+                         stream=None) -> None:
+    """Latent attention over selected slots."""
+    _check("topk_attend_selected", _lib.topk_attend_selected(
+        _ptr(q), q_row_stride, q_head_stride, _ptr(cache), slot_stride, num_slots, _ptr(indices), indices_stride,
+        _ptr(seq_lens_or_null), rows, heads, k, scale, dtype, _ptr(out), _ptr(lse_or_null), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream, q.device)))
+
+
+def topk_attend_paged(q: torch.Tensor, q_row_stride: int, q_query_stride: int, q_head_stride: int,
+                      cache: torch.Tensor, slot_stride: int, num_slots: int, seq_lens: torch.Tensor,
+                      page_table: torch.Tensor, page_table_stride: int, page_size: int, max_seq_len: int, batch: int,
+                      queries: int, heads: int, scale: float, dtype: int, out: torch.Tensor,
+                      lse_or_null: torch.Tensor | None, workspace: torch.Tensor, stream=None) -> None:
+    """Latent attention over whole rows through the page table."""
+    _check("topk_attend_paged", _lib.topk_attend_paged(
+        _ptr(q), q_row_stride, q_query_stride, q_head_stride, _ptr(cache), slot_stride, num_slots, _ptr(seq_lens),
+        _ptr(page_table), page_table_stride, page_size, max_seq_len, batch, queries, heads, scale, dtype, _ptr(out),
+        _ptr(lse_or_null), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, q.device)))
+
+
+def topk_attend_prompt(q: torch.Tensor, q_token_stride: int, q_head_stride: int, k_nope: torch.Tensor,
+                       k_token_stride: int, k_head_stride: int, k_rope: torch.Tensor, k_rope_stride: int,
+                       v: torch.Tensor, v_token_stride: int, v_head_stride: int, cu_q: torch.Tensor,
+                       cu_k: torch.Tensor, batch: int, total_q: int, total_k: int, heads: int, scale: float,
+                       causal: bool, dtype: int, out: torch.Tensor, lse_or_null: torch.Tensor | None,
+                       stream=None) -> None:
+    """Expanded latent attention for prompts."""
+    _check("topk_attend_prompt", _lib.topk_attend_prompt(
+        _ptr(q), q_token_stride, q_head_stride, _ptr(k_nope), k_token_stride, k_head_stride, _ptr(k_rope),
+        k_rope_stride, _ptr(v), v_token_stride, v_head_stride, _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k,
+        heads, scale, int(causal), dtype, _ptr(out), _ptr(lse_or_null), _stream(stream, q.device)))
 
 
 def topk_read_flags(workspace: torch.Tensor, clear: bool = False, stream=None) -> int:

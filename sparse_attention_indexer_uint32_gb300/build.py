@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libtopkidx.so")
-SOURCES = ["topk_kernels.cu", "topk_stream.cu", "topk_warp.cu", "topk_split.cu", "topkidx_api.cu", "topk_noalloc.cu"]
+SOURCES = ["topk_kernels.cu", "topk_stream.cu", "topk_warp.cu", "topk_split.cu", "topkidx_api.cu", "topk_noalloc.cu",
+           "serve_tables.cu", "serve_append.cu", "attend_latent.cu", "attend_prompt.cu", "attend_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,103 @@
+// attend_internal.h -- launch parameters of the block-table, cache-append and
+// attention kernels, shared by the host side of the ABI (attend_api.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "topkidx.h"
+
+namespace topkidx {
+
+constexpr int kLatent = TOPK_LATENT_DIM;
+constexpr int kRope = TOPK_ROPE_DIM;
+constexpr int kWidth = kLatent + kRope;
+constexpr int kNope = TOPK_NOPE_DIM;
+constexpr int kValue = TOPK_VALUE_DIM;
+
+// The ABI's device check and CUDA-error record (topkidx_api.cu).
+topk_status_t api_check_device();
+topk_status_t api_cuda_fail(cudaError_t e, const char* where);
+
+struct TablesParams {
+    const int32_t* context;
+    const int32_t* fresh;
+    int32_t batch;
+    int32_t log2_page;
+    const int32_t* free_pages;
+    int32_t num_free;
+    int32_t* table;
+    int64_t table_stride;
+    int32_t width;
+    int32_t max_tokens;
+    int32_t* seq_lens;
+    int32_t* cu_new;
+    int32_t* slots;
+    int32_t* positions;  // or null
+    int32_t* rows;       // or null
+    int32_t* status;
+};
+cudaError_t launch_block_tables(const TablesParams& p, cudaStream_t stream);
+
+struct AppendParams {
+    const void* rows;
+    int64_t row_stride;
+    int32_t tokens;
+    const void* weight;  // or null
+    float eps;
+    const float* cos_sin;  // or null
+    int32_t num_positions;
+    const int32_t* positions;
+    const int32_t* slots;
+    void* cache;
+    int64_t slot_stride;
+    int32_t num_slots;
+};
+cudaError_t launch_cache_append(const AppendParams& p, bool interleaved, topk_dtype_t dtype, cudaStream_t stream);
+
+// Absorbed latent attention: `batch` rows of queries x heads query heads over
+// up to max_len slots each, listed in `indices` or reached through `table`.
+struct LatentParams {
+    const void* q;
+    int64_t q_row_stride, q_query_stride, q_head_stride;
+    const void* cache;
+    int64_t slot_stride;
+    int32_t num_slots;
+    const int32_t* indices;  // null: through the page table
+    int64_t indices_stride;
+    const int32_t* seq_lens;  // null: every row has max_len indices
+    const int32_t* table;
+    int64_t table_stride;
+    int32_t log2_page;
+    int32_t max_len;
+    int32_t batch, queries, heads;
+    float scale;
+    void* out;
+    float* lse;  // or null
+    void* workspace;
+};
+size_t latent_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
+topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, cudaStream_t stream);
+
+struct PromptParams {
+    const void* q;
+    int64_t q_token_stride, q_head_stride;
+    const void* k_nope;
+    int64_t k_token_stride, k_head_stride;
+    const void* k_rope;
+    int64_t k_rope_stride;
+    const void* v;
+    int64_t v_token_stride, v_head_stride;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int32_t batch, total_q, total_k, heads;
+    float scale;
+    int32_t causal;
+    void* out;
+    float* lse;  // or null
+};
+topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, cudaStream_t stream);
+
+}  // namespace topkidx

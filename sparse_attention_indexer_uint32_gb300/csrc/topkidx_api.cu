@@ -13,6 +13,7 @@
 #include <mutex>
 #include <utility>
 
+#include "attend_internal.h"
 #include "topk_internal.h"
 #include "topkidx.h"
 
@@ -511,6 +512,13 @@ topk_status_t decide_dispatch(int32_t batch, int32_t max_seq_len, int32_t k, con
 }
 
 }  // namespace
+
+namespace topkidx {
+
+topk_status_t api_check_device() { return check_device(); }
+topk_status_t api_cuda_fail(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+
+}  // namespace topkidx
 
 extern "C" {
 
