@@ -320,7 +320,8 @@ size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads
  * sees nothing gets zeros and an lse of -inf.  Products of two-byte values
  * are exact and summed in fp32; the weights p are rounded to the cache's type
  * before the second product.
- *   q                 device [rows][q_row_stride], head h at h * q_head_stride.
+ *   q                 device [rows][q_row_stride], head h at h * q_head_stride
+ *                     (strides of at least 576 where there is more than one).
  *   cache             device [num_slots][slot_stride], 576 values used.
  *   indices           device int32[rows][indices_stride], k used per row.
  *   rows, heads, k    >= 1; rows * heads <= 2^30.
@@ -372,8 +373,12 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
  *   k_nope            device [total_k][k_token_stride], head h at h * k_head_stride
  *   k_rope            device [total_k][k_rope_stride]
  *   v                 device [total_k][v_token_stride], head h at h * v_head_stride
+ *                     (token strides of at least a row's values where there
+ *                     is more than one token; a head stride of 0: all heads
+ *                     alike)
  *   cu_q, cu_k        device int32[batch + 1], not decreasing; values outside
- *                     [0, total] are clamped to it.
+ *                     [0, total] are clamped to it, and one below an earlier
+ *                     one counts as that.
  *   total_q, total_k  >= 0 (total_q 0: nothing is enqueued).
  *   out               device [total_q][heads][128], contiguous.
  *   lse_or_null       device float[total_q][heads].
@@ -385,6 +390,17 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
                                  const int32_t* cu_q, const int32_t* cu_k, int32_t batch, int32_t total_q,
                                  int32_t total_k, int32_t heads, float scale, int32_t causal, topk_dtype_t dtype,
                                  void* out, float* lse_or_null, topk_stream_t stream);
+
+/*
+ * Copies the attention kernels' flag word of the current device (one per
+ * GPU, shared by all calls) to *flags_host after all work enqueued on
+ * `stream` so far (this call synchronises the stream).  TOPK_FLAG_TIMEOUT: a
+ * bounded device wait of some call since the last clearing gave up and that
+ * call's output is void.  clear != 0 resets the word afterwards.  The first
+ * call of an attention entry point on a device looks up the word's address;
+ * make it before any stream capture.
+ */
+topk_status_t topk_read_attend_flags(uint32_t* flags_host, int32_t clear, topk_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* topk_status_string(topk_status_t status);

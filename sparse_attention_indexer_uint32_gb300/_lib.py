@@ -57,6 +57,7 @@ EXPORTED = (
     "topk_attend_selected",
     "topk_attend_paged",
     "topk_attend_prompt",
+    "topk_read_attend_flags",
     "topk_read_flags",
     "topk_status_string",
     "topk_last_error_string",
@@ -140,6 +141,8 @@ def _load() -> ctypes.CDLL:
     lib.topk_attend_prompt.argtypes = [p, i64, i64, p, i64, i64, p, i64, p, i64, i64, p, p, i32, i32, i32, i32, f32,
                                        i32, ctypes.c_int, p, p, p]
     lib.topk_attend_prompt.restype = ctypes.c_int
+    lib.topk_read_attend_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, p]
+    lib.topk_read_attend_flags.restype = ctypes.c_int
     lib.topk_read_flags.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), i32, p]
     lib.topk_read_flags.restype = ctypes.c_int
     lib.topk_status_string.argtypes = [ctypes.c_int]
@@ -305,6 +308,13 @@ def topk_attend_prompt(q: torch.Tensor, q_token_stride: int, q_head_stride: int,
         _ptr(q), q_token_stride, q_head_stride, _ptr(k_nope), k_token_stride, k_head_stride, _ptr(k_rope),
         k_rope_stride, _ptr(v), v_token_stride, v_head_stride, _ptr(cu_q), _ptr(cu_k), batch, total_q, total_k,
         heads, scale, int(causal), dtype, _ptr(out), _ptr(lse_or_null), _stream(stream, q.device)))
+
+
+def topk_read_attend_flags(clear: bool = False, stream=None, device=None) -> int:
+    flags = ctypes.c_uint32(0)
+    _check("topk_read_attend_flags", _lib.topk_read_attend_flags(ctypes.byref(flags), int(clear),
+                                                                 _stream(stream, device)))
+    return int(flags.value)
 
 
 def topk_read_flags(workspace: torch.Tensor, clear: bool = False, stream=None) -> int:

@@ -66,6 +66,11 @@ def _whole(shape: tuple, **tensors) -> None:
             raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}: got {tuple(t.shape)}")
 
 
+def _step(t: torch.Tensor, dim: int, least: int) -> int:
+    """Stride of a dimension; `least` where there is one entry, whose stride means nothing."""
+    return t.stride(dim) if t.shape[dim] > 1 else least
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
     code = _DTYPES.get(t.dtype)
     if code is None:
@@ -103,7 +108,7 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         _whole((max_tokens,), slots=out.slots, positions=out.positions, rows=out.rows)
         _whole((2,), status=out.status)
     _lib.topk_block_tables(context_lens, new_lens, batch, page_size, free_pages, free_pages.numel(), page_table,
-                           page_table.stride(0), pages, max_tokens, *out, stream)
+                           _step(page_table, 0, pages), pages, max_tokens, *out, stream)
     return out
 
 
@@ -124,9 +129,9 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     _whole((_lib.TOPK_LATENT_DIM,), norm_weight=norm_weight)
     if cos_sin is not None:
         _whole((cos_sin.shape[0], _lib.TOPK_ROPE_DIM), cos_sin=cos_sin)
-    _lib.topk_cache_append(rows, rows.stride(0), tokens, norm_weight, eps, cos_sin,
+    _lib.topk_cache_append(rows, _step(rows, 0, width), tokens, norm_weight, eps, cos_sin,
                            0 if cos_sin is None else cos_sin.shape[0], positions, interleaved, slots, cache,
-                           cache.stride(0), cache.shape[0], code, stream)
+                           _step(cache, 0, width), cache.shape[0], code, stream)
 
 
 def _attend_outputs(q, cache, batch, queries, heads, out, lse, workspace):
@@ -164,8 +169,8 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
     _same(torch.int32, q.device, indices=indices, seq_lens=seq_lens)
     _whole((rows,), seq_lens=seq_lens)
     out, lse, workspace = _attend_outputs(q, cache, rows, 1, heads, out, lse, workspace)
-    _lib.topk_attend_selected(q, q.stride(0), q.stride(1), cache, cache.stride(0), cache.shape[0], indices,
-                              indices.stride(0), seq_lens, rows, heads, indices.shape[1], scale, code, out, lse,
+    _lib.topk_attend_selected(q, _step(q, 0, 0), _step(q, 1, 0), cache, _step(cache, 0, cache.shape[1]), cache.shape[0],
+                              indices, _step(indices, 0, indices.shape[1]), seq_lens, rows, heads, indices.shape[1], scale, code, out, lse,
                               workspace, stream)
     return out, lse, workspace
 
@@ -187,8 +192,8 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
     elif max_seq_len > page_table.shape[1] * page_size:
         raise ValueError(f"max_seq_len {max_seq_len} is over {page_table.shape[1]} pages of {page_size}")
     out, lse, workspace = _attend_outputs(q, cache, batch, queries, heads, out, lse, workspace)
-    _lib.topk_attend_paged(q, q.stride(0), q.stride(1), q.stride(2), cache, cache.stride(0), cache.shape[0],
-                           seq_lens, page_table, page_table.stride(0), page_size, max_seq_len, batch, queries, heads,
+    _lib.topk_attend_paged(q, _step(q, 0, 0), _step(q, 1, 0), _step(q, 2, 0), cache, _step(cache, 0, cache.shape[1]),
+                           cache.shape[0], seq_lens, page_table, _step(page_table, 0, page_table.shape[1]), page_size, max_seq_len, batch, queries, heads,
                            scale, code, out, lse, workspace, stream)
     return out, lse, workspace
 
@@ -220,7 +225,8 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
     else:
         _same(torch.float32, dev, lse=lse)
         _whole((total_q, heads), lse=lse)
-    _lib.topk_attend_prompt(q, q.stride(0), q.stride(1), k_nope, k_nope.stride(0), k_nope.stride(1), k_rope,
-                            k_rope.stride(0), v, v.stride(0), v.stride(1), cu_q, cu_k, cu_q.shape[0] - 1, total_q,
-                            total_k, heads, scale, causal, code, out, lse, stream)
+    _lib.topk_attend_prompt(q, _step(q, 0, nope + rope), _step(q, 1, nope + rope), k_nope, _step(k_nope, 0, nope),
+                            _step(k_nope, 1, nope), k_rope, _step(k_rope, 0, rope), v, _step(v, 0, value),
+                            _step(v, 1, value), cu_q, cu_k, cu_q.shape[0] - 1, total_q, total_k, heads, scale, causal,
+                            code, out, lse, stream)
     return out, lse

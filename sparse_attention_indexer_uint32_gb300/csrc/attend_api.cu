@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "attend_internal.h"
 #include "topkidx.h"
@@ -25,7 +26,34 @@ int log2_of(int32_t n) {
 // Rows of two-byte values: 16-byte aligned base and strides.
 bool row_stride_ok(int64_t stride, int64_t least) { return stride >= least && stride <= (int64_t{1} << 38); }
 
+// The rows of a tensor that a product reads: far enough apart not to overlap,
+// unless there is only one.
+bool token_stride_ok(int64_t stride, int64_t least, int64_t count) {
+    return row_stride_ok(stride, count > 1 ? least : 0);
+}
+
 constexpr int64_t kMaxQueryHeads = int64_t{1} << 30;
+
+// The word in which the attention kernels note a wait that gave up, one per GPU.
+__device__ uint32_t g_attend_flags;
+
+// Its address on the current device, looked up once per device.
+topk_status_t attend_flags(uint32_t** flags) {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mutex;
+    static void* known[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return api_cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= kMaxDevices) return api_cuda_fail(cudaErrorInvalidDevice, "attention flags");
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!known[dev]) {
+        e = cudaGetSymbolAddress(&known[dev], g_attend_flags);
+        if (e != cudaSuccess) return api_cuda_fail(e, "attention flags");
+    }
+    *flags = static_cast<uint32_t*>(known[dev]);
+    return TOPK_OK;
+}
 
 }  // namespace
 
@@ -92,13 +120,21 @@ topk_status_t check_latent(const LatentParams& p, topk_dtype_t dtype, size_t wor
     const size_t need = topk_attend_workspace_bytes(p.batch, p.queries, p.heads);
     if (need == 0 || p.num_slots < 1 || std::isnan(p.scale)) return TOPK_EINVAL;
     if (!row_stride_ok(p.slot_stride, kWidth)) return TOPK_EINVAL;
-    if (p.q_row_stride < 0 || p.q_query_stride < 0 || p.q_head_stride < 0) return TOPK_EINVAL;
+    if (!token_stride_ok(p.q_row_stride, kWidth, p.batch) || !token_stride_ok(p.q_query_stride, kWidth, p.queries) ||
+        !token_stride_ok(p.q_head_stride, kWidth, p.heads))
+        return TOPK_EINVAL;
     if (workspace_bytes < need) return TOPK_ENOSPACE;
     if (misaligned(p.q, 16) || misaligned(p.cache, 16) || misaligned(p.out, 16) || misaligned(p.workspace, 16) ||
         misaligned(p.lse, 4) || misaligned(p.indices, 4) || misaligned(p.seq_lens, 4) || misaligned(p.table, 4) ||
         p.q_row_stride % 8 || p.q_query_stride % 8 || p.q_head_stride % 8 || p.slot_stride % 8)
         return TOPK_EALIGN;
     return api_check_device();
+}
+
+topk_status_t run_latent(const LatentParams& p, topk_dtype_t dtype, cudaStream_t stream) {
+    uint32_t* flags = nullptr;
+    const topk_status_t st = attend_flags(&flags);
+    return st == TOPK_OK ? launch_latent(p, dtype, flags, stream) : st;
 }
 
 }  // namespace
@@ -129,7 +165,7 @@ topk_status_t topk_attend_selected(const void* q, int64_t q_row_stride, int64_t 
     p.lse = lse_or_null;
     p.workspace = workspace;
     const topk_status_t st = check_latent(p, dtype, workspace_bytes);
-    return st == TOPK_OK ? launch_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
+    return st == TOPK_OK ? run_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
 }
 
 topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_query_stride, int64_t q_head_stride,
@@ -162,7 +198,7 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
     p.lse = lse_or_null;
     p.workspace = workspace;
     const topk_status_t st = check_latent(p, dtype, workspace_bytes);
-    return st == TOPK_OK ? launch_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
+    return st == TOPK_OK ? run_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
 }
 
 topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,
@@ -175,9 +211,9 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
         return TOPK_EINVAL;
     if ((total_q > 0 && (!q || !out)) || (total_k > 0 && (!k_nope || !k_rope || !v))) return TOPK_EINVAL;
     if (static_cast<int64_t>(total_q) * heads > kMaxQueryHeads) return TOPK_EINVAL;
-    if (!row_stride_ok(q_token_stride, 0) || !row_stride_ok(q_head_stride, 0) || !row_stride_ok(k_token_stride, 0) ||
-        !row_stride_ok(k_head_stride, 0) || !row_stride_ok(k_rope_stride, 0) || !row_stride_ok(v_token_stride, 0) ||
-        !row_stride_ok(v_head_stride, 0))
+    if (!token_stride_ok(q_token_stride, kNope + kRope, total_q) || !token_stride_ok(k_token_stride, kNope, total_k) ||
+        !token_stride_ok(k_rope_stride, kRope, total_k) || !token_stride_ok(v_token_stride, kValue, total_k) ||
+        !row_stride_ok(q_head_stride, 0) || !row_stride_ok(k_head_stride, 0) || !row_stride_ok(v_head_stride, 0))
         return TOPK_EINVAL;
     if (misaligned(q, 16) || misaligned(k_nope, 16) || misaligned(k_rope, 16) || misaligned(v, 16) ||
         misaligned(out, 16) || misaligned(lse_or_null, 4) || misaligned(cu_q, 4) || misaligned(cu_k, 4) ||
@@ -190,7 +226,23 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
     PromptParams p = {q,      q_token_stride, q_head_stride, k_nope, k_token_stride, k_head_stride, k_rope,
                       k_rope_stride, v,       v_token_stride, v_head_stride, cu_q,   cu_k,          batch,
                       total_q, total_k, heads, scale,        causal, out,            lse_or_null};
-    return launch_prompt(p, dtype, reinterpret_cast<cudaStream_t>(stream));
+    uint32_t* flags = nullptr;
+    const topk_status_t st = attend_flags(&flags);
+    return st == TOPK_OK ? launch_prompt(p, dtype, flags, reinterpret_cast<cudaStream_t>(stream)) : st;
+}
+
+topk_status_t topk_read_attend_flags(uint32_t* flags_host, int32_t clear, topk_stream_t stream) {
+    if (!flags_host) return TOPK_EINVAL;
+    const topk_status_t dev = api_check_device();
+    if (dev != TOPK_OK) return dev;
+    uint32_t* flags = nullptr;
+    const topk_status_t st = attend_flags(&flags);
+    if (st != TOPK_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyAsync(flags_host, flags, sizeof(uint32_t), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess && clear) e = cudaMemsetAsync(flags, 0, sizeof(uint32_t), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "attention flags");
 }
 
 }  // extern "C"

@@ -79,7 +79,7 @@ struct LatentParams {
     void* workspace;
 };
 size_t latent_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
-topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, cudaStream_t stream);
+topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream);
 
 struct PromptParams {
     const void* q;
@@ -98,6 +98,6 @@ struct PromptParams {
     void* out;
     float* lse;  // or null
 };
-topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, cudaStream_t stream);
+topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream);
 
 }  // namespace topkidx

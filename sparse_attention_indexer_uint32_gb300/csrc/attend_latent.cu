@@ -1,54 +1,657 @@
-// attend_latent.cu -- absorbed latent attention over selected slots or whole
-// rows of the paged cache: one block per query head.
+// attend_latent.cu -- absorbed latent attention over the paged cache, over
+// selected slots or whole rows, on the tensor cores.
+//
+// Mathematics: as in attend_prompt.cu, with one latent row c_j for every head:
+// s_hj = q_h.c_j over 576 values, o_h = sum_j p_hj c_j over the first 512.  So a
+// row of the cache is read once for up to 128 (query, head) rows of the
+// products, 2 * 128 * 1088 operations on 1152 bytes: near the balance of the
+// tensor cores and the memory for 128 heads, bound by memory for fewer.
+//
+// A pair of blocks (a cluster, one per two SMs) takes 128 (query, head) rows
+// and walks the slots 128 at a time.  One sum of 128 x 512 in fp32 alone would
+// fill an SM's tensor memory, and 128 queries with 128 latent rows its shared
+// memory; the pair splits both: products are issued for two SMs at once
+// (cta_group::2, M = 128), block r holding the rows 64 r.. of A, half of B and
+// the sums of its own rows.  For the first product B is the tile's slots 64 r..
+// (all 576 values, K contiguous), for the second the values 256 r.. of all 128
+// slots (N contiguous).  The two views overlap in one quarter that cannot be
+// shared, because one descriptor serves both blocks: 17/18 of the tile is
+// copied to each block (the second time from L2).
+//
+// The copies are gathers of four rows of 64 values by slot number; a slot that
+// is not seen gets a row outside the cache, which copies as zeros, so what it
+// holds never meets the sums.
+//
+// Work is cut in equal runs of tiles, through the rows' ends: the host does not
+// know the lengths.  A run's first and last row may be shared with the pairs
+// before and after; those write fp32 sums to the workspace and a second kernel
+// joins them, in the order of the slots (no atomics: equal calls give equal
+// bits).
+//
+// Warps of each block: 0-3 softmax and results (thread t: row t & 63, slots 64
+// (t >> 6).. of the tile, values 256 (t >> 6).. of the sums), 4 products (first
+// block only), 5 copies of slots for the first product, 6 for the second, 7
+// queries.
 #include <cuda_runtime.h>
 
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 
 #include "attend_internal.h"
-#include "attend_simple.cuh"
+#include "tc.cuh"
+#include "tensor_map.h"
 
 namespace topkidx {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(kSimpleWarps * 32) latent_kernel(const LatentParams p) {
-    const int64_t m = blockIdx.x;
-    const int h = static_cast<int>(m % p.heads), i = static_cast<int>(m / p.heads % p.queries);
-    const int64_t b = m / p.heads / p.queries;
-    const T* q = static_cast<const T*>(p.q) + b * p.q_row_stride + i * p.q_query_stride + h * p.q_head_stride;
-    int n = p.max_len;
-    if (p.seq_lens) n = min(max(p.seq_lens[b], 0), n);
-    n = max(n - (p.queries - 1 - i), 0);
-    const auto slot_of = [&](int j) -> int32_t {
-        if (p.indices) return p.indices[b * p.indices_stride + j];
-        const int64_t s = (static_cast<int64_t>(p.table[b * p.table_stride + (j >> p.log2_page)]) << p.log2_page) +
-                          (j & ((1 << p.log2_page) - 1));
-        return s >= 0 && s < p.num_slots ? static_cast<int32_t>(s) : -1;
-    };
-    const T* row = nullptr;
-    simple_attend<T, kWidth, kLatent>(
-        n, p.scale, [&](int d) { return to_float(q[d]); },
-        [&](int j) {
-            const int32_t s = slot_of(j);
-            row = static_cast<const T*>(p.cache) + static_cast<int64_t>(s) * p.slot_stride;
-            return s >= 0 && s < p.num_slots;
-        },
-        [&](int, int d) { return to_float(row[d]); }, [&](int, int d) { return to_float(row[d]); },
-        static_cast<T*>(p.out) + m * kLatent, p.lse ? p.lse + m : nullptr);
+constexpr int kRows = 128;                  // (query, head) rows of a pair
+constexpr int kTile = 128;                  // slots a step
+constexpr int kHalf = 64;
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 80;
+constexpr int kKeyPiece = kHalf * 128;      // 64 slots of 64 values
+constexpr int kValuePiece = kTile * 128;    // 128 slots of 64 values
+constexpr int kPieces = kWidth / 64;        // 9
+constexpr int kKeyGroups = 3;               // pieces of keys wait and are freed three at a time
+constexpr int kQueryBytes = kPieces * kKeyPiece;
+constexpr int kKeyBytes = kPieces * kKeyPiece;
+constexpr int kValueBytes = 4 * kValuePiece;
+constexpr int kWeightBytes = 2 * kKeyPiece;
+constexpr uint32_t kColumns = 512;
+constexpr uint32_t kScore = 256;            // column of the two score tiles; the sums have 0..255
+constexpr float kLag = 8.f;
+
+struct Shared {
+    uint64_t query_full, query_empty;
+    uint64_t key_full[kKeyGroups], key_empty[kKeyGroups];
+    uint64_t value_full[2], value_empty[2];
+    uint64_t score[2], weight, sum, end;
+    uint64_t mask_full[4];
+    uint32_t mask[4][4];
+    float exchange[2][kRows];
+    uint32_t tmem, gave_up;
+    int64_t begin, total;  // first tile of this pair's run, tiles of all runs
+    int32_t row, tile;     // where the run begins: row of the batch, tile in its group rows
+    int64_t scan[kThreads / 32];
+};
+constexpr int kSmem = kQueryBytes + kKeyBytes + kValueBytes + kWeightBytes + 1024 + 2048;
+static_assert(sizeof(Shared) <= 2048, "barriers fit");
+static_assert(kSmem <= 232448, "shared memory of a block");
+
+struct LatentMaps {
+    CUtensorMap q, cache;
+};
+
+__device__ __forceinline__ int length_of(const LatentParams& p, int b) {
+    return p.seq_lens ? min(max(p.seq_lens[b], 0), p.max_len) : p.max_len;
+}
+// Tiles of one group of 128 rows; an empty row has one, all of it hidden.
+__device__ __forceinline__ int tiles_of(int length) { return max((length + kTile - 1) / kTile, 1); }
+__device__ __forceinline__ int groups_of(const LatentParams& p) { return (p.queries * p.heads + kRows - 1) / kRows; }
+
+// Run of pair i of n: [total i / n, total (i + 1) / n).
+__device__ __forceinline__ int64_t run_start(int64_t total, int i, int n) { return total * i / n; }
+
+// All threads of a block: the tiles of the whole batch, and the row of the
+// batch in which tile `run_start(total, pair, pairs)` lies, with the tile's
+// number from that row's first.
+__device__ void locate(const LatentParams& p, int pair, int pairs, int64_t* scan, int64_t* total_out, int64_t* begin_out,
+                       int32_t* row_out, int32_t* tile_out) {
+    const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int groups = groups_of(p);
+    if (!p.seq_lens) {
+        const int64_t each = static_cast<int64_t>(tiles_of(p.max_len)) * groups;
+        if (tid == 0) {
+            const int64_t total = each * p.batch, begin = run_start(total, pair, pairs);
+            *total_out = total;
+            *begin_out = begin;
+            *row_out = static_cast<int32_t>(begin / each);
+            *tile_out = static_cast<int32_t>(begin % each);
+        }
+        __syncthreads();
+        return;
+    }
+    const int per = (p.batch + threads - 1) / threads;
+    const int from = min(tid * per, p.batch), to = min(from + per, p.batch);
+    int64_t mine = 0;
+    for (int b = from; b < to; ++b) mine += static_cast<int64_t>(tiles_of(length_of(p, b))) * groups;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < threads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    before += upto - mine;
+    const int64_t begin = run_start(total, pair, pairs);
+    if (begin >= before && begin < before + mine) {
+        int64_t at = before;
+        int b = from;
+        while (true) {
+            const int64_t n = static_cast<int64_t>(tiles_of(length_of(p, b))) * groups;
+            if (begin < at + n) break;
+            at += n;
+            ++b;
+        }
+        *total_out = total;
+        *begin_out = begin;
+        *row_out = b;
+        *tile_out = static_cast<int32_t>(begin - at);
+    }
+    __syncthreads();
+}
+
+// A run's pieces: tiles [first, last) of one group of 128 rows.
+struct Segment {
+    int row, group, first, last, tiles, length;
+};
+struct Walk {
+    const LatentParams& p;
+    int64_t left;
+    int row, group, first, groups;
+
+    __device__ Walk(const LatentParams& p, const Shared& sh, int pair, int pairs)
+        : p(p), left(run_start(sh.total, pair + 1, pairs) - sh.begin), row(sh.row), groups(groups_of(p)) {
+        const int tiles = tiles_of(length_of(p, min(row, p.batch - 1)));
+        group = sh.tile / tiles;
+        first = sh.tile % tiles;
+    }
+    __device__ bool next(Segment& s) {
+        if (left <= 0) return false;
+        s.row = row;
+        s.group = group;
+        s.length = length_of(p, row);
+        s.tiles = tiles_of(s.length);
+        s.first = first;
+        s.last = static_cast<int>(min(static_cast<int64_t>(s.tiles), first + left));
+        left -= s.last - s.first;
+        first = 0;
+        if (++group == groups) {
+            group = 0;
+            ++row;
+        }
+        return true;
+    }
+};
+
+// The slots of four neighbouring positions, num_slots (outside the cache)
+// where there is none.
+__device__ __forceinline__ int4 slots_of(const LatentParams& p, int row, int length, int64_t at) {
+    int s[4];
+    if (p.indices) {
+        const int32_t* from = p.indices + static_cast<int64_t>(row) * p.indices_stride;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = at + i < length ? from[at + i] : -1;
+    } else {
+        const int32_t* from = p.table + static_cast<int64_t>(row) * p.table_stride;
+        const int mask = (1 << p.log2_page) - 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = -1;
+            if (at + i < length) {
+                const int pos = static_cast<int>(at) + i;
+                const int64_t slot = (static_cast<int64_t>(from[pos >> p.log2_page]) << p.log2_page) + (pos & mask);
+                if (slot >= 0 && slot < p.num_slots) s[i] = static_cast<int>(slot);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (s[i] < 0 || s[i] >= p.num_slots) s[i] = p.num_slots;
+    return make_int4(s[0], s[1], s[2], s[3]);
+}
+
+// Partial sums in the workspace, two places a pair: 0 for a row begun by an
+// earlier pair, 1 for a row begun by this pair and finished by a later one.
+__device__ __forceinline__ float* part_sums(const LatentParams& p, int rows, int place) {
+    return static_cast<float*>(p.workspace) + static_cast<int64_t>(place) * rows * (kLatent + 2);
+}
+
+template <bool kBf16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    latent_kernel(const LatentParams p, const __grid_constant__ LatentMaps maps, uint32_t* flags, float scale_log2,
+                  bool negate, bool whole_rows) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t queries = base, keys = queries + kQueryBytes, values = keys + kKeyBytes,
+                   weights = values + kValueBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(raw + (weights + kWeightBytes - ptx::smem_addr(raw)));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(ptx::cluster_ctarank());
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        sh.gave_up = 0;
+        ptx::mbar_init(&sh.query_full, 1);
+        ptx::mbar_init(&sh.query_empty, 1);
+        for (int i = 0; i < kKeyGroups; ++i) {
+            ptx::mbar_init(&sh.key_full[i], 1);
+            ptx::mbar_init(&sh.key_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.value_full[i], 1);
+            ptx::mbar_init(&sh.value_empty[i], 1);
+            ptx::mbar_init(&sh.score[i], 1);
+        }
+        ptx::mbar_init(&sh.weight, 8);
+        ptx::mbar_init(&sh.sum, 1);
+        ptx::mbar_init(&sh.end, 1);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh.mask_full[i], 1);
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == 4) tc::alloc<2>(ptx::smem_addr(&sh.tmem), kColumns);
+    locate(p, pair, pairs, sh.scan, &sh.total, &sh.begin, &sh.row, &sh.tile);
+    tc::fence_before();
+    ptx::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem;
+    const tc::Waits wait{&sh.gave_up};
+    Walk walk(p, sh, pair, pairs);
+    Segment s;
+
+    if (warp == 7) {
+        if (lane == 0) {
+            const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
+            for (int n = 0; walk.next(s); ++n) {
+                if (n > 0) wait(&sh.query_empty, (n - 1) & 1);
+                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full, 2 * kQueryBytes);
+                const int m = s.group * kRows + rank * kHalf;
+                for (int c = 0; c < kPieces; ++c) {
+                    if (whole_rows) {
+                        tc::load_4d_pair(queries + c * kKeyPiece, &maps.q, 64 * c, m, 0, s.row, full);
+                    } else {
+                        for (int i = 0; i < kHalf; ++i)
+                            tc::load_4d_pair(queries + c * kKeyPiece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
+                                             (m + i) / p.heads, s.row, full);
+                    }
+                }
+                if (sh.gave_up) {
+                    if (rank == 0) tc::Waits::drain(&sh.query_full, n & 1);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 5) {
+        // Slots 64 rank.. of each tile, all values: 16 gathers a piece, lane
+        // i those of slots 4 (i % 16)...
+        uint32_t full[kKeyGroups];
+        for (int g = 0; g < kKeyGroups; ++g) full[g] = ptx::map_rank(ptx::smem_addr(&sh.key_full[g]), 0);
+        const int at = rank * kHalf + 4 * (lane & 15);
+        int n = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        int4 slots = more ? slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at) : int4{};
+        while (more && !wait.over()) {
+            const int4 now = slots;
+            // The next tile's slots are fetched while this one's copies wait.
+            if (++tile == s.last) {
+                more = walk.next(s);
+                tile = s.first;
+            }
+            if (more) slots = slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at);
+            for (int g = 0; g < kKeyGroups; ++g) {
+                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
+                if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_full[g], 2 * 3 * kKeyPiece);
+                for (int i = lane >> 4; i < 3; i += 2)
+                    tc::gather4_pair(keys + (3 * g + i) * kKeyPiece + (lane & 15) * 512, &maps.cache, 64 * (3 * g + i), now,
+                                     full[g]);
+            }
+            ++n;
+        }
+        __syncwarp();
+        if (sh.gave_up && rank == 0 && n > 0)
+            for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_full[g], (n - 1) & 1);
+    } else if (warp == 6) {
+        // All slots of each tile, values 256 rank..: 32 gathers a piece.
+        uint32_t full[2];
+        for (int g = 0; g < 2; ++g) full[g] = ptx::map_rank(ptx::smem_addr(&sh.value_full[g]), 0);
+        int n = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        int4 slots = more ? slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 4 * lane) : int4{};
+        while (more && !wait.over()) {
+            const int4 now = slots;
+            if (++tile == s.last) {
+                more = walk.next(s);
+                tile = s.first;
+            }
+            if (more) slots = slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 4 * lane);
+            // One bit a slot that is seen.  Place n % 4 was last read for tile
+            // n - 4, whose second product the copies of tile n - 2 waited for.
+            uint32_t bits = (now.x < p.num_slots ? 1u : 0u) | (now.y < p.num_slots ? 2u : 0u) |
+                            (now.z < p.num_slots ? 4u : 0u) | (now.w < p.num_slots ? 8u : 0u);
+            bits <<= 4 * (lane & 7);
+            bits |= __shfl_xor_sync(~0u, bits, 1);
+            bits |= __shfl_xor_sync(~0u, bits, 2);
+            bits |= __shfl_xor_sync(~0u, bits, 4);
+            if ((lane & 7) == 0) sh.mask[n & 3][lane >> 3] = bits;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.mask_full[n & 3]);
+            for (int g = 0; g < 2; ++g) {
+                if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
+                if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_full[g], 2 * 2 * kValuePiece);
+                for (int i = 0; i < 2; ++i)
+                    tc::gather4_pair(values + (2 * g + i) * kValuePiece + lane * 512, &maps.cache,
+                                     256 * rank + 64 * (2 * g + i), now, full[g]);
+            }
+            ++n;
+        }
+        __syncwarp();
+        if (sh.gave_up && rank == 0 && n > 0)
+            for (int g = 0; g < 2; ++g) tc::Waits::drain(&sh.value_full[g], (n - 1) & 1);
+    } else if (warp == 4) {
+        if (rank == 0 && lane == 0) {
+            const uint32_t score_instr = tc::instruction(kBf16, kRows, kTile, negate, false);
+            const uint32_t sum_instr = tc::instruction(kBf16, kRows, 256, false, true);
+            const auto sums = [&](int n, bool add) {  // second product of tile n
+                wait(&sh.weight, n & 1);
+                tc::fence_after();
+                for (int g = 0; g < 2; ++g) {
+                    wait(&sh.value_full[g], n & 1);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t a = tc::operand(weights + (k >> 2) * kKeyPiece) + 2 * (k & 3);
+                        const uint64_t b = tc::operand(values + 2 * g * kValuePiece, kValuePiece) + 128 * k;
+                        tc::mma<2>(tmem + 128 * g, a, b, sum_instr, add || k > 0);
+                    }
+                    tc::commit_pair(&sh.value_empty[g]);
+                }
+                tc::commit_pair(&sh.sum);
+            };
+            int n = 0;
+            bool add = false;  // whether the sums of the tile before are added to
+            for (int segment = 0; walk.next(s); ++segment) {
+                for (int tile = s.first; tile < s.last; ++tile, ++n) {
+                    if (tile == s.first) {
+                        // The queries' place is free before the last sums of
+                        // the segment before are due: those go first.
+                        if (n > 0) sums(n - 1, add);
+                        wait(&sh.query_full, segment & 1);
+                    }
+                    for (int g = 0; g < kKeyGroups; ++g) {
+                        wait(&sh.key_full[g], n & 1);
+#pragma unroll
+                        for (int k = 0; k < 12; ++k) {
+                            const uint32_t piece = (3 * g + (k >> 2)) * kKeyPiece;
+                            tc::mma<2>(tmem + kScore + kHalf * (n & 1), tc::operand(queries + piece) + 2 * (k & 3),
+                                       tc::operand(keys + piece) + 2 * (k & 3), score_instr, (g | k) != 0);
+                        }
+                        tc::commit_pair(&sh.key_empty[g]);
+                    }
+                    tc::commit_pair(&sh.score[n & 1]);
+                    if (tile == s.last - 1) tc::commit_pair(&sh.query_empty);
+                    if (tile > s.first) sums(n - 1, add);
+                    add = tile > s.first;
+                }
+            }
+            if (n > 0) sums(n - 1, add);
+            tc::commit<2>(&sh.end);
+            tc::Waits::drain(&sh.end, 0);
+        }
+    } else {
+        const int r = threadIdx.x & 63, half = threadIdx.x >> 6;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
+        const uint32_t weight_full = ptx::map_rank(ptx::smem_addr(&sh.weight), 0);
+        const uint32_t weight_row = weights + half * kKeyPiece + r * 128;
+        const int all = p.queries * p.heads, part_rows = min(all, kRows);
+        int n = 0;
+        while (walk.next(s)) {
+            const int m_row = s.group * kRows + rank * kHalf + r;
+            const int limit = s.length - (p.queries - 1 - min(m_row / p.heads, p.queries - 1));
+            float m = -INFINITY, l = 0.f;
+            for (int tile = s.first; tile < s.last; ++tile, ++n) {
+                wait.warp(&sh.mask_full[n & 3], (n >> 2) & 1);
+                wait.warp(&sh.score[n & 1], (n >> 1) & 1);
+                tc::fence_after();
+                uint32_t raw_s[kHalf];
+                tc::load32(lanes + kScore + kHalf * (n & 1), raw_s);
+                tc::load32(lanes + kScore + kHalf * (n & 1) + 32, raw_s + 32);
+                uint64_t seen = *reinterpret_cast<const uint64_t*>(&sh.mask[n & 3][2 * half]);
+                const int left = limit - tile * kTile - half * kHalf;  // of this thread's slots
+                if (left < kHalf) seen &= left <= 0 ? 0ull : (~0ull >> (kHalf - left));
+                tc::wait_load();
+                float* x = reinterpret_cast<float*>(raw_s);
+                if (__any_sync(~0u, seen != ~0ull)) {
+                    const uint32_t lo = static_cast<uint32_t>(seen), hi = static_cast<uint32_t>(seen >> 32);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (!((lo >> i) & 1)) x[i] = -INFINITY;
+                        if (!((hi >> i) & 1)) x[32 + i] = -INFINITY;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+                float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale_log2;
+                // The other half of the slots is with thread t ^ 64.
+                sh.exchange[n & 1][threadIdx.x] = tile_top;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                tile_top = fmaxf(tile_top, sh.exchange[n & 1][threadIdx.x ^ 64]);
+                const bool raise = tile_top > m + kLag || (m == -INFINITY && tile_top > m);
+                const float next = raise ? tile_top : m;
+                const float by = raise ? tc::exp2_approx(m - next) : 1.f;
+                m = next;
+                l *= by;
+                const float shift = m == -INFINITY ? 0.f : -m;
+                uint32_t w[32];
+                float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float a = tc::exp2_approx(fmaf(x[2 * i], scale_log2, shift));
+                    const float b = tc::exp2_approx(fmaf(x[2 * i + 1], scale_log2, shift));
+                    add[(2 * i) & 3] += a;
+                    add[(2 * i + 1) & 3] += b;
+                    w[i] = tc::pack<kBf16>(a, b);
+                }
+                l += (add[0] + add[1]) + (add[2] + add[3]);
+                // The weights' place and the sums are free once the second
+                // product of the tile before is done.
+                if (n > 0) {
+                    wait.warp(&sh.sum, (n - 1) & 1);
+                    tc::fence_after();
+                }
+                if (tile > s.first && __any_sync(~0u, raise)) {
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t o[32];
+                        tc::load32(lanes + 32 * c, o);
+                        tc::wait_load();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                        tc::store32(lanes + 32 * c, o);
+                    }
+                    tc::wait_store();
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    ptx::sts_u4(weight_row + ((i ^ (r & 7)) << 4),
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+                tc::fence_async();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::arrive_cluster(weight_full);
+            }
+            // The sums of both halves, then the values 256 half.. of the row.
+            wait.warp(&sh.sum, (n - 1) & 1);
+            tc::fence_after();
+            sh.exchange[n & 1][threadIdx.x] = l;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            l += sh.exchange[n & 1][threadIdx.x ^ 64];
+            // exchange[n & 1] is written again by the next tile n.
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const bool whole = s.first == 0 && s.last == s.tiles;
+            const int64_t at = static_cast<int64_t>(s.row) * all + m_row;
+            float* part = nullptr;
+            if (!whole) {
+                part = part_sums(p, part_rows, 2 * pair + (s.first == 0 ? 1 : 0));
+                if (half == 0 && m_row < all) {
+                    float* stats = part + static_cast<int64_t>(part_rows) * kLatent + 2 * (m_row - s.group * kRows);
+                    stats[0] = m;
+                    stats[1] = l;
+                }
+                part += static_cast<int64_t>(m_row - s.group * kRows) * kLatent + 256 * half;
+            }
+            const float by = l == 0.f ? 0.f : 1.f / l;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kLatent + 256 * half);
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t o[32];
+                tc::load32(lanes + 32 * c, o);
+                tc::wait_load();
+                if (m_row < all && whole) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = __uint_as_float(o[8 * i + 2 * k]) * by,
+                                        b = __uint_as_float(o[8 * i + 2 * k + 1]) * by;
+                            w[k] = l == 0.f ? 0u : tc::pack<kBf16>(a, b);
+                        }
+                        out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (m_row < all) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(part + 32 * c)[i] =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+                __syncwarp();
+            }
+            if (whole && p.lse && half == 0 && m_row < all)
+                p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            tc::fence_before();
+        }
+    }
+    __syncwarp();
+    // Neither block ends, nor gives its tensor memory back, while products of
+    // the pair or copies may still use it.
+    ptx::cluster_sync();
+    if (warp == 4) {
+        tc::fence_after();
+        tc::dealloc<2>(tmem, kColumns);
+    }
+    if (threadIdx.x == 0 && sh.gave_up) atomicOr(flags, TOPK_FLAG_TIMEOUT);
+}
+
+// Joins the rows that several pairs shared: block (i, j) the first four..
+// values' share j of the row in which the run of pair i + 1 begins, if that
+// run is the first to begin inside it.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 4;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentParams p, int pairs) {
+    __shared__ int64_t scan[kJoinThreads / 32], total, begin;
+    __shared__ int32_t row, tile;
+    const int pair = static_cast<int>(blockIdx.x) + 1;
+    locate(p, pair, pairs, scan, &total, &begin, &row, &tile);
+    const int tiles = tiles_of(length_of(p, row));
+    const int group = tile / tiles, first = tile % tiles;
+    const int64_t start = begin - first, end = start + tiles;  // of the group's tiles
+    if (first == 0 || run_start(total, pair - 1, pairs) > start) return;
+    const int all = p.queries * p.heads, part_rows = min(all, kRows);
+    // Pairs pair - 1 .. last hold a part each, those with an empty run none.
+    int last = pair;
+    while (last + 1 < pairs && run_start(total, last + 1, pairs) < end) ++last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = static_cast<int>(blockIdx.y) * kJoinRows + warp;
+    const int m_row = group * kRows + r;
+    if (r >= part_rows || m_row >= all) return;
+    const auto place = [&](int i) { return 2 * i + (i == pair - 1 ? 1 : 0); };
+    float m = -INFINITY, l = 0.f, o[kLatent / 32] = {};
+    const auto none = [&](int i) { return run_start(total, i, pairs) == run_start(total, i + 1, pairs); };
+    for (int i = pair - 1; i <= last; ++i) {
+        if (none(i)) continue;
+        m = fmaxf(m, part_sums(p, part_rows, place(i))[static_cast<int64_t>(part_rows) * kLatent + 2 * r]);
+    }
+    for (int i = pair - 1; i <= last; ++i) {
+        if (none(i)) continue;
+        const float* part = part_sums(p, part_rows, place(i));
+        const float* stats = part + static_cast<int64_t>(part_rows) * kLatent + 2 * r;
+        if (stats[1] == 0.f) continue;
+        const float by = exp2f(stats[0] - (m == -INFINITY ? 0.f : m));
+        l += stats[1] * by;
+        const float4* from = reinterpret_cast<const float4*>(part + static_cast<int64_t>(r) * kLatent);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 x = from[32 * c + lane];
+            o[4 * c] += x.x * by;
+            o[4 * c + 1] += x.y * by;
+            o[4 * c + 2] += x.z * by;
+            o[4 * c + 3] += x.w * by;
+        }
+    }
+    const float by = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = static_cast<int64_t>(row) * all + m_row;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kLatent);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        out[32 * c + lane] = make_uint2(tc::pack<kBf16>(o[4 * c] * by, o[4 * c + 1] * by),
+                                        tc::pack<kBf16>(o[4 * c + 2] * by, o[4 * c + 3] * by));
+    if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+int pairs_of_device() {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int n = sms / 2;
+    return n < 1 ? 1 : n > kMaxPairs ? kMaxPairs : n;
 }
 
 }  // namespace
 
-size_t latent_workspace_bytes(int32_t, int32_t, int32_t) { return 16; }
+size_t latent_workspace_bytes(int32_t, int32_t queries, int32_t heads) {
+    const int64_t all = static_cast<int64_t>(queries) * heads;
+    return static_cast<size_t>(2 * kMaxPairs) * static_cast<size_t>(all < kRows ? all : kRows) * (kLatent + 2) *
+           sizeof(float);
+}
 
-topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, cudaStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.batch) * p.queries * p.heads);
-    if (dtype == TOPK_BF16)
-        latent_kernel<__nv_bfloat16><<<blocks, kSimpleWarps * 32, 0, stream>>>(p);
-    else
-        latent_kernel<__half><<<blocks, kSimpleWarps * 32, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "latent attention launch");
+topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream) {
+    const bool bf16 = dtype == TOPK_BF16;
+    LatentMaps maps;
+    // Query rows: one dimension of (query, head) where those have one stride,
+    // copied 64 rows at a time; else one row at a time.
+    const bool whole_rows = p.queries == 1 || p.heads == 1 || p.q_query_stride == p.heads * p.q_head_stride;
+    const int64_t any = 2 * kWidth;  // stride of a dimension of one entry
+    const int64_t rows = whole_rows ? static_cast<int64_t>(p.queries) * p.heads : p.heads;
+    const int64_t row_step = whole_rows && p.heads == 1 ? p.q_query_stride : p.q_head_stride;
+    const int64_t q_dims[4] = {kWidth, rows, whole_rows ? 1 : p.queries, p.batch};
+    const int64_t q_steps[3] = {rows > 1 ? 2 * row_step : any, whole_rows ? any : 2 * p.q_query_stride,
+                                p.batch > 1 ? 2 * p.q_row_stride : any};
+    CUresult r = encode_map(&maps.q, bf16, p.q, 4, q_dims, q_steps, 1, whole_rows ? kHalf : 1);
+    const int64_t c_dims[2] = {kWidth, p.num_slots}, c_steps[1] = {2 * p.slot_stride};
+    if (r == CUDA_SUCCESS) r = encode_map(&maps.cache, bf16, p.cache, 2, c_dims, c_steps, 1, 1);
+    if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "latent attention tensor map");
+
+    const auto kernel = bf16 ? latent_kernel<true> : latent_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return api_cuda_fail(e, "latent attention shared memory");
+    const int64_t groups = (static_cast<int64_t>(p.queries) * p.heads + kRows - 1) / kRows;
+    const int64_t tiles = p.batch * groups * (p.max_len > kTile ? (p.max_len + int64_t{kTile} - 1) / kTile : 1);
+    const int device = pairs_of_device();
+    const int pairs = tiles < device ? static_cast<int>(tiles) : device;
+    const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
+    kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps, flags, scale_log2, p.scale < 0.f, whole_rows);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
+    if (pairs > 1) {
+        const int64_t all = static_cast<int64_t>(p.queries) * p.heads;
+        const int part_rows = static_cast<int>(all < kRows ? all : kRows);
+        const dim3 grid(static_cast<unsigned>(pairs - 1), static_cast<unsigned>((part_rows + kJoinRows - 1) / kJoinRows));
+        (bf16 ? join_kernel<true> : join_kernel<false>)<<<grid, kJoinThreads, 0, stream>>>(p, pairs);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return api_cuda_fail(e, "latent attention join launch");
+    }
+    return TOPK_OK;
 }
 
 }  // namespace topkidx

@@ -1,56 +1,407 @@
-// attend_prompt.cu -- expanded latent attention for prompts: one block per
-// query head.
+// attend_prompt.cu -- expanded latent attention for prompts (ragged, causal or
+// not) on the tensor cores.
+//
+// Mathematics: o = sum_j p_j v_j, p = softmax(scale (q_n.k_n + q_r.k_r)), with a
+// running maximum m and sum l per query: a tile of keys adds
+// 2^(x_j - m) v_j, x = scale log2(e) s, and when a tile's maximum passes m by
+// more than 8 (a factor of 256 that fp32 sums and two-byte weights hold with
+// room) the sums so far are multiplied by 2^(m - m').  The rotary part is
+// one more 64-wide chunk of the first product, read once for all heads'
+// blocks, so keys are never put together in memory.
+//
+// A block has two tiles of 128 queries of one head and walks the keys 128 at a
+// time; the tiles share each load of keys and values.  Its tensor memory is
+// full: two score tiles (128 columns each, the weights go back into their
+// first 64 as two-byte pairs and are the second product's A operand from
+// there) and two sums (128 each).  While one tile's softmax runs, the tensor
+// cores work on the other tile.  Shared memory: 96 KB of queries, and a ring of
+// eight 16 KB pieces (three of keys and two of values per step).
+//
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one query a thread), 8 products,
+// 9 copies.
 #include <cuda_runtime.h>
 
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 
 #include "attend_internal.h"
-#include "attend_simple.cuh"
+#include "tc.cuh"
+#include "tensor_map.h"
 
 namespace topkidx {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(kSimpleWarps * 32) prompt_kernel(const PromptParams p) {
-    const int64_t m = blockIdx.x;
-    const int h = static_cast<int>(m % p.heads);
-    const int64_t t = m / p.heads;
-    int b = -1, q0 = 0, q1 = 0;
-    for (int r = 0; r < p.batch; ++r) {
-        const int lo = min(max(p.cu_q[r], 0), p.total_q), hi = min(max(p.cu_q[r + 1], lo), p.total_q);
-        if (t >= lo && t < hi) {
-            b = r;
-            q0 = lo;
-            q1 = hi;
-            break;
+constexpr int kTile = 128;                   // queries a tile, keys a step
+constexpr int kBlockRows = 2 * kTile;
+constexpr int kPiece = 16384;                // 128 rows of 128 bytes
+constexpr int kRing = 8;
+constexpr int kKeyPieces = 3, kStepPieces = 5;
+constexpr int kThreads = 320;
+constexpr uint32_t kColumns = 512;
+constexpr float kLag = 8.f;
+
+struct PromptMaps {
+    CUtensorMap q, k_nope, k_rope, v;
+};
+
+struct Barriers {
+    uint64_t full[kRing], empty[kRing];
+    uint64_t query[2];
+    uint64_t score[2], weight[2], sum[2];
+    uint64_t end;
+    uint32_t tmem;
+    uint32_t gave_up;
+    int32_t block;  // of the request's
+    int4 range;     // its first query, the end of its queries, the same of its keys
+};
+constexpr int kSmem = 6 * kPiece + kRing * kPiece + static_cast<int>(sizeof(Barriers)) + 1024;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps, uint32_t* flags, float scale_log2,
+                  bool negate) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t queries = base, ring = base + 6 * kPiece;
+    Barriers& bar = *reinterpret_cast<Barriers*>(raw + (base - ptx::smem_addr(raw)) + (6 + kRing) * kPiece);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.heads));
+    const int index = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.heads));
+
+    // The request that this block's queries are in: blocks are numbered
+    // through the requests, ceil(queries / 256) each.  Offsets below an
+    // earlier one count as that one, so requests never overlap.
+    if (warp == 0) {
+        int before = 0, found = -1, block = 0;
+        int q_upto = min(max(p.cu_q[0], 0), p.total_q), k_upto = min(max(p.cu_k[0], 0), p.total_k);
+        int4 range = {};
+        for (int r0 = 0; r0 < p.batch && found < 0; r0 += 32) {
+            const int r = min(r0 + lane, p.batch - 1);
+            int q_end = max(min(p.cu_q[r + 1], p.total_q), q_upto), k_end = max(min(p.cu_k[r + 1], p.total_k), k_upto);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(~0u, q_end, d), y = __shfl_up_sync(~0u, k_end, d);
+                if (lane >= d) {
+                    q_end = max(q_end, x);
+                    k_end = max(k_end, y);
+                }
+            }
+            int q_start = __shfl_up_sync(~0u, q_end, 1), k_start = __shfl_up_sync(~0u, k_end, 1);
+            if (lane == 0) {
+                q_start = q_upto;
+                k_start = k_upto;
+            }
+            int upto = (q_end - q_start + kBlockRows - 1) / kBlockRows;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(~0u, upto, d);
+                if (lane >= d) upto += x;
+            }
+            const unsigned past = __ballot_sync(~0u, before + upto > index);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                found = r0 + at;
+                // Blocks of a request in falling order: with causal masks the longest first.
+                const int mine = (q_end - q_start + kBlockRows - 1) / kBlockRows;
+                block = before + __shfl_sync(~0u, upto, at) - __shfl_sync(~0u, mine, at);
+                block = __shfl_sync(~0u, mine, at) - 1 - (index - block);
+                range.x = __shfl_sync(~0u, q_start, at);
+                range.y = __shfl_sync(~0u, q_end, at);
+                range.z = __shfl_sync(~0u, k_start, at);
+                range.w = __shfl_sync(~0u, k_end, at);
+            }
+            before += __shfl_sync(~0u, upto, 31);
+            q_upto = __shfl_sync(~0u, q_end, 31);
+            k_upto = __shfl_sync(~0u, k_end, 31);
+        }
+        if (lane == 0) {
+            bar.range = range;
+            bar.block = found < 0 ? -1 : block;
+            bar.gave_up = 0;
+            for (int i = 0; i < kRing; ++i) {
+                ptx::mbar_init(&bar.full[i], 1);
+                ptx::mbar_init(&bar.empty[i], 1);
+            }
+            for (int t = 0; t < 2; ++t) {
+                ptx::mbar_init(&bar.query[t], 1);
+                ptx::mbar_init(&bar.score[t], 1);
+                ptx::mbar_init(&bar.weight[t], 4);
+                ptx::mbar_init(&bar.sum[t], 1);
+            }
+            ptx::mbar_init(&bar.end, 1);
+            ptx::fence_mbarrier_init();
         }
     }
-    if (b < 0) return;
-    const int k0 = min(max(p.cu_k[b], 0), p.total_k), k1 = min(max(p.cu_k[b + 1], k0), p.total_k);
-    int n = k1 - k0;
-    if (p.causal) n = max(n - (q1 - 1 - static_cast<int>(t)), 0);
-    const T* q = static_cast<const T*>(p.q) + t * p.q_token_stride + h * p.q_head_stride;
-    const T* kn = static_cast<const T*>(p.k_nope) + k0 * p.k_token_stride + h * p.k_head_stride;
-    const T* kr = static_cast<const T*>(p.k_rope) + k0 * p.k_rope_stride;
-    const T* v = static_cast<const T*>(p.v) + k0 * p.v_token_stride + h * p.v_head_stride;
-    simple_attend<T, kNope + kRope, kValue>(
-        n, p.scale, [&](int d) { return to_float(q[d]); }, [&](int) { return true; },
-        [&](int j, int d) {
-            return to_float(d < kNope ? kn[j * p.k_token_stride + d] : kr[j * p.k_rope_stride + d - kNope]);
-        },
-        [&](int j, int d) { return to_float(v[j * p.v_token_stride + d]); }, static_cast<T*>(p.out) + m * kValue,
-        p.lse ? p.lse + m : nullptr);
+    __syncthreads();
+    if (bar.block < 0) return;  // more blocks than the requests have
+
+    if (warp == 8) tc::alloc<1>(ptx::smem_addr(&bar.tmem), kColumns);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = bar.tmem;
+    const tc::Waits wait{&bar.gave_up};
+
+    const int q0 = bar.range.x, q1 = bar.range.y, k0 = bar.range.z, k1 = bar.range.w;
+    const int keys = k1 - k0;
+    const int first = q0 + bar.block * kBlockRows;  // first query of tile 0
+    // Keys seen by query i (of the whole tensor): all, or all but those after it.
+    const auto seen = [&](int i) { return p.causal ? max(keys - (q1 - 1 - i), 0) : keys; };
+    int steps[2];
+    for (int t = 0; t < 2; ++t) {
+        const int last = min(first + (t + 1) * kTile, q1) - 1;
+        steps[t] = last < first + t * kTile ? 0 : (seen(last) + kTile - 1) / kTile;
+    }
+    const int n = max(steps[0], steps[1]);
+
+    if (warp == 9) {
+        if (lane == 0) {
+            int issued = 0;
+            const auto take = [&](uint32_t bytes) {  // the next free piece of the ring
+                const int s = issued % kRing;
+                if (issued >= kRing) wait(&bar.empty[s], ((issued / kRing) - 1) & 1);
+                ptx::mbar_arrive_expect_tx(&bar.full[s], bytes);
+                ++issued;
+                return s;
+            };
+            const int q_head = p.q_head_stride ? head : 0, k_head = p.k_head_stride ? head : 0,
+                      v_head = p.v_head_stride ? head : 0;
+            const auto load_queries = [&](int t) {
+                ptx::mbar_arrive_expect_tx(&bar.query[t], 3 * kPiece);
+                for (int c = 0; c < 3; ++c)
+                    tc::load_3d(queries + (3 * t + c) * kPiece, &maps.q, 64 * c, q_head, first + t * kTile, &bar.query[t]);
+            };
+            if (steps[0]) load_queries(0);
+            for (int j = 0; j < n && !bar.gave_up; ++j) {
+                const int row = k0 + j * kTile;
+                for (int c = 0; c < 2; ++c) {
+                    const int s = take(kPiece);
+                    tc::load_3d(ring + s * kPiece, &maps.k_nope, 64 * c, k_head, row, &bar.full[s]);
+                }
+                const int s = take(kPiece);
+                tc::load_2d(ring + s * kPiece, &maps.k_rope, 0, row, &bar.full[s]);
+                if (j == 0 && steps[1]) load_queries(1);
+                for (int c = 0; c < 2; ++c) {  // 64 keys by 128 values
+                    const int s = take(kPiece);
+                    for (int d = 0; d < 2; ++d)
+                        tc::load_3d(ring + s * kPiece + d * (kPiece / 2), &maps.v, 64 * d, v_head, row + 64 * c,
+                                    &bar.full[s]);
+                }
+            }
+            if (bar.gave_up) {  // what is in flight lands before the block ends
+                for (int i = max(0, issued - kRing); i < issued; ++i)
+                    tc::Waits::drain(&bar.full[i % kRing], (i / kRing) & 1);
+                for (int t = 0; t < 2; ++t)
+                    if (steps[t]) tc::Waits::drain(&bar.query[t], 0);
+            }
+        }
+    } else if (warp == 8) {
+        const uint32_t score_instr = tc::instruction(kBf16, kTile, kTile, negate, false);
+        const uint32_t sum_instr = tc::instruction(kBf16, kTile, kValue, false, true);
+        const auto scores = [&](int t, int j) {
+            if (j == 0) wait.warp(&bar.query[t], 0);
+            for (int c = 0; c < kKeyPieces; ++c) {
+                const int i = j * kStepPieces + c;
+                wait.warp(&bar.full[i % kRing], (i / kRing) & 1);
+                if (lane == 0) {
+                    const uint64_t a = tc::operand(queries + (3 * t + c) * kPiece);
+                    const uint64_t b = tc::operand(ring + (i % kRing) * kPiece);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma<1>(tmem + t * kTile, a + 2 * k, b + 2 * k, score_instr, (c | k) != 0);
+                }
+            }
+            if (lane == 0) tc::commit<1>(&bar.score[t]);
+        };
+        const auto release = [&](int from, int count) {
+            if (lane == 0)
+                for (int i = from; i < from + count; ++i) tc::commit<1>(&bar.empty[i % kRing]);
+        };
+        for (int t = 0; t < 2; ++t)
+            if (steps[t]) scores(t, 0);
+        if (n) release(0, kKeyPieces);
+        for (int j = 0; j < n; ++j) {
+            const int vi = j * kStepPieces + kKeyPieces;
+            for (int c = 0; c < 2; ++c) wait.warp(&bar.full[(vi + c) % kRing], ((vi + c) / kRing) & 1);
+            const int left = keys - j * kTile;
+            if (left < kTile) {
+                // Rows past the request's keys belong to others or to nobody
+                // and may hold anything: a weight of zero would not hide a NaN.
+                for (int i = left * 16 + lane; i < kTile * 16; i += 32) {
+                    const int row = i >> 4, piece = (vi + (row >> 6)) % kRing;
+                    ptx::sts_u4(ring + piece * kPiece + ((i >> 3) & 1) * (kPiece / 2) + (row & 63) * 128 + (i & 7) * 16,
+                                make_uint4(0, 0, 0, 0));
+                }
+                tc::fence_async();
+                __syncwarp();
+            }
+            for (int t = 0; t < 2; ++t) {
+                if (j < steps[t]) {
+                    wait.warp(&bar.weight[t], j & 1);
+                    tc::fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint64_t b = tc::operand(ring + ((vi + (k >> 2)) % kRing) * kPiece, kPiece / 2);
+                            tc::mma_tmem(tmem + 256 + t * kValue, tmem + t * kTile + 8 * k, b + 128 * (k & 3), sum_instr,
+                                         j > 0 || k > 0);
+                        }
+                        tc::commit<1>(&bar.sum[t]);
+                    }
+                }
+                if (t == 1) release(vi, 2);
+                if (j + 1 < steps[t]) scores(t, j + 1);
+            }
+            if (j + 1 < n) release((j + 1) * kStepPieces, kKeyPieces);
+        }
+        if (lane == 0) {
+            tc::commit<1>(&bar.end);
+            tc::Waits::drain(&bar.end, 0);
+        }
+        __syncwarp();
+    } else {
+        const int t = warp >> 2, row = threadIdx.x & 127;
+        const int query = first + t * kTile + row;
+        const int limit = query < q1 ? seen(query) : 0;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const uint32_t score = lanes + t * kTile, sums = lanes + 256 + t * kValue;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < steps[t]; ++j) {
+            wait.warp(&bar.score[t], j & 1);
+            tc::fence_after();
+            uint32_t raw_s[kTile];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::load32(score + 32 * c, raw_s + 32 * c);
+            tc::wait_load();
+            float* s = reinterpret_cast<float*>(raw_s);
+            const int left = limit - j * kTile;
+            if (__any_sync(~0u, left < kTile)) {
+#pragma unroll
+                for (int i = 0; i < kTile; ++i)
+                    if (i >= left) s[i] = -INFINITY;
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
+            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale_log2;
+            const bool raise = tile_top > m + kLag || (m == -INFINITY && tile_top > m);
+            if (__any_sync(~0u, raise)) {
+                const float next = raise ? tile_top : m;
+                const float by = raise ? tc::exp2_approx(m - next) : 1.f;
+                m = next;
+                l *= by;
+                if (j > 0) {
+                    wait.warp(&bar.sum[t], (j - 1) & 1);
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tc::load32(sums + 32 * c, o);
+                        tc::wait_load();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                        tc::store32(sums + 32 * c, o);
+                    }
+                }
+            }
+            const float shift = m == -INFINITY ? 0.f : -m;
+            float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float a = tc::exp2_approx(fmaf(s[64 * c + 2 * i], scale_log2, shift));
+                    const float b = tc::exp2_approx(fmaf(s[64 * c + 2 * i + 1], scale_log2, shift));
+                    add[(2 * i) & 3] += a;
+                    add[(2 * i + 1) & 3] += b;
+                    w[i] = tc::pack<kBf16>(a, b);
+                }
+                tc::store32(score + 32 * c, w);
+            }
+            l += (add[0] + add[1]) + (add[2] + add[3]);
+            tc::wait_store();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bar.weight[t]);
+        }
+        if (steps[t]) {
+            wait.warp(&bar.sum[t], (steps[t] - 1) & 1);
+            tc::fence_after();
+        }
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = static_cast<int64_t>(query) * p.heads + head;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kValue);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            if (steps[t]) {
+                tc::load32(sums + 32 * c, o);
+                tc::wait_load();
+            }
+            if (query < q1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a = __uint_as_float(o[8 * i + 2 * k]) * by, b = __uint_as_float(o[8 * i + 2 * k + 1]) * by;
+                        w[k] = l == 0.f ? 0u : tc::pack<kBf16>(a, b);
+                    }
+                    out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();
+        }
+        if (p.lse && query < q1) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        tc::fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc::fence_after();
+        tc::dealloc<1>(tmem, kColumns);
+    }
+    if (threadIdx.x == 0 && bar.gave_up) atomicOr(flags, TOPK_FLAG_TIMEOUT);
 }
 
 }  // namespace
 
-topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, cudaStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.total_q) * p.heads);
-    if (dtype == TOPK_BF16)
-        prompt_kernel<__nv_bfloat16><<<blocks, kSimpleWarps * 32, 0, stream>>>(p);
-    else
-        prompt_kernel<__half><<<blocks, kSimpleWarps * 32, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream) {
+    const bool bf16 = dtype == TOPK_BF16;
+    PromptMaps maps;
+    const auto map3 = [&](CUtensorMap* m, const void* base, int64_t width, int64_t head_stride, int64_t tokens,
+                          int64_t token_stride, int rows) {
+        // A stride of 0 (all heads alike) is one head for the map; the stride
+        // of an extent of one is not used and need not be a legal one.
+        const int64_t heads = head_stride ? p.heads : 1;
+        const int64_t dims[3] = {width, heads, tokens};
+        const int64_t steps[2] = {2 * (heads > 1 ? head_stride : width), 2 * (tokens > 1 ? token_stride : width)};
+        return encode_map(m, bf16, base, 3, dims, steps, 2, rows);
+    };
+    const int64_t rope_dims[2] = {kRope, p.total_k}, rope_step[1] = {2 * (p.total_k > 1 ? p.k_rope_stride : kRope)};
+    // Without keys nothing is copied through their maps: any address will do.
+    const void* any = p.q;
+    CUresult r = map3(&maps.q, p.q, kNope + kRope, p.q_head_stride, p.total_q, p.q_token_stride, kTile);
+    if (r == CUDA_SUCCESS)
+        r = map3(&maps.k_nope, p.total_k ? p.k_nope : any, kNope, p.k_head_stride, p.total_k, p.k_token_stride, kTile);
+    if (r == CUDA_SUCCESS) r = encode_map(&maps.k_rope, bf16, p.total_k ? p.k_rope : any, 2, rope_dims, rope_step, 1, kTile);
+    if (r == CUDA_SUCCESS)
+        r = map3(&maps.v, p.total_k ? p.v : any, kValue, p.v_head_stride, p.total_k, p.v_token_stride, kTile / 2);
+    if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "prompt attention tensor map");
+
+    const auto kernel = bf16 ? prompt_kernel<true> : prompt_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return api_cuda_fail(e, "prompt attention shared memory");
+    // Every request adds at most one block to total / 256.
+    const unsigned grid = static_cast<unsigned>(p.heads) *
+                          static_cast<unsigned>(p.total_q / kBlockRows + (p.batch < p.total_q ? p.batch : p.total_q));
+    // Scores of a negative scale come from negated queries, so that the
+    // largest score is always the largest exponent.
+    // A scale of zero becomes the least normal number: hidden scores stay -inf.
+    const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
+    kernel<<<grid, kThreads, kSmem, stream>>>(p, maps, flags, scale_log2, p.scale < 0.f);
+    e = cudaGetLastError();
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "prompt attention launch");
 }
 

@@ -1,0 +1,231 @@
+// tc.cuh -- thin inline-PTX wrappers for the 5th-generation tensor cores
+// (tcgen05, tensor memory), tiled bulk copies and bounded waits.
+//
+// Shared-memory tiles are rows of 128 bytes (64 two-byte values) under the
+// 128-byte swizzle: the 16-byte piece c of row r lies at piece c ^ (r & 7) of
+// that row, and tiles start on 1024 bytes.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace topkidx {
+namespace tc {
+
+// ------------------------------------------------------------- descriptors
+// kind::f16 instruction: D fp32; A and B bf16 or fp16.  b_cols: B is stored
+// with its N index contiguous (a row of 128 bytes holds 64 columns of one k).
+__host__ __device__ constexpr uint32_t instruction(bool bf16, int m, int n, bool negate_a, bool b_cols) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((negate_a ? 1u : 0u) << 13) |
+           ((b_cols ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Shared-memory operand under the 128-byte swizzle.  K contiguous: groups of
+// eight rows are 1024 bytes apart, 16 values of k are 32 bytes further on.  N
+// contiguous (b_cols): groups of eight k are 1024 bytes apart, the next 64
+// columns `columns` bytes; 16 values of k are 2048 bytes further on.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t columns = 16) {
+    return (static_cast<uint64_t>((addr & 0x3ffffu) >> 4)) | (static_cast<uint64_t>(columns >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// ------------------------------------------------------------ tensor memory
+template <int kGroup>
+__device__ __forceinline__ void alloc(uint32_t smem_result, uint32_t columns) {
+    if constexpr (kGroup == 1)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_result),
+                     "r"(columns)
+                     : "memory");
+    else
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_result),
+                     "r"(columns)
+                     : "memory");
+}
+template <int kGroup>
+__device__ __forceinline__ void dealloc(uint32_t addr, uint32_t columns) {
+    if constexpr (kGroup == 1) {
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    } else {
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    }
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes (one lane a thread).
+__device__ __forceinline__ void load32(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void store32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// -------------------------------------------------------------- products
+// D[tmem] (+)= A B; issued by one thread.
+template <int kGroup>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+    if constexpr (kGroup == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(add))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(add))
+            : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// Arrives on `bar` once every product issued by this thread so far is done.
+template <int kGroup>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (kGroup == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         ptx::smem_addr(bar))
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         ptx::smem_addr(bar))
+                     : "memory");
+}
+// The same on the barrier at this offset in both blocks of a pair.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// Generic-proxy writes of shared memory before tensor-core reads of it.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ------------------------------------------------------------- tiled copies
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(ptx::smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(ptx::smem_addr(bar))
+        : "memory");
+}
+
+// Copies of a block pair: the bytes are counted on a barrier of either block
+// (a shared::cluster address).
+__device__ __forceinline__ void load_4d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+// Four rows of 64 values each, one row a coordinate; rows outside the tensor
+// are zeros.
+__device__ __forceinline__ void gather4_pair(uint32_t dst, const CUtensorMap* map, int x, int4 rows, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
+        : "memory");
+}
+// Arrival on a barrier of either block of the cluster.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// -------------------------------------------------------------- arithmetic
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two floats to two-byte values, `lo` in the low half.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    if constexpr (kBf16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ------------------------------------------------------------ bounded waits
+// A wait gives up after kLimitNs and sets the block's flag; from then on
+// every wait of the block returns at once, so that the block runs to its end
+// on whatever its buffers hold.
+constexpr uint64_t kLimitNs = 2000000000ull;
+
+struct Waits {
+    volatile uint32_t* gave_up;  // in shared memory
+
+    __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
+        if (ptx::mbar_test_wait(bar, parity)) return;
+        slow(bar, parity);
+    }
+    // By a whole warp, which goes on together.
+    __device__ __forceinline__ void warp(uint64_t* bar, uint32_t parity) const {
+        (*this)(bar, parity);
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool over() const { return __any_sync(~0u, *gave_up != 0u); }
+    __device__ __noinline__ void slow(uint64_t* bar, uint32_t parity) const {
+        const uint64_t t0 = ptx::global_timer_ns();
+        while (!*gave_up && !ptx::mbar_try_wait_sleep(bar, parity, 20000u)) {
+            if (ptx::global_timer_ns() - t0 >= kLimitNs) {
+                *gave_up = 1u;
+                return;
+            }
+        }
+    }
+    // For copies or products still in flight when a block ends early.
+    __device__ __forceinline__ static void drain(uint64_t* bar, uint32_t parity) {
+        (void)ptx::mbar_wait_bounded(bar, parity, kLimitNs);
+    }
+};
+
+}  // namespace tc
+}  // namespace topkidx
