@@ -18,9 +18,14 @@
 // shared, because one descriptor serves both blocks: 17/18 of the tile is
 // copied to each block (the second time from L2).
 //
-// The copies are gathers of four rows of 64 values by slot number; a slot that
-// is not seen gets a row outside the cache, which copies as zeros, so what it
-// holds never meets the sums.
+// Selected slots are copied 16 bytes a thread, two warps per block; a slot that
+// is not seen is filled with zeros, so what it holds never meets the sums.
+// (Gathers of four rows by the copy engine took 38-57 cycles for 512 bytes and
+// bound the kernel at 10400 cycles a tile.)  Pages of 16 slots or more are
+// copied by the engine, up to 64 rows of 64 values at a time; the rows past a
+// sequence's end are set to zero after they land.  In both cases a warp waits
+// for what landed, orders it before the products' reads, and tells the first
+// block.
 //
 // Work is cut in equal runs of tiles, through the rows' ends: the host does not
 // know the lengths.  A run's first and last row may be shared with the pairs
@@ -30,8 +35,8 @@
 //
 // Warps of each block: 0-3 softmax and results (thread t: row t & 63, slots 64
 // (t >> 6).. of the tile, values 256 (t >> 6).. of the sums), 4 products (first
-// block only), 5 copies of slots for the first product, 6 for the second, 7
-// queries.
+// block only), 5 copies of slots for the first product and of queries, 6 copies
+// for the second product, 7 tells of what landed.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -64,8 +69,9 @@ constexpr float kLag = 8.f;
 
 struct Shared {
     uint64_t query_full, query_empty;
-    uint64_t key_full[kKeyGroups], key_empty[kKeyGroups];
-    uint64_t value_full[2], value_empty[2];
+    // landed: in this block; full: in both (used in the first block).
+    uint64_t key_landed[kKeyGroups], key_full[kKeyGroups], key_empty[kKeyGroups];
+    uint64_t value_landed[2], value_full[2], value_empty[2];
     uint64_t score[2], weight, sum, end;
     uint64_t mask_full[4];
     uint32_t mask[4][4];
@@ -181,31 +187,19 @@ struct Walk {
     }
 };
 
-// The slots of four neighbouring positions, num_slots (outside the cache)
-// where there is none.
-__device__ __forceinline__ int4 slots_of(const LatentParams& p, int row, int length, int64_t at) {
-    int s[4];
-    if (p.indices) {
-        const int32_t* from = p.indices + static_cast<int64_t>(row) * p.indices_stride;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = at + i < length ? from[at + i] : -1;
-    } else {
-        const int32_t* from = p.table + static_cast<int64_t>(row) * p.table_stride;
-        const int mask = (1 << p.log2_page) - 1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[i] = -1;
-            if (at + i < length) {
-                const int pos = static_cast<int>(at) + i;
-                const int64_t slot = (static_cast<int64_t>(from[pos >> p.log2_page]) << p.log2_page) + (pos & mask);
-                if (slot >= 0 && slot < p.num_slots) s[i] = static_cast<int>(slot);
-            }
-        }
+// Slot of a position, -1 where it is not seen.
+template <bool kPaged>
+__device__ __forceinline__ int slot_of(const LatentParams& p, int row, int length, int64_t at) {
+    if (at >= length) return -1;
+    if (!kPaged && p.indices) {
+        const int32_t s = p.indices[static_cast<int64_t>(row) * p.indices_stride + at];
+        return s < p.num_slots ? s : -1;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (s[i] < 0 || s[i] >= p.num_slots) s[i] = p.num_slots;
-    return make_int4(s[0], s[1], s[2], s[3]);
+    const int pos = static_cast<int>(at);
+    const int64_t s = (static_cast<int64_t>(p.table[static_cast<int64_t>(row) * p.table_stride + (pos >> p.log2_page)])
+                       << p.log2_page) +
+                      (pos & ((1 << p.log2_page) - 1));
+    return s >= 0 && s < p.num_slots ? static_cast<int>(s) : -1;
 }
 
 // Partial sums in the workspace, two places a pair: 0 for a row begun by an
@@ -214,10 +208,10 @@ __device__ __forceinline__ float* part_sums(const LatentParams& p, int rows, int
     return static_cast<float*>(p.workspace) + static_cast<int64_t>(place) * rows * (kLatent + 2);
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kPaged>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_kernel(const LatentParams p, const __grid_constant__ LatentMaps maps, uint32_t* flags, float scale_log2,
-                  bool negate, bool whole_rows) {
+                  bool negate, bool whole_rows, int box_rows) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t queries = base, keys = queries + kQueryBytes, values = keys + kKeyBytes,
@@ -231,12 +225,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sh.gave_up = 0;
         ptx::mbar_init(&sh.query_full, 1);
         ptx::mbar_init(&sh.query_empty, 1);
+        const uint32_t landings = kPaged ? 1 : 32;
         for (int i = 0; i < kKeyGroups; ++i) {
-            ptx::mbar_init(&sh.key_full[i], 1);
+            ptx::mbar_init(&sh.key_landed[i], landings);
+            ptx::mbar_init(&sh.key_full[i], 2);
             ptx::mbar_init(&sh.key_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&sh.value_full[i], 1);
+            ptx::mbar_init(&sh.value_landed[i], landings);
+            ptx::mbar_init(&sh.value_full[i], 2);
             ptx::mbar_init(&sh.value_empty[i], 1);
             ptx::mbar_init(&sh.score[i], 1);
         }
@@ -256,96 +253,211 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walk walk(p, sh, pair, pairs);
     Segment s;
 
-    if (warp == 7) {
-        if (lane == 0) {
-            const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
-            for (int n = 0; walk.next(s); ++n) {
-                if (n > 0) wait(&sh.query_empty, (n - 1) & 1);
-                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full, 2 * kQueryBytes);
-                const int m = s.group * kRows + rank * kHalf;
-                for (int c = 0; c < kPieces; ++c) {
-                    if (whole_rows) {
-                        tc::load_4d_pair(queries + c * kKeyPiece, &maps.q, 64 * c, m, 0, s.row, full);
-                    } else {
-                        for (int i = 0; i < kHalf; ++i)
-                            tc::load_4d_pair(queries + c * kKeyPiece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
-                                             (m + i) / p.heads, s.row, full);
-                    }
-                }
-                if (sh.gave_up) {
-                    if (rank == 0) tc::Waits::drain(&sh.query_full, n & 1);
-                    break;
-                }
+    if (warp == 5) {
+        // Slots 64 rank.. of each tile, all values, and the segments' queries.
+        const uint32_t query_full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
+        int n = 0, segment = 0;
+        bool more = walk.next(s), fresh = true;
+        int tile = s.first, row = s.row, group = s.group;
+        const auto fetch = [&](int* slots) {  // slots lane and lane + 32 of the half, or those of box `lane`
+            const int64_t at = static_cast<int64_t>(tile) * kTile + rank * kHalf;
+            if (kPaged) {
+                slots[0] = lane * box_rows < kHalf ? slot_of<kPaged>(p, s.row, s.length, at + lane * box_rows) : -1;
+            } else {
+                slots[0] = slot_of<kPaged>(p, s.row, s.length, at + lane);
+                slots[1] = slot_of<kPaged>(p, s.row, s.length, at + 32 + lane);
             }
-        }
-    } else if (warp == 5) {
-        // Slots 64 rank.. of each tile, all values: 16 gathers a piece, lane
-        // i those of slots 4 (i % 16)...
-        uint32_t full[kKeyGroups];
-        for (int g = 0; g < kKeyGroups; ++g) full[g] = ptx::map_rank(ptx::smem_addr(&sh.key_full[g]), 0);
-        const int at = rank * kHalf + 4 * (lane & 15);
-        int n = 0;
-        bool more = walk.next(s);
-        int tile = s.first;
-        int4 slots = more ? slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at) : int4{};
+        };
+        int next_slots[2];
+        if (more) fetch(next_slots);
         while (more && !wait.over()) {
-            const int4 now = slots;
+            const int slots[2] = {next_slots[0], next_slots[1]};
+            const bool load_queries = fresh;
+            row = s.row;
+            group = s.group;
             // The next tile's slots are fetched while this one's copies wait.
-            if (++tile == s.last) {
+            fresh = ++tile == s.last;
+            if (fresh) {
                 more = walk.next(s);
                 tile = s.first;
             }
-            if (more) slots = slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at);
+            if (more) fetch(next_slots);
+            const uint8_t* from[16];
+            uint32_t bytes = 0;
+            if (!kPaged) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int slot = __shfl_sync(~0u, slots[q >> 3], (4 * q + (lane >> 3)) & 31);
+                    bytes |= (slot >= 0 ? 1u : 0u) << q;
+                    from[q] = static_cast<const uint8_t*>(p.cache) + max(slot, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
+                }
+            }
             for (int g = 0; g < kKeyGroups; ++g) {
                 if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
-                if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_full[g], 2 * 3 * kKeyPiece);
-                for (int i = lane >> 4; i < 3; i += 2)
-                    tc::gather4_pair(keys + (3 * g + i) * kKeyPiece + (lane & 15) * 512, &maps.cache, 64 * (3 * g + i), now,
-                                     full[g]);
+                const uint32_t to = keys + 3 * g * kKeyPiece;
+                if (kPaged) {
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], 3 * kKeyPiece);
+                    __syncwarp();
+                    if (lane * box_rows < kHalf)
+                        for (int c = 0; c < 3; ++c)
+                            tc::load_2d(to + c * kKeyPiece + lane * box_rows * 128, &maps.cache, 64 * (3 * g + c),
+                                        slots[0] < 0 ? p.num_slots : slots[0], &sh.key_landed[g]);
+                } else {
+                    const int r = lane >> 3;
+                    const uint32_t even = to + r * 128 + (((lane & 7) ^ r) << 4), odd = to + r * 128 + (((lane & 7) ^ r ^ 4) << 4);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+#pragma unroll
+                        for (int c = 0; c < 3; ++c)
+                            tc::copy16((q & 1 ? odd : even) + q * 512 + c * kKeyPiece, from[q] + 128 * (3 * g + c),
+                                       ((bytes >> q) & 1) * 16);
+                    tc::copy16_arrive(&sh.key_landed[g]);
+                }
             }
             ++n;
+            if (load_queries) {
+                if (lane == 0) {
+                    if (segment > 0) wait(&sh.query_empty, (segment - 1) & 1);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full, 2 * kQueryBytes);
+                    const int m = group * kRows + rank * kHalf;
+                    for (int c = 0; c < kPieces; ++c) {
+                        if (whole_rows) {
+                            tc::load_4d_pair(queries + c * kKeyPiece, &maps.q, 64 * c, m, 0, row, query_full);
+                        } else {
+                            for (int i = 0; i < kHalf; ++i)
+                                tc::load_4d_pair(queries + c * kKeyPiece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
+                                                 (m + i) / p.heads, row, query_full);
+                        }
+                    }
+                }
+                __syncwarp();
+                ++segment;
+            }
         }
-        __syncwarp();
-        if (sh.gave_up && rank == 0 && n > 0)
-            for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_full[g], (n - 1) & 1);
+        if (!kPaged) tc::copy16_drain();
+        if (wait.over()) {
+            if (kPaged && n > 0)
+                for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
+            if (rank == 0 && segment > 0) tc::Waits::drain(&sh.query_full, (segment - 1) & 1);
+        }
     } else if (warp == 6) {
-        // All slots of each tile, values 256 rank..: 32 gathers a piece.
-        uint32_t full[2];
-        for (int g = 0; g < 2; ++g) full[g] = ptx::map_rank(ptx::smem_addr(&sh.value_full[g]), 0);
+        // All slots of each tile, values 256 rank...
         int n = 0;
         bool more = walk.next(s);
         int tile = s.first;
-        int4 slots = more ? slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 4 * lane) : int4{};
+        const auto fetch = [&](int* slots) {  // slots lane, lane + 32, ..
+            for (int i = 0; i < 4; ++i)
+                slots[i] = slot_of<kPaged>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
+        };
+        int next_slots[4];
+        if (more) fetch(next_slots);
         while (more && !wait.over()) {
-            const int4 now = slots;
+            const int slots[4] = {next_slots[0], next_slots[1], next_slots[2], next_slots[3]};
             if (++tile == s.last) {
                 more = walk.next(s);
                 tile = s.first;
             }
-            if (more) slots = slots_of(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 4 * lane);
+            if (more) fetch(next_slots);
             // One bit a slot that is seen.  Place n % 4 was last read for tile
             // n - 4, whose second product the copies of tile n - 2 waited for.
-            uint32_t bits = (now.x < p.num_slots ? 1u : 0u) | (now.y < p.num_slots ? 2u : 0u) |
-                            (now.z < p.num_slots ? 4u : 0u) | (now.w < p.num_slots ? 8u : 0u);
-            bits <<= 4 * (lane & 7);
-            bits |= __shfl_xor_sync(~0u, bits, 1);
-            bits |= __shfl_xor_sync(~0u, bits, 2);
-            bits |= __shfl_xor_sync(~0u, bits, 4);
-            if ((lane & 7) == 0) sh.mask[n & 3][lane >> 3] = bits;
-            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = __ballot_sync(~0u, slots[i] >= 0);
+                if (lane == 0) sh.mask[n & 3][i] = bits;
+            }
             if (lane == 0) ptx::mbar_arrive(&sh.mask_full[n & 3]);
+            int box = -1;
+            if (kPaged) {
+                // Box `lane` starts at position lane * box_rows of the tile.
+                const int at = lane * box_rows;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = __shfl_sync(~0u, slots[i], at & 31);
+                    if ((at >> 5) == i) box = x;
+                }
+            }
             for (int g = 0; g < 2; ++g) {
                 if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
-                if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_full[g], 2 * 2 * kValuePiece);
-                for (int i = 0; i < 2; ++i)
-                    tc::gather4_pair(values + (2 * g + i) * kValuePiece + lane * 512, &maps.cache,
-                                     256 * rank + 64 * (2 * g + i), now, full[g]);
+                const uint32_t to = values + 2 * g * kValuePiece;
+                if (kPaged) {
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_landed[g], 2 * kValuePiece);
+                    __syncwarp();
+                    if (lane * box_rows < kTile)
+                        for (int c = 0; c < 2; ++c)
+                            tc::load_2d(to + c * kValuePiece + lane * box_rows * 128, &maps.cache,
+                                        256 * rank + 64 * (2 * g + c), box < 0 ? p.num_slots : box, &sh.value_landed[g]);
+                } else {
+                    const int r = lane >> 3;
+                    const uint32_t even = to + r * 128 + (((lane & 7) ^ r) << 4), odd = to + r * 128 + (((lane & 7) ^ r ^ 4) << 4);
+                    const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + 256 * g + (lane & 7) * 16;
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        const int slot = __shfl_sync(~0u, slots[q >> 3], (4 * q + r) & 31);
+                        const uint8_t* from = cache + max(slot, 0) * (2 * p.slot_stride);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tc::copy16((q & 1 ? odd : even) + q * 512 + c * kValuePiece, from + 128 * c, slot >= 0 ? 16 : 0);
+                    }
+                    tc::copy16_arrive(&sh.value_landed[g]);
+                }
             }
             ++n;
         }
-        __syncwarp();
-        if (sh.gave_up && rank == 0 && n > 0)
-            for (int g = 0; g < 2; ++g) tc::Waits::drain(&sh.value_full[g], (n - 1) & 1);
+        if (!kPaged) tc::copy16_drain();
+        if (kPaged && n > 0 && wait.over())
+            for (int g = 0; g < 2; ++g) tc::Waits::drain(&sh.value_landed[g], (n - 1) & 1);
+    } else if (warp == 7) {
+        // Tells the first block of each group of pieces that landed here,
+        // those of keys and of values as they come.
+        const int64_t tiles = walk.left;
+        int64_t keys_done = 0, values_done = 0;
+        int kg = 0, vg = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        uint64_t idle = 0;
+        while (more && (keys_done < tiles || values_done < tiles)) {
+            if (keys_done < tiles &&
+                __any_sync(~0u, ptx::mbar_test_wait(&sh.key_landed[kg], static_cast<uint32_t>(keys_done) & 1))) {
+                tc::fence_async();
+                __syncwarp();
+                if (lane == 0) tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.key_full[kg]), 0));
+                if (++kg == kKeyGroups) {
+                    kg = 0;
+                    ++keys_done;
+                }
+                idle = 0;
+            } else if (values_done < tiles &&
+                       __any_sync(~0u, ptx::mbar_test_wait(&sh.value_landed[vg], static_cast<uint32_t>(values_done) & 1))) {
+                const int left = s.length - tile * kTile;
+                if (kPaged && left < kTile) {
+                    // Rows past the sequence's end may hold anything, and a
+                    // weight of zero would not hide a NaN.
+                    for (int i = max(left, 0) * 16 + lane; i < kTile * 16; i += 32)
+                        ptx::sts_u4(values + (2 * vg + ((i >> 3) & 1)) * kValuePiece + (i >> 4) * 128 + (i & 7) * 16,
+                                    make_uint4(0, 0, 0, 0));
+                }
+                tc::fence_async();
+                __syncwarp();
+                if (lane == 0) tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.value_full[vg]), 0));
+                if (++vg == 2) {
+                    vg = 0;
+                    ++values_done;
+                    if (++tile == s.last && values_done < tiles) {
+                        walk.next(s);
+                        tile = s.first;
+                    }
+                }
+                idle = 0;
+            } else {
+                const uint64_t now = ptx::global_timer_ns();
+                if (idle == 0) idle = now;
+                if (__any_sync(~0u, now - idle >= tc::kLimitNs)) {
+                    if (lane == 0) *wait.gave_up = 1u;
+                    __syncwarp();
+                }
+                if (wait.over()) break;
+            }
+        }
     } else if (warp == 4) {
         if (rank == 0 && lane == 0) {
             const uint32_t score_instr = tc::instruction(kBf16, kRows, kTile, negate, false);
@@ -629,10 +741,14 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t*
                                 p.batch > 1 ? 2 * p.q_row_stride : any};
     CUresult r = encode_map(&maps.q, bf16, p.q, 4, q_dims, q_steps, 1, whole_rows ? kHalf : 1);
     const int64_t c_dims[2] = {kWidth, p.num_slots}, c_steps[1] = {2 * p.slot_stride};
-    if (r == CUDA_SUCCESS) r = encode_map(&maps.cache, bf16, p.cache, 2, c_dims, c_steps, 1, 1);
+    // Pages of 16 slots or more go through the copy engine.
+    const bool paged = !p.indices && p.log2_page >= 4;
+    const int box_rows = paged && p.log2_page < 6 ? 1 << p.log2_page : kHalf;
+    if (r == CUDA_SUCCESS) r = encode_map(&maps.cache, bf16, p.cache, 2, c_dims, c_steps, 1, box_rows);
     if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "latent attention tensor map");
 
-    const auto kernel = bf16 ? latent_kernel<true> : latent_kernel<false>;
+    const auto kernel = paged ? (bf16 ? latent_kernel<true, true> : latent_kernel<false, true>)
+                              : (bf16 ? latent_kernel<true, false> : latent_kernel<false, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention shared memory");
     const int64_t groups = (static_cast<int64_t>(p.queries) * p.heads + kRows - 1) / kRows;
@@ -640,7 +756,8 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t*
     const int device = pairs_of_device();
     const int pairs = tiles < device ? static_cast<int>(tiles) : device;
     const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
-    kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps, flags, scale_log2, p.scale < 0.f, whole_rows);
+    kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps, flags, scale_log2, p.scale < 0.f, whole_rows,
+                                                  box_rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
     if (pairs > 1) {

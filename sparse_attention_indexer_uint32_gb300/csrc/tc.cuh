@@ -162,15 +162,15 @@ __device__ __forceinline__ void load_4d_pair(uint32_t dst, const CUtensorMap* ma
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
-// Four rows of 64 values each, one row a coordinate; rows outside the tensor
-// are zeros.
-__device__ __forceinline__ void gather4_pair(uint32_t dst, const CUtensorMap* map, int x, int4 rows, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
-        : "memory");
+// 16 bytes, or zeros where `bytes` is 0 (then nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// Arrives on `bar` (one of its expected arrivals) once this thread's copy16s so far have landed.
+__device__ __forceinline__ void copy16_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void copy16_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrival on a barrier of either block of the cluster.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
