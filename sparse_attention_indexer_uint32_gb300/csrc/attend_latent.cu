@@ -414,7 +414,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int kg = 0, vg = 0;
         bool more = walk.next(s);
         int tile = s.first;
-        uint64_t idle = 0;
+        uint32_t idle = 0;
+        uint64_t since = 0;
         while (more && (keys_done < tiles || values_done < tiles)) {
             if (keys_done < tiles &&
                 __any_sync(~0u, ptx::mbar_test_wait(&sh.key_landed[kg], static_cast<uint32_t>(keys_done) & 1))) {
@@ -449,33 +450,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 idle = 0;
             } else {
-                const uint64_t now = ptx::global_timer_ns();
-                if (idle == 0) idle = now;
-                if (__any_sync(~0u, now - idle >= tc::kLimitNs)) {
-                    if (lane == 0) *wait.gave_up = 1u;
-                    __syncwarp();
+                // The clock and the block's flag are looked at now and then.
+                if ((++idle & 255) == 0) {
+                    const uint64_t now = ptx::global_timer_ns();
+                    if (idle == 256) since = now;
+                    if (__any_sync(~0u, now - since >= tc::kLimitNs)) {
+                        if (lane == 0) *wait.gave_up = 1u;
+                        __syncwarp();
+                    }
+                    if (wait.over()) break;
                 }
-                if (wait.over()) break;
             }
         }
     } else if (warp == 4) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t score_instr = tc::instruction(kBf16, kRows, kTile, negate, false);
             const uint32_t sum_instr = tc::instruction(kBf16, kRows, 256, false, true);
+            const uint64_t query_at = tc::operand(queries), key_at = tc::operand(keys), weight_at = tc::operand(weights),
+                           value_at = tc::operand(values, kValuePiece);
             const auto sums = [&](int n, bool add) {  // second product of tile n
-                wait(&sh.weight, n & 1);
+                wait.warp(&sh.weight, n & 1);
                 tc::fence_after();
                 for (int g = 0; g < 2; ++g) {
-                    wait(&sh.value_full[g], n & 1);
+                    wait.warp(&sh.value_full[g], n & 1);
+                    if (tc::elect()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint64_t a = tc::operand(weights + (k >> 2) * kKeyPiece) + 2 * (k & 3);
-                        const uint64_t b = tc::operand(values + 2 * g * kValuePiece, kValuePiece) + 128 * k;
-                        tc::mma<2>(tmem + 128 * g, a, b, sum_instr, add || k > 0);
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma<2>(tmem + 128 * g, weight_at + (k >> 2) * (kKeyPiece >> 4) + 2 * (k & 3),
+                                       value_at + 2 * g * (kValuePiece >> 4) + 128 * k, sum_instr, add || k > 0);
+                        tc::commit_pair(&sh.value_empty[g]);
+                        if (g == 1) tc::commit_pair(&sh.sum);
                     }
-                    tc::commit_pair(&sh.value_empty[g]);
+                    __syncwarp();
                 }
-                tc::commit_pair(&sh.sum);
             };
             int n = 0;
             bool add = false;  // whether the sums of the tile before are added to
@@ -485,27 +492,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         // The queries' place is free before the last sums of
                         // the segment before are due: those go first.
                         if (n > 0) sums(n - 1, add);
-                        wait(&sh.query_full, segment & 1);
+                        wait.warp(&sh.query_full, segment & 1);
                     }
                     for (int g = 0; g < kKeyGroups; ++g) {
-                        wait(&sh.key_full[g], n & 1);
+                        wait.warp(&sh.key_full[g], n & 1);
+                        if (tc::elect()) {
 #pragma unroll
-                        for (int k = 0; k < 12; ++k) {
-                            const uint32_t piece = (3 * g + (k >> 2)) * kKeyPiece;
-                            tc::mma<2>(tmem + kScore + kHalf * (n & 1), tc::operand(queries + piece) + 2 * (k & 3),
-                                       tc::operand(keys + piece) + 2 * (k & 3), score_instr, (g | k) != 0);
+                            for (int k = 0; k < 12; ++k) {
+                                const uint32_t at = (3 * g + (k >> 2)) * (kKeyPiece >> 4) + 2 * (k & 3);
+                                tc::mma<2>(tmem + kScore + kHalf * (n & 1), query_at + at, key_at + at, score_instr,
+                                           (g | k) != 0);
+                            }
+                            tc::commit_pair(&sh.key_empty[g]);
+                            if (g == kKeyGroups - 1) {
+                                tc::commit_pair(&sh.score[n & 1]);
+                                if (tile == s.last - 1) tc::commit_pair(&sh.query_empty);
+                            }
                         }
-                        tc::commit_pair(&sh.key_empty[g]);
+                        __syncwarp();
                     }
-                    tc::commit_pair(&sh.score[n & 1]);
-                    if (tile == s.last - 1) tc::commit_pair(&sh.query_empty);
                     if (tile > s.first) sums(n - 1, add);
                     add = tile > s.first;
                 }
             }
             if (n > 0) sums(n - 1, add);
-            tc::commit<2>(&sh.end);
-            tc::Waits::drain(&sh.end, 0);
+            if (tc::elect()) {
+                tc::commit<2>(&sh.end);
+                tc::Waits::drain(&sh.end, 0);
+            }
         }
     } else {
         const int r = threadIdx.x & 63, half = threadIdx.x >> 6;
