@@ -18,7 +18,7 @@
 // shared, because one descriptor serves both blocks: 17/18 of the tile is
 // copied to each block (the second time from L2).
 //
-// Selected slots are copied 16 bytes a thread, two warps per block; a slot that
+// Selected slots are copied 16 bytes a thread, four warps per block; a slot that
 // is not seen is filled with zeros, so what it holds never meets the sums.
 // (Gathers of four rows by the copy engine took 38-57 cycles for 512 bytes and
 // bound the kernel at 10400 cycles a tile.)  Pages of 16 slots or more are
@@ -35,8 +35,8 @@
 //
 // Warps of each block: 0-3 softmax and results (thread t: row t & 63, slots 64
 // (t >> 6).. of the tile, values 256 (t >> 6).. of the sums), 4 products (first
-// block only), 5 copies of slots for the first product and of queries, 6 copies
-// for the second product, 7 tells of what landed.
+// block only), 5 and 8 copies for the first product, 6 and 9 for the second, 7
+// tells of what landed, 10 queries, 11 rows to L2 ahead of their copies.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -53,7 +53,8 @@ namespace {
 constexpr int kRows = 128;                  // (query, head) rows of a pair
 constexpr int kTile = 128;                  // slots a step
 constexpr int kHalf = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kQueryWarp = 10, kPrefetchWarp = 11;
 constexpr int kMaxPairs = 80;
 constexpr int kKeyPiece = kHalf * 128;      // 64 slots of 64 values
 constexpr int kValuePiece = kTile * 128;    // 128 slots of 64 values
@@ -77,6 +78,7 @@ struct Shared {
     uint32_t mask[4][4];
     float exchange[2][kRows];
     uint32_t tmem, gave_up;
+    volatile int32_t copied;  // tiles whose first copies are all under way
     int64_t begin, total;  // first tile of this pair's run, tiles of all runs
     int32_t row, tile;     // where the run begins: row of the batch, tile in its group rows
     int64_t scan[kThreads / 32];
@@ -223,9 +225,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         sh.gave_up = 0;
+        sh.copied = 0;
         ptx::mbar_init(&sh.query_full, 1);
         ptx::mbar_init(&sh.query_empty, 1);
-        const uint32_t landings = kPaged ? 1 : 32;
+        const uint32_t landings = kPaged ? 1 : 64;
         for (int i = 0; i < kKeyGroups; ++i) {
             ptx::mbar_init(&sh.key_landed[i], landings);
             ptx::mbar_init(&sh.key_full[i], 2);
@@ -240,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&sh.weight, 8);
         ptx::mbar_init(&sh.sum, 1);
         ptx::mbar_init(&sh.end, 1);
-        for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh.mask_full[i], 1);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh.mask_full[i], kPaged ? 1 : 2);
         ptx::fence_mbarrier_init();
     }
     if (warp == 4) tc::alloc<2>(ptx::smem_addr(&sh.tmem), kColumns);
@@ -253,101 +256,138 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walk walk(p, sh, pair, pairs);
     Segment s;
 
-    if (warp == 5) {
-        // Slots 64 rank.. of each tile, all values, and the segments' queries.
-        const uint32_t query_full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
-        int n = 0, segment = 0;
-        bool more = walk.next(s), fresh = true;
-        int tile = s.first, row = s.row, group = s.group;
-        const auto fetch = [&](int* slots) {  // slots lane and lane + 32 of the half, or those of box `lane`
-            const int64_t at = static_cast<int64_t>(tile) * kTile + rank * kHalf;
-            if (kPaged) {
-                slots[0] = lane * box_rows < kHalf ? slot_of<kPaged>(p, s.row, s.length, at + lane * box_rows) : -1;
-            } else {
-                slots[0] = slot_of<kPaged>(p, s.row, s.length, at + lane);
-                slots[1] = slot_of<kPaged>(p, s.row, s.length, at + 32 + lane);
+    if (!kPaged && (warp == 5 || warp == 8)) {
+        // Selected slots, first product: slots 64 rank + 32 part.. of each
+        // tile, all values; 16 bytes a lane, four rows at a time.
+        const int part = warp == 8 ? 1 : 0, r = lane >> 3;
+        const int at = rank * kHalf + 32 * part + lane;
+        int n = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        int next_slot = more ? slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at) : -1;
+        while (more && !wait.over()) {
+            const int slot = next_slot;
+            // The next tile's slots are fetched while this one's copies wait.
+            if (++tile == s.last) {
+                more = walk.next(s);
+                tile = s.first;
             }
+            if (more) next_slot = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at);
+            const uint8_t* from[8];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int x = __shfl_sync(~0u, slot, 4 * q + r);
+                bytes |= (x >= 0 ? 1u : 0u) << q;
+                from[q] = static_cast<const uint8_t*>(p.cache) + max(x, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
+            }
+            for (int g = 0; g < kKeyGroups; ++g) {
+                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
+                const uint32_t to = keys + 3 * g * kKeyPiece + part * 4096 + r * 128;
+                const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+                        tc::copy16((q & 1 ? odd : even) + q * 512 + c * kKeyPiece, from[q] + 128 * (3 * g + c),
+                                   ((bytes >> q) & 1) * 16);
+                tc::copy16_arrive(&sh.key_landed[g]);
+            }
+            ++n;
+            if (part == 0 && lane == 0) sh.copied = n;
+        }
+        tc::copy16_drain();
+    } else if (!kPaged && (warp == 6 || warp == 9)) {
+        // Selected slots, second product: slots 64 part.. of each tile,
+        // values 256 rank...
+        const int part = warp == 9 ? 1 : 0, r = lane >> 3;
+        int n = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        const auto fetch = [&](int* slots) {
+            for (int i = 0; i < 2; ++i)
+                slots[i] = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + kHalf * part + 32 * i + lane);
         };
         int next_slots[2];
         if (more) fetch(next_slots);
         while (more && !wait.over()) {
             const int slots[2] = {next_slots[0], next_slots[1]};
-            const bool load_queries = fresh;
-            row = s.row;
-            group = s.group;
-            // The next tile's slots are fetched while this one's copies wait.
-            fresh = ++tile == s.last;
-            if (fresh) {
+            if (++tile == s.last) {
                 more = walk.next(s);
                 tile = s.first;
             }
             if (more) fetch(next_slots);
-            const uint8_t* from[16];
-            uint32_t bytes = 0;
-            if (!kPaged) {
+            // One bit a slot that is seen.  Place n % 4 was last read for tile
+            // n - 4, whose second product the copies of tile n - 2 waited for.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t bits = __ballot_sync(~0u, slots[i] >= 0);
+                if (lane == 0) sh.mask[n & 3][2 * part + i] = bits;
+            }
+            if (lane == 0) ptx::mbar_arrive(&sh.mask_full[n & 3]);
+            for (int g = 0; g < 2; ++g) {
+                if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
+                const uint32_t to = values + 2 * g * kValuePiece + part * kKeyPiece + r * 128;
+                const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
+                const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + 256 * g + (lane & 7) * 16;
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
-                    const int slot = __shfl_sync(~0u, slots[q >> 3], (4 * q + (lane >> 3)) & 31);
-                    bytes |= (slot >= 0 ? 1u : 0u) << q;
-                    from[q] = static_cast<const uint8_t*>(p.cache) + max(slot, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
-                }
-            }
-            for (int g = 0; g < kKeyGroups; ++g) {
-                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
-                const uint32_t to = keys + 3 * g * kKeyPiece;
-                if (kPaged) {
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], 3 * kKeyPiece);
-                    __syncwarp();
-                    if (lane * box_rows < kHalf)
-                        for (int c = 0; c < 3; ++c)
-                            tc::load_2d(to + c * kKeyPiece + lane * box_rows * 128, &maps.cache, 64 * (3 * g + c),
-                                        slots[0] < 0 ? p.num_slots : slots[0], &sh.key_landed[g]);
-                } else {
-                    const int r = lane >> 3;
-                    const uint32_t even = to + r * 128 + (((lane & 7) ^ r) << 4), odd = to + r * 128 + (((lane & 7) ^ r ^ 4) << 4);
+                    const int x = __shfl_sync(~0u, slots[q >> 3], (4 * q + r) & 31);
+                    const uint8_t* from = cache + max(x, 0) * (2 * p.slot_stride);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q)
-#pragma unroll
-                        for (int c = 0; c < 3; ++c)
-                            tc::copy16((q & 1 ? odd : even) + q * 512 + c * kKeyPiece, from[q] + 128 * (3 * g + c),
-                                       ((bytes >> q) & 1) * 16);
-                    tc::copy16_arrive(&sh.key_landed[g]);
+                    for (int c = 0; c < 2; ++c)
+                        tc::copy16((q & 1 ? odd : even) + q * 512 + c * kValuePiece, from + 128 * c, x >= 0 ? 16 : 0);
                 }
+                tc::copy16_arrive(&sh.value_landed[g]);
             }
             ++n;
-            if (load_queries) {
-                if (lane == 0) {
-                    if (segment > 0) wait(&sh.query_empty, (segment - 1) & 1);
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full, 2 * kQueryBytes);
-                    const int m = group * kRows + rank * kHalf;
-                    for (int c = 0; c < kPieces; ++c) {
-                        if (whole_rows) {
-                            tc::load_4d_pair(queries + c * kKeyPiece, &maps.q, 64 * c, m, 0, row, query_full);
-                        } else {
-                            for (int i = 0; i < kHalf; ++i)
-                                tc::load_4d_pair(queries + c * kKeyPiece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
-                                                 (m + i) / p.heads, row, query_full);
-                        }
-                    }
-                }
-                __syncwarp();
-                ++segment;
+        }
+        tc::copy16_drain();
+    } else if (kPaged && warp == 5) {
+        // Pages, first product: slots 64 rank.. of each tile, all values.
+        int n = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        const bool mine = lane * box_rows < kHalf;
+        const auto fetch = [&]() {  // row of the cache at which box `lane` begins
+            const int x = mine ? slot_of<true>(p, s.row, s.length,
+                                               static_cast<int64_t>(tile) * kTile + rank * kHalf + lane * box_rows)
+                               : -1;
+            return x < 0 ? p.num_slots : x;
+        };
+        int next_box = more ? fetch() : 0;
+        while (more && !wait.over()) {
+            const int box = next_box;
+            if (++tile == s.last) {
+                more = walk.next(s);
+                tile = s.first;
             }
+            if (more) next_box = fetch();
+            for (int g = 0; g < kKeyGroups; ++g) {
+                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], 3 * kKeyPiece);
+                __syncwarp();
+                if (mine)
+                    for (int c = 3 * g; c < 3 * g + 3; ++c)
+                        tc::load_2d(keys + c * kKeyPiece + lane * box_rows * 128, &maps.cache, 64 * c, box,
+                                    &sh.key_landed[g]);
+            }
+            ++n;
+            // The rows of the next tile come to L2 while this one's are used:
+            // shared memory has room for one tile only.
+            if (more && mine)
+                for (int c = 0; c < kPieces; ++c) tc::prefetch_2d(&maps.cache, 64 * c, next_box);
         }
-        if (!kPaged) tc::copy16_drain();
-        if (wait.over()) {
-            if (kPaged && n > 0)
-                for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
-            if (rank == 0 && segment > 0) tc::Waits::drain(&sh.query_full, (segment - 1) & 1);
-        }
-    } else if (warp == 6) {
-        // All slots of each tile, values 256 rank...
+        if (n > 0 && wait.over())
+            for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
+    } else if (kPaged && warp == 6) {
+        // Pages, second product: all slots of each tile, values 256 rank...
         int n = 0;
         bool more = walk.next(s);
         int tile = s.first;
         const auto fetch = [&](int* slots) {  // slots lane, lane + 32, ..
             for (int i = 0; i < 4; ++i)
-                slots[i] = slot_of<kPaged>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
+                slots[i] = slot_of<true>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
         };
         int next_slots[4];
         if (more) fetch(next_slots);
@@ -358,54 +398,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tile = s.first;
             }
             if (more) fetch(next_slots);
-            // One bit a slot that is seen.  Place n % 4 was last read for tile
-            // n - 4, whose second product the copies of tile n - 2 waited for.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) {  // as for selected slots
                 const uint32_t bits = __ballot_sync(~0u, slots[i] >= 0);
                 if (lane == 0) sh.mask[n & 3][i] = bits;
             }
             if (lane == 0) ptx::mbar_arrive(&sh.mask_full[n & 3]);
+            // Box `lane` starts at position lane * box_rows of the tile.
+            const int at = lane * box_rows;
             int box = -1;
-            if (kPaged) {
-                // Box `lane` starts at position lane * box_rows of the tile.
-                const int at = lane * box_rows;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int x = __shfl_sync(~0u, slots[i], at & 31);
-                    if ((at >> 5) == i) box = x;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int x = __shfl_sync(~0u, slots[i], at & 31);
+                if ((at >> 5) == i) box = x;
             }
+            if (box < 0) box = p.num_slots;
             for (int g = 0; g < 2; ++g) {
                 if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
-                const uint32_t to = values + 2 * g * kValuePiece;
-                if (kPaged) {
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_landed[g], 2 * kValuePiece);
-                    __syncwarp();
-                    if (lane * box_rows < kTile)
-                        for (int c = 0; c < 2; ++c)
-                            tc::load_2d(to + c * kValuePiece + lane * box_rows * 128, &maps.cache,
-                                        256 * rank + 64 * (2 * g + c), box < 0 ? p.num_slots : box, &sh.value_landed[g]);
-                } else {
-                    const int r = lane >> 3;
-                    const uint32_t even = to + r * 128 + (((lane & 7) ^ r) << 4), odd = to + r * 128 + (((lane & 7) ^ r ^ 4) << 4);
-                    const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + 256 * g + (lane & 7) * 16;
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        const int slot = __shfl_sync(~0u, slots[q >> 3], (4 * q + r) & 31);
-                        const uint8_t* from = cache + max(slot, 0) * (2 * p.slot_stride);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tc::copy16((q & 1 ? odd : even) + q * 512 + c * kValuePiece, from + 128 * c, slot >= 0 ? 16 : 0);
-                    }
-                    tc::copy16_arrive(&sh.value_landed[g]);
-                }
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_landed[g], 2 * kValuePiece);
+                __syncwarp();
+                if (at < kTile)
+                    for (int c = 2 * g; c < 2 * g + 2; ++c)
+                        tc::load_2d(values + c * kValuePiece + at * 128, &maps.cache, 256 * rank + 64 * c, box,
+                                    &sh.value_landed[g]);
             }
             ++n;
         }
-        if (!kPaged) tc::copy16_drain();
-        if (kPaged && n > 0 && wait.over())
+        if (n > 0 && wait.over())
             for (int g = 0; g < 2; ++g) tc::Waits::drain(&sh.value_landed[g], (n - 1) & 1);
+    } else if (warp == kQueryWarp) {
+        if (lane == 0) {
+            const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
+            for (int n = 0; walk.next(s); ++n) {
+                if (n > 0) wait(&sh.query_empty, (n - 1) & 1);
+                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full, 2 * kQueryBytes);
+                const int m = s.group * kRows + rank * kHalf;
+                for (int c = 0; c < kPieces; ++c) {
+                    if (whole_rows) {
+                        tc::load_4d_pair(queries + c * kKeyPiece, &maps.q, 64 * c, m, 0, s.row, full);
+                    } else {
+                        for (int i = 0; i < kHalf; ++i)
+                            tc::load_4d_pair(queries + c * kKeyPiece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
+                                             (m + i) / p.heads, s.row, full);
+                    }
+                }
+                if (*wait.gave_up) {
+                    if (rank == 0) tc::Waits::drain(&sh.query_full, n & 1);
+                    break;
+                }
+            }
+        }
+    } else if (!kPaged && warp == kPrefetchWarp) {
+        // The rows of the tile after the one being copied come to L2 while
+        // that one's are used: shared memory has room for one tile only.
+        const int at = rank * kHalf + lane;
+        int n = 0;
+        uint32_t spins = 0;
+        uint64_t since = 0;
+        bool over = false;
+        while (!over && walk.next(s))
+            for (int tile = s.first; tile < s.last && !over; ++tile, ++n) {
+                int slots[2];
+                for (int i = 0; i < 2; ++i)
+                    slots[i] = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at + 32 * i);
+                // Once the copies of the tile before are under way; a tile
+                // whose own copies are needs no more help.
+                while (!over && __any_sync(~0u, sh.copied < n)) over = wait.idle(spins, since);
+                spins = 0;
+                if (__any_sync(~0u, sh.copied > n)) continue;
+                for (int i = 0; i < 2; ++i)
+                    if (slots[i] >= 0) {
+                        const uint8_t* row = static_cast<const uint8_t*>(p.cache) + slots[i] * (2 * p.slot_stride);
+                        for (int c = 0; c < kPieces; ++c) ptx::prefetch_l2(row + 128 * c);
+                    }
+            }
     } else if (warp == 7) {
         // Tells the first block of each group of pieces that landed here,
         // those of keys and of values as they come.
@@ -414,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int kg = 0, vg = 0;
         bool more = walk.next(s);
         int tile = s.first;
-        uint32_t idle = 0;
+        uint32_t spins = 0;
         uint64_t since = 0;
         while (more && (keys_done < tiles || values_done < tiles)) {
             if (keys_done < tiles &&
@@ -426,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     kg = 0;
                     ++keys_done;
                 }
-                idle = 0;
+                spins = 0;
             } else if (values_done < tiles &&
                        __any_sync(~0u, ptx::mbar_test_wait(&sh.value_landed[vg], static_cast<uint32_t>(values_done) & 1))) {
                 const int left = s.length - tile * kTile;
@@ -448,18 +514,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tile = s.first;
                     }
                 }
-                idle = 0;
+                spins = 0;
             } else {
-                // The clock and the block's flag are looked at now and then.
-                if ((++idle & 255) == 0) {
-                    const uint64_t now = ptx::global_timer_ns();
-                    if (idle == 256) since = now;
-                    if (__any_sync(~0u, now - since >= tc::kLimitNs)) {
-                        if (lane == 0) *wait.gave_up = 1u;
-                        __syncwarp();
-                    }
-                    if (wait.over()) break;
-                }
+                if (wait.idle(spins, since)) break;
             }
         }
     } else if (warp == 4) {
@@ -468,60 +525,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t sum_instr = tc::instruction(kBf16, kRows, 256, false, true);
             const uint64_t query_at = tc::operand(queries), key_at = tc::operand(keys), weight_at = tc::operand(weights),
                            value_at = tc::operand(values, kValuePiece);
-            const auto sums = [&](int n, bool add) {  // second product of tile n
-                wait.warp(&sh.weight, n & 1);
-                tc::fence_after();
-                for (int g = 0; g < 2; ++g) {
-                    wait.warp(&sh.value_full[g], n & 1);
+            // A third of the first product of tile `scored`, at most one ahead
+            // of the second (there are two score tiles), or a half of the
+            // second product of tile `summed`: whichever has its operands, so
+            // that neither waits behind the other's copies.
+            const auto ready = [](uint64_t* bar, int64_t n) {
+                return __any_sync(~0u, ptx::mbar_test_wait(bar, static_cast<uint32_t>(n) & 1));
+            };
+            const int64_t tiles = walk.left;
+            int64_t scored = 0, summed = 0;
+            int kg = 0, vg = 0, tile = 0, segment = -1;
+            bool first[2] = {};  // whether tiles n - 1 and n, by n mod 2, begin their segments
+            uint32_t spins = 0;
+            uint64_t since = 0;
+            s.first = s.last = 0;
+            while (summed < tiles) {
+                if (summed < scored && (vg > 0 || ready(&sh.weight, summed)) && ready(&sh.value_full[vg], summed)) {
+                    const bool add = !first[summed & 1];
+                    tc::fence_after();
                     if (tc::elect()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            tc::mma<2>(tmem + 128 * g, weight_at + (k >> 2) * (kKeyPiece >> 4) + 2 * (k & 3),
-                                       value_at + 2 * g * (kValuePiece >> 4) + 128 * k, sum_instr, add || k > 0);
-                        tc::commit_pair(&sh.value_empty[g]);
-                        if (g == 1) tc::commit_pair(&sh.sum);
+                            tc::mma<2>(tmem + 128 * vg, weight_at + (k >> 2) * (kKeyPiece >> 4) + 2 * (k & 3),
+                                       value_at + 2 * vg * (kValuePiece >> 4) + 128 * k, sum_instr, add || k > 0);
+                        tc::commit_pair(&sh.value_empty[vg]);
+                        if (vg == 1) tc::commit_pair(&sh.sum);
                     }
                     __syncwarp();
+                    vg ^= 1;
+                    if (vg == 0) ++summed;
+                    spins = 0;
+                    continue;
                 }
-            };
-            int n = 0;
-            bool add = false;  // whether the sums of the tile before are added to
-            for (int segment = 0; walk.next(s); ++segment) {
-                for (int tile = s.first; tile < s.last; ++tile, ++n) {
-                    if (tile == s.first) {
-                        // The queries' place is free before the last sums of
-                        // the segment before are due: those go first.
-                        if (n > 0) sums(n - 1, add);
-                        wait.warp(&sh.query_full, segment & 1);
+                if (scored < tiles && scored - summed < 2) {
+                    if (tile == s.last) {
+                        walk.next(s);
+                        tile = s.first;
+                        ++segment;
                     }
-                    for (int g = 0; g < kKeyGroups; ++g) {
-                        wait.warp(&sh.key_full[g], n & 1);
+                    if ((kg > 0 || tile > s.first || ready(&sh.query_full, segment)) && ready(&sh.key_full[kg], scored)) {
+                        const uint32_t d = tmem + kScore + kHalf * (static_cast<uint32_t>(scored) & 1);
+                        tc::fence_after();
                         if (tc::elect()) {
 #pragma unroll
                             for (int k = 0; k < 12; ++k) {
-                                const uint32_t at = (3 * g + (k >> 2)) * (kKeyPiece >> 4) + 2 * (k & 3);
-                                tc::mma<2>(tmem + kScore + kHalf * (n & 1), query_at + at, key_at + at, score_instr,
-                                           (g | k) != 0);
+                                const uint32_t at = (3 * kg + (k >> 2)) * (kKeyPiece >> 4) + 2 * (k & 3);
+                                tc::mma<2>(d, query_at + at, key_at + at, score_instr, (kg | k) != 0);
                             }
-                            tc::commit_pair(&sh.key_empty[g]);
-                            if (g == kKeyGroups - 1) {
-                                tc::commit_pair(&sh.score[n & 1]);
+                            tc::commit_pair(&sh.key_empty[kg]);
+                            if (kg == kKeyGroups - 1) {
+                                tc::commit_pair(&sh.score[scored & 1]);
                                 if (tile == s.last - 1) tc::commit_pair(&sh.query_empty);
                             }
                         }
                         __syncwarp();
+                        if (++kg == kKeyGroups) {
+                            kg = 0;
+                            first[scored & 1] = tile == s.first;
+                            ++tile;
+                            ++scored;
+                        }
+                        spins = 0;
+                        continue;
                     }
-                    if (tile > s.first) sums(n - 1, add);
-                    add = tile > s.first;
                 }
+                if (wait.idle(spins, since)) break;
             }
-            if (n > 0) sums(n - 1, add);
             if (tc::elect()) {
                 tc::commit<2>(&sh.end);
                 tc::Waits::drain(&sh.end, 0);
             }
         }
-    } else {
+    } else if (warp < 4) {
         const int r = threadIdx.x & 63, half = threadIdx.x >> 6;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
         const uint32_t weight_full = ptx::map_rank(ptx::smem_addr(&sh.weight), 0);

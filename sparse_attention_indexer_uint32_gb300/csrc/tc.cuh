@@ -155,6 +155,11 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, in
         "l"(map), "r"(x), "r"(y), "r"(ptx::smem_addr(bar))
         : "memory");
 }
+// The same tile to L2 only.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
@@ -225,6 +230,17 @@ struct Waits {
     __device__ __forceinline__ void warp(uint64_t* bar, uint32_t parity) const {
         (*this)(bar, parity);
         __syncwarp();
+    }
+    // For a warp that polls several barriers: counts a poll in which none was
+    // ready, looks at the clock and the flag now and then, and says whether to
+    // give up.  `spins` is 0 after one that was.
+    __device__ __forceinline__ bool idle(uint32_t& spins, uint64_t& since) const {
+        if ((++spins & 255) != 0) return false;
+        const uint64_t now = ptx::global_timer_ns();
+        if (spins == 256) since = now;
+        if (now - since >= kLimitNs) *gave_up = 1u;
+        __syncwarp();
+        return over();
     }
     __device__ __forceinline__ bool over() const { return __any_sync(~0u, *gave_up != 0u); }
     __device__ __noinline__ void slow(uint64_t* bar, uint32_t parity) const {
