@@ -325,7 +325,7 @@ size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads
  *   cache             device [num_slots][slot_stride], 576 values used.
  *   indices           device int32[rows][indices_stride], k used per row.
  *   rows, heads, k    >= 1; rows * heads <= 2^30.
- *   out               device [rows][heads][512], contiguous.
+ *   out               device [rows][heads][512], contiguous, 32-byte aligned.
  *   lse_or_null       device float[rows][heads].
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_ENOSPACE, TOPK_EDEVICE, TOPK_ECUDA.
  */
@@ -347,7 +347,8 @@ topk_status_t topk_attend_selected(const void* q, int64_t q_row_stride, int64_t 
  *                     i * q_query_stride, head h at h * q_head_stride.
  *   page_table        as in topk_transform; page_table_stride >=
  *                     ceil(max_seq_len / page_size).
- *   out               device [batch][queries][heads][512], contiguous.
+ *   out               device [batch][queries][heads][512], contiguous, 32-byte
+ *                     aligned.
  *   lse_or_null       device float[batch][queries][heads].
  */
 topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_query_stride, int64_t q_head_stride,
@@ -380,7 +381,7 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
  *                     [0, total] are clamped to it, and one below an earlier
  *                     one counts as that.
  *   total_q, total_k  >= 0 (total_q 0: nothing is enqueued).
- *   out               device [total_q][heads][128], contiguous.
+ *   out               device [total_q][heads][128], contiguous, 32-byte aligned.
  *   lse_or_null       device float[total_q][heads].
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
  */

@@ -46,10 +46,19 @@ def topk_transform(scores: torch.Tensor, seq_lens: torch.Tensor, page_table: tor
 
 
 _DTYPES = {torch.bfloat16: _lib.TOPK_BF16, torch.float16: _lib.TOPK_FP16}
+_LATENT, _ROPE, _NOPE, _VALUE = _lib.TOPK_LATENT_DIM, _lib.TOPK_ROPE_DIM, _lib.TOPK_NOPE_DIM, _lib.TOPK_VALUE_DIM
+_WIDTH = _LATENT + _ROPE
+_I32, _F32 = torch.int32, torch.float32
+_c = _lib.library()
+
+
+# The calls below look their arguments over twice at most: one condition that
+# is true of every right call (a few microseconds), and, where it is not, the
+# checks that say which argument is wrong.
 
 
 def _same(dtype: torch.dtype, device: torch.device, **tensors) -> None:
-    """Raises unless the tensors (None is skipped) are of this type, on this device, with contiguous rows."""
+    """Raises unless the tensors (None is skipped) are of this type, on this GPU, with contiguous rows."""
     for name, t in tensors.items():
         if t is None:
             continue
@@ -66,6 +75,11 @@ def _whole(shape: tuple, **tensors) -> None:
             raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}: got {tuple(t.shape)}")
 
 
+def _on_gpu(t: torch.Tensor) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"the tensors must be on a GPU: got {t.device}")
+
+
 def _step(t: torch.Tensor, dim: int, least: int) -> int:
     """Stride of a dimension; `least` where there is one entry, whose stride means nothing."""
     return t.stride(dim) if t.shape[dim] > 1 else least
@@ -76,6 +90,10 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     if code is None:
         raise ValueError(f"{name} must be bfloat16 or float16: got {t.dtype}")
     return code
+
+
+def _is(t: torch.Tensor, dtype: torch.dtype, gpu: int, shape: tuple) -> bool:
+    return t.dtype is dtype and t.get_device() == gpu and t.shape == shape and t.is_contiguous()
 
 
 class BlockTables(NamedTuple):
@@ -89,27 +107,63 @@ class BlockTables(NamedTuple):
     status: torch.Tensor  # [2]
 
 
+def _check_tables(context_lens, new_lens, free_pages, page_table, max_tokens, out):
+    dev = context_lens.device
+    _same(_I32, dev, context_lens=context_lens, new_lens=new_lens, free_pages=free_pages, page_table=page_table)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [batch, pages]: got {tuple(page_table.shape)}")
+    batch = page_table.shape[0]
+    _whole((batch,), context_lens=context_lens, new_lens=new_lens)
+    _whole((free_pages.numel(),), free_pages=free_pages)
+    if out is not None:
+        _same(_I32, dev, **out._asdict())
+        _whole((batch,), seq_lens=out.seq_lens)
+        _whole((batch + 1,), cu_new=out.cu_new)
+        _whole((max_tokens,), slots=out.slots, positions=out.positions, rows=out.rows)
+        _whole((2,), status=out.status)
+    _on_gpu(context_lens)
+
+
 def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
                  page_table: torch.Tensor, page_size: int, max_tokens: int, out: BlockTables | None = None,
                  stream=None) -> BlockTables:
     """Runs ``topk_block_tables``: writes the new pages into ``page_table`` ([batch, pages], in place) and returns
     the step's lengths, offsets and slot map (in ``out``, where the result of an earlier call is given)."""
-    dev, i32 = context_lens.device, torch.int32
-    batch, pages = page_table.shape
-    _same(i32, dev, context_lens=context_lens, new_lens=new_lens, free_pages=free_pages, page_table=page_table)
-    _whole((batch,), context_lens=context_lens, new_lens=new_lens)
+    gpu, shape = context_lens.get_device(), page_table.shape
+    if not (gpu >= 0 and len(shape) == 2 and page_table.dtype is _I32 and page_table.get_device() == gpu
+            and (shape[1] <= 1 or page_table.stride(1) == 1) and _is(context_lens, _I32, gpu, shape[:1])
+            and _is(new_lens, _I32, gpu, shape[:1]) and _is(free_pages, _I32, gpu, (free_pages.numel(),))
+            and (out is None or (_is(out[0], _I32, gpu, shape[:1]) and _is(out[1], _I32, gpu, (shape[0] + 1,))
+                                 and _is(out[2], _I32, gpu, (max_tokens,)) and _is(out[3], _I32, gpu, (max_tokens,))
+                                 and _is(out[4], _I32, gpu, (max_tokens,)) and _is(out[5], _I32, gpu, (2,))))):
+        _check_tables(context_lens, new_lens, free_pages, page_table, max_tokens, out)
+    batch, pages = shape
     if out is None:
-        buf = torch.empty(2 * batch + 3 + 3 * max_tokens, dtype=i32, device=dev)
+        buf = torch.empty(2 * batch + 3 + 3 * max_tokens, dtype=_I32, device=context_lens.device)
         out = BlockTables(*buf.split([batch, batch + 1, max_tokens, max_tokens, max_tokens, 2]))
-    else:
-        _same(i32, dev, **out._asdict())
-        _whole((batch,), seq_lens=out.seq_lens)
-        _whole((batch + 1,), cu_new=out.cu_new)
-        _whole((max_tokens,), slots=out.slots, positions=out.positions, rows=out.rows)
-        _whole((2,), status=out.status)
-    _lib.topk_block_tables(context_lens, new_lens, batch, page_size, free_pages, free_pages.numel(), page_table,
-                           _step(page_table, 0, pages), pages, max_tokens, *out, stream)
+    status = _c.topk_block_tables(
+        context_lens.data_ptr(), new_lens.data_ptr(), batch, page_size, free_pages.data_ptr(), free_pages.numel(),
+        page_table.data_ptr(), page_table.stride(0) if batch > 1 else pages, pages, max_tokens, out[0].data_ptr(),
+        out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), out[5].data_ptr(),
+        _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_block_tables", status)
     return out
+
+
+def _check_append(rows, slots, cache, norm_weight, cos_sin, positions):
+    dev = cache.device
+    _dtype(cache, "cache")
+    _same(cache.dtype, dev, rows=rows, cache=cache, norm_weight=norm_weight)
+    _same(_I32, dev, slots=slots, positions=positions)
+    _same(_F32, dev, cos_sin=cos_sin)
+    if rows.dim() != 2 or cache.dim() != 2 or rows.shape[1] != _WIDTH or cache.shape[1] != _WIDTH:
+        raise ValueError(f"rows and cache must be [.., {_WIDTH}]: got {tuple(rows.shape)} and {tuple(cache.shape)}")
+    _whole((rows.shape[0],), slots=slots, positions=positions)
+    _whole((_LATENT,), norm_weight=norm_weight)
+    if cos_sin is not None:
+        _whole((cos_sin.shape[0], _ROPE), cos_sin=cos_sin)
+    _on_gpu(cache)
 
 
 def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
@@ -118,42 +172,50 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     """Runs ``topk_cache_append``: ``rows`` [tokens, 576] (512 latent values, 64 rotary ones) to ``slots`` of
     ``cache`` [num_slots, 576], normed by ``norm_weight`` [512] and rotated by ``cos_sin`` (float32
     [num_positions, 64]: cosines, sines) at ``positions``, where these are given."""
-    dev, width = cache.device, _lib.TOPK_LATENT_DIM + _lib.TOPK_ROPE_DIM
-    code, tokens = _dtype(cache, "cache"), rows.shape[0]
-    _same(cache.dtype, dev, rows=rows, cache=cache, norm_weight=norm_weight)
-    _same(torch.int32, dev, slots=slots, positions=positions)
-    _same(torch.float32, dev, cos_sin=cos_sin)
-    if rows.dim() != 2 or cache.dim() != 2 or rows.shape[1] != width or cache.shape[1] != width:
-        raise ValueError(f"rows and cache must be [.., {width}]: got {tuple(rows.shape)} and {tuple(cache.shape)}")
-    _whole((tokens,), slots=slots, positions=positions)
-    _whole((_lib.TOPK_LATENT_DIM,), norm_weight=norm_weight)
-    if cos_sin is not None:
-        _whole((cos_sin.shape[0], _lib.TOPK_ROPE_DIM), cos_sin=cos_sin)
-    _lib.topk_cache_append(rows, _step(rows, 0, width), tokens, norm_weight, eps, cos_sin,
-                           0 if cos_sin is None else cos_sin.shape[0], positions, interleaved, slots, cache,
-                           _step(cache, 0, width), cache.shape[0], code, stream)
+    gpu, dtype, shape, places = cache.get_device(), cache.dtype, rows.shape, cache.shape
+    code = _DTYPES.get(dtype)
+    if not (gpu >= 0 and code is not None and rows.dtype is dtype and rows.get_device() == gpu and len(shape) == 2
+            and len(places) == 2 and shape[1] == _WIDTH == places[1] and rows.stride(1) == 1 == cache.stride(1)
+            and _is(slots, _I32, gpu, shape[:1]) and (positions is None or _is(positions, _I32, gpu, shape[:1]))
+            and (norm_weight is None or _is(norm_weight, dtype, gpu, (_LATENT,)))
+            and (cos_sin is None or _is(cos_sin, _F32, gpu, (len(cos_sin), _ROPE)))):
+        _check_append(rows, slots, cache, norm_weight, cos_sin, positions)
+    status = _c.topk_cache_append(
+        rows.data_ptr(), rows.stride(0) if shape[0] > 1 else _WIDTH, shape[0],
+        None if norm_weight is None else norm_weight.data_ptr(), eps, None if cos_sin is None else cos_sin.data_ptr(),
+        0 if cos_sin is None else len(cos_sin), None if positions is None else positions.data_ptr(), interleaved,
+        slots.data_ptr(), cache.data_ptr(), cache.stride(0) if places[0] > 1 else _WIDTH, places[0], code,
+        _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_cache_append", status)
 
 
-def _attend_outputs(q, cache, batch, queries, heads, out, lse, workspace):
-    """Checks (or allocates) what both cache attentions share."""
-    dev = q.device
-    _same(q.dtype, dev, q=q, cache=cache, out=out)
-    width, latent = _lib.TOPK_LATENT_DIM + _lib.TOPK_ROPE_DIM, _lib.TOPK_LATENT_DIM
-    if q.shape[-1] != width or cache.dim() != 2 or cache.shape[1] != width:
-        raise ValueError(f"q and cache must be [.., {width}]: got {tuple(q.shape)} and {tuple(cache.shape)}")
-    if out is None:
-        out = torch.empty((*q.shape[:-1], latent), dtype=q.dtype, device=dev)
-    else:
-        _whole((*q.shape[:-1], latent), out=out)
-    if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    else:
-        _same(torch.float32, dev, lse=lse)
-        _whole(q.shape[:-1], lse=lse)
-    need = _lib.topk_attend_workspace_bytes(batch, queries, heads)
+def _check_attend(q, cache, out, lse):
+    """What both cache attentions share."""
+    _dtype(q, "q")
+    _same(q.dtype, q.device, q=q, cache=cache, out=out)
+    if q.shape[-1] != _WIDTH or cache.dim() != 2 or cache.shape[1] != _WIDTH:
+        raise ValueError(f"q and cache must be [.., {_WIDTH}]: got {tuple(q.shape)} and {tuple(cache.shape)}")
+    _whole((*q.shape[:-1], _LATENT), out=out)
+    _same(_F32, q.device, lse=lse)
+    _whole(q.shape[:-1], lse=lse)
+    _on_gpu(q)
+
+
+def _fits(q, cache, out, lse, gpu, dtype, shape) -> bool:
+    """Whether they are what both cache attentions take."""
+    rows = cache.shape
+    return (gpu >= 0 and shape[-1] == _WIDTH and q.stride(-1) == 1 and cache.dtype is dtype
+            and cache.get_device() == gpu and len(rows) == 2 and rows[1] == _WIDTH and cache.stride(1) == 1
+            and (out is None or _is(out, dtype, gpu, shape[:-1] + (_LATENT,)))
+            and (lse is None or _is(lse, _F32, gpu, shape[:-1])))
+
+
+def _attend_workspace(workspace, batch, queries, heads, device):
+    need = _c.topk_attend_workspace_bytes(batch, queries, heads)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return out, lse, workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace
 
 
 def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor, scale: float,
@@ -162,16 +224,34 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
     """Runs ``topk_attend_selected``: ``q`` [rows, heads, 576] over the slots ``indices`` [rows, k] (int32, as
     :func:`topk_transform` writes them) of ``cache`` [num_slots, 576].  ``seq_lens`` [rows], where given, bounds
     the slots looked at.  Returns ``(out [rows, heads, 512], lse [rows, heads], workspace)``."""
-    if q.dim() != 3 or indices.dim() != 2 or indices.shape[0] != q.shape[0]:
-        raise ValueError(f"q and indices must be [rows, heads, ..] and [rows, k]: got {tuple(q.shape)} and "
-                         f"{tuple(indices.shape)}")
-    code, (rows, heads, _) = _dtype(q, "q"), q.shape
-    _same(torch.int32, q.device, indices=indices, seq_lens=seq_lens)
-    _whole((rows,), seq_lens=seq_lens)
-    out, lse, workspace = _attend_outputs(q, cache, rows, 1, heads, out, lse, workspace)
-    _lib.topk_attend_selected(q, _step(q, 0, 0), _step(q, 1, 0), cache, _step(cache, 0, cache.shape[1]), cache.shape[0],
-                              indices, _step(indices, 0, indices.shape[1]), seq_lens, rows, heads, indices.shape[1], scale, code, out, lse,
-                              workspace, stream)
+    gpu, dtype, shape, listed = q.get_device(), q.dtype, q.shape, indices.shape
+    code = _DTYPES.get(dtype)
+    if not (code is not None and len(shape) == 3 and len(listed) == 2 and listed[0] == shape[0]
+            and indices.dtype is _I32 and indices.get_device() == gpu and (listed[1] <= 1 or indices.stride(1) == 1)
+            and (seq_lens is None or _is(seq_lens, _I32, gpu, shape[:1]))
+            and _fits(q, cache, out, lse, gpu, dtype, shape)):
+        if q.dim() != 3 or indices.dim() != 2 or indices.shape[0] != q.shape[0]:
+            raise ValueError(f"q and indices must be [rows, heads, ..] and [rows, k]: got {tuple(q.shape)} and "
+                             f"{tuple(indices.shape)}")
+        _dtype(q, "q")
+        _same(_I32, q.device, indices=indices, seq_lens=seq_lens)
+        _whole(shape[:1], seq_lens=seq_lens)
+        _check_attend(q, cache, out, lse)
+    rows, heads, _ = shape
+    if out is None:
+        out = torch.empty((rows, heads, _LATENT), dtype=dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=_F32, device=q.device)
+    workspace = _attend_workspace(workspace, rows, 1, heads, q.device)
+    slots = cache.shape[0]
+    status = _c.topk_attend_selected(
+        q.data_ptr(), _step(q, 0, _WIDTH), _step(q, 1, _WIDTH), cache.data_ptr(),
+        cache.stride(0) if slots > 1 else _WIDTH, slots, indices.data_ptr(),
+        indices.stride(0) if rows > 1 else listed[1], None if seq_lens is None else seq_lens.data_ptr(), rows, heads,
+        listed[1], scale, code, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_attend_selected", status)
     return out, lse, workspace
 
 
@@ -181,21 +261,60 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
     """Runs ``topk_attend_paged``: ``q`` [batch, queries, heads, 576], the newest tokens' queries, over each
     request's positions through ``page_table`` [batch, pages].  Returns ``(out [batch, queries, heads, 512],
     lse [batch, queries, heads], workspace)``."""
-    if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
-        raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
-                         f"{tuple(q.shape)} and {tuple(page_table.shape)}")
-    code, (batch, queries, heads, _) = _dtype(q, "q"), q.shape
-    _same(torch.int32, q.device, seq_lens=seq_lens, page_table=page_table)
-    _whole((batch,), seq_lens=seq_lens)
+    gpu, dtype, shape, listed = q.get_device(), q.dtype, q.shape, page_table.shape
+    code = _DTYPES.get(dtype)
+    if not (code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
+            and page_table.dtype is _I32 and page_table.get_device() == gpu
+            and (listed[1] <= 1 or page_table.stride(1) == 1) and _is(seq_lens, _I32, gpu, shape[:1])
+            and _fits(q, cache, out, lse, gpu, dtype, shape)):
+        if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+            raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
+                             f"{tuple(q.shape)} and {tuple(page_table.shape)}")
+        _dtype(q, "q")
+        _same(_I32, q.device, seq_lens=seq_lens, page_table=page_table)
+        _whole(shape[:1], seq_lens=seq_lens)
+        if max_seq_len is not None and max_seq_len > listed[1] * page_size:
+            raise ValueError(f"max_seq_len {max_seq_len} is over {listed[1]} pages of {page_size}")
+        _check_attend(q, cache, out, lse)
+    batch, queries, heads, _ = shape
     if max_seq_len is None:
-        max_seq_len = min(page_table.shape[1] * page_size, 2 ** 31 - 1)
-    elif max_seq_len > page_table.shape[1] * page_size:
-        raise ValueError(f"max_seq_len {max_seq_len} is over {page_table.shape[1]} pages of {page_size}")
-    out, lse, workspace = _attend_outputs(q, cache, batch, queries, heads, out, lse, workspace)
-    _lib.topk_attend_paged(q, _step(q, 0, 0), _step(q, 1, 0), _step(q, 2, 0), cache, _step(cache, 0, cache.shape[1]),
-                           cache.shape[0], seq_lens, page_table, _step(page_table, 0, page_table.shape[1]), page_size, max_seq_len, batch, queries, heads,
-                           scale, code, out, lse, workspace, stream)
+        max_seq_len = min(listed[1] * page_size, 2 ** 31 - 1)
+    elif max_seq_len > listed[1] * page_size:
+        raise ValueError(f"max_seq_len {max_seq_len} is over {listed[1]} pages of {page_size}")
+    if out is None:
+        out = torch.empty((batch, queries, heads, _LATENT), dtype=dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((batch, queries, heads), dtype=_F32, device=q.device)
+    workspace = _attend_workspace(workspace, batch, queries, heads, q.device)
+    slots = cache.shape[0]
+    status = _c.topk_attend_paged(
+        q.data_ptr(), _step(q, 0, _WIDTH), _step(q, 1, _WIDTH), _step(q, 2, _WIDTH), cache.data_ptr(),
+        cache.stride(0) if slots > 1 else _WIDTH, slots, seq_lens.data_ptr(), page_table.data_ptr(),
+        page_table.stride(0) if batch > 1 else listed[1], page_size, max_seq_len, batch, queries, heads, scale, code,
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_attend_paged", status)
     return out, lse, workspace
+
+
+def _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse):
+    dev = q.device
+    _dtype(q, "q")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q and v must be [tokens, heads, ..]: got {tuple(q.shape)} and {tuple(v.shape)}")
+    (total_q, heads, _), total_k = q.shape, v.shape[0]
+    for name, t, shape in (("q", q, (total_q, heads, _NOPE + _ROPE)), ("k_nope", k_nope, (total_k, heads, _NOPE)),
+                           ("k_rope", k_rope, (total_k, _ROPE)), ("v", v, (total_k, heads, _VALUE))):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}: got {tuple(t.shape)}")
+    _whole(cu_q.shape[:1], cu_q=cu_q, cu_k=cu_k)
+    _whole((total_q, heads, _VALUE), out=out)
+    _whole((total_q, heads), lse=lse)
+    _same(q.dtype, dev, q=q, k_nope=k_nope, k_rope=k_rope, v=v, out=out)
+    _same(_I32, dev, cu_q=cu_q, cu_k=cu_k)
+    _same(_F32, dev, lse=lse)
+    _on_gpu(q)
 
 
 def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -204,29 +323,27 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
     """Runs ``topk_attend_prompt``: ``q`` [total_q, heads, 192], ``k_nope`` [total_k, heads, 128], ``k_rope``
     [total_k, 64], ``v`` [total_k, heads, 128], requests by the offsets ``cu_q`` and ``cu_k`` [batch + 1].
     Returns ``(out [total_q, heads, 128], lse [total_q, heads])``."""
-    code, dev = _dtype(q, "q"), q.device
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError(f"q and v must be [tokens, heads, ..]: got {tuple(q.shape)} and {tuple(v.shape)}")
-    (total_q, heads, _), total_k = q.shape, v.shape[0]
-    _same(q.dtype, dev, q=q, k_nope=k_nope, k_rope=k_rope, v=v, out=out)
-    _same(torch.int32, dev, cu_q=cu_q, cu_k=cu_k)
-    nope, rope, value = _lib.TOPK_NOPE_DIM, _lib.TOPK_ROPE_DIM, _lib.TOPK_VALUE_DIM
-    for name, t, shape in (("q", q, (total_q, heads, nope + rope)), ("k_nope", k_nope, (total_k, heads, nope)),
-                           ("k_rope", k_rope, (total_k, rope)), ("v", v, (total_k, heads, value))):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {shape}: got {tuple(t.shape)}")
-    _whole(cu_q.shape[:1], cu_q=cu_q, cu_k=cu_k)
+    gpu, dtype, shape, marks = q.get_device(), q.dtype, q.shape, cu_q.shape
+    code, tokens = _DTYPES.get(dtype), v.shape[:1]
+    if not (gpu >= 0 and code is not None and len(shape) == 3 and shape[2] == _NOPE + _ROPE and q.stride(2) == 1
+            and k_nope.dtype is dtype and k_nope.get_device() == gpu and k_nope.shape == tokens + (shape[1], _NOPE)
+            and k_nope.stride(2) == 1 and v.dtype is dtype and v.get_device() == gpu
+            and v.shape == tokens + (shape[1], _VALUE) and v.stride(2) == 1 and k_rope.dtype is dtype
+            and k_rope.get_device() == gpu and k_rope.shape == tokens + (_ROPE,) and k_rope.stride(1) == 1
+            and len(marks) == 1 and _is(cu_q, _I32, gpu, marks) and _is(cu_k, _I32, gpu, marks)
+            and (out is None or _is(out, dtype, gpu, shape[:2] + (_VALUE,)))
+            and (lse is None or _is(lse, _F32, gpu, shape[:2]))):
+        _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse)
+    total_q, heads, _ = shape
     if out is None:
-        out = torch.empty((total_q, heads, value), dtype=q.dtype, device=dev)
-    else:
-        _whole((total_q, heads, value), out=out)
+        out = torch.empty((total_q, heads, _VALUE), dtype=dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((total_q, heads), dtype=torch.float32, device=dev)
-    else:
-        _same(torch.float32, dev, lse=lse)
-        _whole((total_q, heads), lse=lse)
-    _lib.topk_attend_prompt(q, _step(q, 0, nope + rope), _step(q, 1, nope + rope), k_nope, _step(k_nope, 0, nope),
-                            _step(k_nope, 1, nope), k_rope, _step(k_rope, 0, rope), v, _step(v, 0, value),
-                            _step(v, 1, value), cu_q, cu_k, cu_q.shape[0] - 1, total_q, total_k, heads, scale, causal,
-                            code, out, lse, stream)
+        lse = torch.empty((total_q, heads), dtype=_F32, device=q.device)
+    status = _c.topk_attend_prompt(
+        q.data_ptr(), _step(q, 0, _NOPE + _ROPE), _step(q, 1, _NOPE + _ROPE), k_nope.data_ptr(),
+        _step(k_nope, 0, _NOPE), _step(k_nope, 1, _NOPE), k_rope.data_ptr(), _step(k_rope, 0, _ROPE), v.data_ptr(),
+        _step(v, 0, _VALUE), _step(v, 1, _VALUE), cu_q.data_ptr(), cu_k.data_ptr(), marks[0] - 1, total_q, tokens[0],
+        heads, scale, causal, code, out.data_ptr(), lse.data_ptr(), _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_attend_prompt", status)
     return out, lse

@@ -2,6 +2,7 @@
 // entry points of include/topkidx.h: argument checks before any launch.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -37,21 +38,30 @@ constexpr int64_t kMaxQueryHeads = int64_t{1} << 30;
 // The word in which the attention kernels note a wait that gave up, one per GPU.
 __device__ uint32_t g_attend_flags;
 
-// Its address on the current device, looked up once per device.
-topk_status_t attend_flags(uint32_t** flags) {
-    constexpr int kMaxDevices = 64;
+// The current device, looked up once.
+topk_status_t attend_device(AttendDevice* out) {
+    static AttendDevice known[AttendDevice::kMax];
+    static std::atomic<bool> looked_up[AttendDevice::kMax];
     static std::mutex mutex;
-    static void* known[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return api_cuda_fail(e, "cudaGetDevice");
-    if (dev < 0 || dev >= kMaxDevices) return api_cuda_fail(cudaErrorInvalidDevice, "attention flags");
-    std::lock_guard<std::mutex> lock(mutex);
-    if (!known[dev]) {
-        e = cudaGetSymbolAddress(&known[dev], g_attend_flags);
-        if (e != cudaSuccess) return api_cuda_fail(e, "attention flags");
+    if (dev < 0 || dev >= AttendDevice::kMax) return api_cuda_fail(cudaErrorInvalidDevice, "attention device");
+    if (!looked_up[dev].load(std::memory_order_acquire)) {
+        const topk_status_t st = api_check_device();
+        if (st != TOPK_OK) return st;
+        std::lock_guard<std::mutex> lock(mutex);
+        AttendDevice d;
+        d.index = dev;
+        void* flags = nullptr;
+        e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaGetSymbolAddress(&flags, g_attend_flags);
+        if (e != cudaSuccess) return api_cuda_fail(e, "attention device");
+        d.flags = static_cast<uint32_t*>(flags);
+        known[dev] = d;
+        looked_up[dev].store(true, std::memory_order_release);
     }
-    *flags = static_cast<uint32_t*>(known[dev]);
+    *out = known[dev];
     return TOPK_OK;
 }
 
@@ -124,17 +134,17 @@ topk_status_t check_latent(const LatentParams& p, topk_dtype_t dtype, size_t wor
         !token_stride_ok(p.q_head_stride, kWidth, p.heads))
         return TOPK_EINVAL;
     if (workspace_bytes < need) return TOPK_ENOSPACE;
-    if (misaligned(p.q, 16) || misaligned(p.cache, 16) || misaligned(p.out, 16) || misaligned(p.workspace, 16) ||
+    if (misaligned(p.q, 16) || misaligned(p.cache, 16) || misaligned(p.out, 32) || misaligned(p.workspace, 16) ||
         misaligned(p.lse, 4) || misaligned(p.indices, 4) || misaligned(p.seq_lens, 4) || misaligned(p.table, 4) ||
         p.q_row_stride % 8 || p.q_query_stride % 8 || p.q_head_stride % 8 || p.slot_stride % 8)
         return TOPK_EALIGN;
-    return api_check_device();
+    return TOPK_OK;
 }
 
 topk_status_t run_latent(const LatentParams& p, topk_dtype_t dtype, cudaStream_t stream) {
-    uint32_t* flags = nullptr;
-    const topk_status_t st = attend_flags(&flags);
-    return st == TOPK_OK ? launch_latent(p, dtype, flags, stream) : st;
+    AttendDevice device;
+    const topk_status_t st = attend_device(&device);
+    return st == TOPK_OK ? launch_latent(p, dtype, device, stream) : st;
 }
 
 }  // namespace
@@ -216,31 +226,28 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
         !row_stride_ok(q_head_stride, 0) || !row_stride_ok(k_head_stride, 0) || !row_stride_ok(v_head_stride, 0))
         return TOPK_EINVAL;
     if (misaligned(q, 16) || misaligned(k_nope, 16) || misaligned(k_rope, 16) || misaligned(v, 16) ||
-        misaligned(out, 16) || misaligned(lse_or_null, 4) || misaligned(cu_q, 4) || misaligned(cu_k, 4) ||
+        misaligned(out, 32) || misaligned(lse_or_null, 4) || misaligned(cu_q, 4) || misaligned(cu_k, 4) ||
         q_token_stride % 8 || q_head_stride % 8 || k_token_stride % 8 || k_head_stride % 8 || k_rope_stride % 8 ||
         v_token_stride % 8 || v_head_stride % 8)
         return TOPK_EALIGN;
-    const topk_status_t dev = api_check_device();
-    if (dev != TOPK_OK) return dev;
+    AttendDevice device;
+    const topk_status_t st = attend_device(&device);
+    if (st != TOPK_OK) return st;
     if (total_q == 0) return TOPK_OK;
     PromptParams p = {q,      q_token_stride, q_head_stride, k_nope, k_token_stride, k_head_stride, k_rope,
                       k_rope_stride, v,       v_token_stride, v_head_stride, cu_q,   cu_k,          batch,
                       total_q, total_k, heads, scale,        causal, out,            lse_or_null};
-    uint32_t* flags = nullptr;
-    const topk_status_t st = attend_flags(&flags);
-    return st == TOPK_OK ? launch_prompt(p, dtype, flags, reinterpret_cast<cudaStream_t>(stream)) : st;
+    return launch_prompt(p, dtype, device, reinterpret_cast<cudaStream_t>(stream));
 }
 
 topk_status_t topk_read_attend_flags(uint32_t* flags_host, int32_t clear, topk_stream_t stream) {
     if (!flags_host) return TOPK_EINVAL;
-    const topk_status_t dev = api_check_device();
-    if (dev != TOPK_OK) return dev;
-    uint32_t* flags = nullptr;
-    const topk_status_t st = attend_flags(&flags);
+    AttendDevice device;
+    const topk_status_t st = attend_device(&device);
     if (st != TOPK_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemcpyAsync(flags_host, flags, sizeof(uint32_t), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess && clear) e = cudaMemsetAsync(flags, 0, sizeof(uint32_t), s);
+    cudaError_t e = cudaMemcpyAsync(flags_host, device.flags, sizeof(uint32_t), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess && clear) e = cudaMemsetAsync(device.flags, 0, sizeof(uint32_t), s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "attention flags");
 }

@@ -2,6 +2,7 @@
 // attention kernels, shared by the host side of the ABI (attend_api.cu).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -20,6 +21,24 @@ constexpr int kValue = TOPK_VALUE_DIM;
 // The ABI's device check and CUDA-error record (topkidx_api.cu).
 topk_status_t api_check_device();
 topk_status_t api_cuda_fail(cudaError_t e, const char* where);
+
+// The current device, as the attention launches need it.
+struct AttendDevice {
+    static constexpr int kMax = 64;
+    int index = 0;
+    int sms = 0;
+    uint32_t* flags = nullptr;  // where a wait that gave up is noted
+};
+
+// Lets a kernel take `bytes` of shared memory, once per kernel and device
+// (`done`; a second thread that comes in between sets the same value).
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<bool>& done) {
+    if (done.load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.store(true, std::memory_order_release);
+    return e;
+}
 
 struct TablesParams {
     const int32_t* context;
@@ -79,7 +98,7 @@ struct LatentParams {
     void* workspace;
 };
 size_t latent_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
-topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream);
+topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
 
 struct PromptParams {
     const void* q;
@@ -98,6 +117,6 @@ struct PromptParams {
     void* out;
     float* lse;  // or null
 };
-topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream);
+topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
 
 }  // namespace topkidx

@@ -39,6 +39,7 @@
 // tells of what landed, 10 queries, 11 rows to L2 ahead of their copies.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -98,12 +99,15 @@ __device__ __forceinline__ int length_of(const LatentParams& p, int b) {
 __device__ __forceinline__ int tiles_of(int length) { return max((length + kTile - 1) / kTile, 1); }
 __device__ __forceinline__ int groups_of(const LatentParams& p) { return (p.queries * p.heads + kRows - 1) / kRows; }
 
-// Run of pair i of n: [total i / n, total (i + 1) / n).
-__device__ __forceinline__ int64_t run_start(int64_t total, int i, int n) { return total * i / n; }
+// Run of pair i of n: [total i / n, total (i + 1) / n); with fewer tiles than
+// pairs the first `total` pairs have one each.
+__device__ __forceinline__ int64_t run_start(int64_t total, int i, int n) {
+    return total < n ? min(static_cast<int64_t>(i), total) : total * i / n;
+}
 
 // All threads of a block: the tiles of the whole batch, and the row of the
 // batch in which tile `run_start(total, pair, pairs)` lies, with the tile's
-// number from that row's first.
+// number from that row's first (the last tile for a pair without a run).
 __device__ void locate(const LatentParams& p, int pair, int pairs, int64_t* scan, int64_t* total_out, int64_t* begin_out,
                        int32_t* row_out, int32_t* tile_out) {
     const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -112,10 +116,11 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, int64_t* scan
         const int64_t each = static_cast<int64_t>(tiles_of(p.max_len)) * groups;
         if (tid == 0) {
             const int64_t total = each * p.batch, begin = run_start(total, pair, pairs);
+            const int64_t at = min(begin, total - 1);
             *total_out = total;
             *begin_out = begin;
-            *row_out = static_cast<int32_t>(begin / each);
-            *tile_out = static_cast<int32_t>(begin % each);
+            *row_out = static_cast<int32_t>(at / each);
+            *tile_out = static_cast<int32_t>(at % each);
         }
         __syncthreads();
         return;
@@ -139,19 +144,20 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, int64_t* scan
     }
     before += upto - mine;
     const int64_t begin = run_start(total, pair, pairs);
-    if (begin >= before && begin < before + mine) {
+    const int64_t tile = min(begin, total - 1);
+    if (tile >= before && tile < before + mine) {
         int64_t at = before;
         int b = from;
         while (true) {
             const int64_t n = static_cast<int64_t>(tiles_of(length_of(p, b))) * groups;
-            if (begin < at + n) break;
+            if (tile < at + n) break;
             at += n;
             ++b;
         }
         *total_out = total;
         *begin_out = begin;
         *row_out = b;
-        *tile_out = static_cast<int32_t>(begin - at);
+        *tile_out = static_cast<int32_t>(tile - at);
     }
     __syncthreads();
 }
@@ -204,10 +210,22 @@ __device__ __forceinline__ int slot_of(const LatentParams& p, int row, int lengt
     return s >= 0 && s < p.num_slots ? static_cast<int>(s) : -1;
 }
 
-// Partial sums in the workspace, two places a pair: 0 for a row begun by an
-// earlier pair, 1 for a row begun by this pair and finished by a later one.
-__device__ __forceinline__ float* part_sums(const LatentParams& p, int rows, int place) {
-    return static_cast<float*>(p.workspace) + static_cast<int64_t>(place) * rows * (kLatent + 2);
+// Workspace: what each pair but the first has to join (see Join), then partial
+// sums, two places a pair: 0 for a row begun by an earlier pair, 1 for a row
+// begun by this pair and finished by a later one.  A place holds the sums as
+// [512 / 4][rows] float4, then (maximum, sum) by row: threads hold a row each,
+// so neighbouring threads write and read neighbouring addresses.
+struct alignas(16) Join {
+    int32_t parts;  // parts of the group of rows in which this pair's run is the first to begin, 0: none
+    int32_t rows;   // rows of the group
+    int64_t at;     // first (query, head) row of the group
+};
+constexpr size_t kJoinBytes = kMaxPairs * sizeof(Join);
+static_assert(kJoinBytes % 16 == 0, "partial sums are aligned");
+
+__device__ __forceinline__ float* part_of(const LatentParams& p, int rows, int place) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kJoinBytes) +
+           static_cast<int64_t>(place) * rows * (kLatent + 2);
 }
 
 template <bool kBf16, bool kPaged>
@@ -253,6 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
     const tc::Waits wait{&sh.gave_up};
+    ptx::launch_dependents();
     Walk walk(p, sh, pair, pairs);
     Segment s;
 
@@ -427,6 +446,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (n > 0 && wait.over())
             for (int g = 0; g < 2; ++g) tc::Waits::drain(&sh.value_landed[g], (n - 1) & 1);
     } else if (warp == kQueryWarp) {
+        if (lane == 0 && rank == 0 && pair > 0) {
+            const int tiles = tiles_of(length_of(p, walk.row)), all = p.queries * p.heads;
+            const int64_t start = sh.begin - walk.first;  // of the group's tiles
+            Join join = {};
+            if (walk.left > 0 && walk.first > 0 && run_start(sh.total, pair - 1, pairs) <= start) {
+                // Runs that begin before the group's end, and the one before this.
+                const int64_t last = sh.total < pairs ? start + tiles - 1 : ((start + tiles) * pairs - 1) / sh.total;
+                join.parts = static_cast<int32_t>(last) - pair + 2;
+                join.rows = min(all - walk.group * kRows, kRows);
+                join.at = static_cast<int64_t>(walk.row) * all + walk.group * kRows;
+            }
+            static_cast<Join*>(p.workspace)[pair] = join;
+        }
         if (lane == 0) {
             const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
             for (int n = 0; walk.next(s); ++n) {
@@ -689,18 +721,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const bool whole = s.first == 0 && s.last == s.tiles;
             const int64_t at = static_cast<int64_t>(s.row) * all + m_row;
-            float* part = nullptr;
-            if (!whole) {
-                part = part_sums(p, part_rows, 2 * pair + (s.first == 0 ? 1 : 0));
-                if (half == 0 && m_row < all) {
-                    float* stats = part + static_cast<int64_t>(part_rows) * kLatent + 2 * (m_row - s.group * kRows);
-                    stats[0] = m;
-                    stats[1] = l;
-                }
-                part += static_cast<int64_t>(m_row - s.group * kRows) * kLatent + 256 * half;
-            }
+            const int r_part = m_row - s.group * kRows;
+            float* part = whole ? nullptr : part_of(p, part_rows, 2 * pair + (s.first == 0 ? 1 : 0));
+            if (!whole && half == 0 && m_row < all)
+                reinterpret_cast<float2*>(part + static_cast<int64_t>(part_rows) * kLatent)[r_part] = make_float2(m, l);
             const float by = l == 0.f ? 0.f : 1.f / l;
-            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kLatent + 256 * half);
+            uint16_t* out = static_cast<uint16_t*>(p.out) + at * kLatent + 256 * half;
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
                 uint32_t o[32];
@@ -708,21 +734,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::wait_load();
                 if (m_row < all && whole) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float a = __uint_as_float(o[8 * i + 2 * k]) * by,
-                                        b = __uint_as_float(o[8 * i + 2 * k + 1]) * by;
+                        for (int k = 0; k < 8; ++k) {
+                            const float a = __uint_as_float(o[16 * i + 2 * k]) * by,
+                                        b = __uint_as_float(o[16 * i + 2 * k + 1]) * by;
                             w[k] = l == 0.f ? 0u : tc::pack<kBf16>(a, b);
                         }
-                        out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        tc::store_v8(out + 32 * c + 16 * i, w);
                     }
                 } else if (m_row < all) {
+                    uint4* to = reinterpret_cast<uint4*>(part) + static_cast<int64_t>(64 * half + 8 * c) * part_rows + r_part;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<uint4*>(part + 32 * c)[i] =
-                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        to[i * part_rows] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
                 __syncwarp();
             }
@@ -742,48 +768,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && sh.gave_up) atomicOr(flags, TOPK_FLAG_TIMEOUT);
 }
 
-// Joins the rows that several pairs shared: block (i, j) the first four..
-// values' share j of the row in which the run of pair i + 1 begins, if that
-// run is the first to begin inside it.
+// Joins the rows that several pairs shared: block (i, j) those of pair i + 1's
+// Join, 16 values of 32 rows by each warp, a row a lane.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinRows = 4;
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentParams p, int pairs) {
-    __shared__ int64_t scan[kJoinThreads / 32], total, begin;
-    __shared__ int32_t row, tile;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentParams p) {
     const int pair = static_cast<int>(blockIdx.x) + 1;
-    locate(p, pair, pairs, scan, &total, &begin, &row, &tile);
-    const int tiles = tiles_of(length_of(p, row));
-    const int group = tile / tiles, first = tile % tiles;
-    const int64_t start = begin - first, end = start + tiles;  // of the group's tiles
-    if (first == 0 || run_start(total, pair - 1, pairs) > start) return;
-    const int all = p.queries * p.heads, part_rows = min(all, kRows);
-    // Pairs pair - 1 .. last hold a part each, those with an empty run none.
-    int last = pair;
-    while (last + 1 < pairs && run_start(total, last + 1, pairs) < end) ++last;
+    ptx::grid_dependency_wait();
+    const Join join = static_cast<const Join*>(p.workspace)[pair];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = static_cast<int>(blockIdx.y) * kJoinRows + warp;
-    const int m_row = group * kRows + r;
-    if (r >= part_rows || m_row >= all) return;
-    const auto place = [&](int i) { return 2 * i + (i == pair - 1 ? 1 : 0); };
-    float m = -INFINITY, l = 0.f, o[kLatent / 32] = {};
-    const auto none = [&](int i) { return run_start(total, i, pairs) == run_start(total, i + 1, pairs); };
-    for (int i = pair - 1; i <= last; ++i) {
-        if (none(i)) continue;
-        m = fmaxf(m, part_sums(p, part_rows, place(i))[static_cast<int64_t>(part_rows) * kLatent + 2 * r]);
-    }
-    for (int i = pair - 1; i <= last; ++i) {
-        if (none(i)) continue;
-        const float* part = part_sums(p, part_rows, place(i));
-        const float* stats = part + static_cast<int64_t>(part_rows) * kLatent + 2 * r;
-        if (stats[1] == 0.f) continue;
-        const float by = exp2f(stats[0] - (m == -INFINITY ? 0.f : m));
-        l += stats[1] * by;
-        const float4* from = reinterpret_cast<const float4*>(part + static_cast<int64_t>(r) * kLatent);
+    const int r = static_cast<int>(blockIdx.y >> 3) * 32 + lane;
+    const int c0 = 4 * (static_cast<int>(blockIdx.y & 7) * (kJoinThreads / 32) + warp);  // float4 columns
+    if (r >= join.rows || join.parts == 0) return;
+    const int part_rows = min(p.queries * p.heads, kRows);
+    const auto stats_of = [&](int i) {
+        const float* part = part_of(p, part_rows, 2 * (pair - 1 + i) + (i == 0 ? 1 : 0));
+        return reinterpret_cast<const float2*>(part + static_cast<int64_t>(part_rows) * kLatent)[r];
+    };
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < join.parts; ++i) m = fmaxf(m, stats_of(i).x);
+    if (m == -INFINITY) m = 0.f;
+    float l = 0.f, o[16] = {};
+#pragma unroll 4
+    for (int i = 0; i < join.parts; ++i) {
+        const float2 stats = stats_of(i);
+        const float4* from = reinterpret_cast<const float4*>(part_of(p, part_rows, 2 * (pair - 1 + i) + (i == 0 ? 1 : 0))) +
+                             static_cast<int64_t>(c0) * part_rows + r;
+        // A part that saw nothing has no sums.
+        const float by = stats.y == 0.f ? 0.f : exp2f(stats.x - m);
+        l += stats.y * by;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 x = from[32 * c + lane];
+            const float4 x = from[c * part_rows];
             o[4 * c] += x.x * by;
             o[4 * c + 1] += x.y * by;
             o[4 * c + 2] += x.z * by;
@@ -791,39 +809,31 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentParams p
         }
     }
     const float by = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = static_cast<int64_t>(row) * all + m_row;
-    uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * kLatent);
+    uint32_t w[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        out[32 * c + lane] = make_uint2(tc::pack<kBf16>(o[4 * c] * by, o[4 * c + 1] * by),
-                                        tc::pack<kBf16>(o[4 * c + 2] * by, o[4 * c + 3] * by));
-    if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-}
-
-int pairs_of_device() {
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int n = sms / 2;
-    return n < 1 ? 1 : n > kMaxPairs ? kMaxPairs : n;
+    for (int i = 0; i < 8; ++i) w[i] = tc::pack<kBf16>(o[2 * i] * by, o[2 * i + 1] * by);
+    const int64_t at = join.at + r;
+    tc::store_v8(static_cast<uint16_t*>(p.out) + at * kLatent + 4 * c0, w);
+    if (p.lse && c0 == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace
 
 size_t latent_workspace_bytes(int32_t, int32_t queries, int32_t heads) {
     const int64_t all = static_cast<int64_t>(queries) * heads;
-    return static_cast<size_t>(2 * kMaxPairs) * static_cast<size_t>(all < kRows ? all : kRows) * (kLatent + 2) *
-           sizeof(float);
+    return kJoinBytes + static_cast<size_t>(2 * kMaxPairs) * static_cast<size_t>(all < kRows ? all : kRows) *
+                            (kLatent + 2) * sizeof(float);
 }
 
-topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream) {
+topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream) {
     const bool bf16 = dtype == TOPK_BF16;
     LatentMaps maps;
     // Query rows: one dimension of (query, head) where those have one stride,
     // copied 64 rows at a time; else one row at a time.
     const bool whole_rows = p.queries == 1 || p.heads == 1 || p.q_query_stride == p.heads * p.q_head_stride;
     const int64_t any = 2 * kWidth;  // stride of a dimension of one entry
-    const int64_t rows = whole_rows ? static_cast<int64_t>(p.queries) * p.heads : p.heads;
+    const int64_t all = static_cast<int64_t>(p.queries) * p.heads;
+    const int64_t rows = whole_rows ? all : p.heads;
     const int64_t row_step = whole_rows && p.heads == 1 ? p.q_query_stride : p.q_head_stride;
     const int64_t q_dims[4] = {kWidth, rows, whole_rows ? 1 : p.queries, p.batch};
     const int64_t q_steps[3] = {rows > 1 ? 2 * row_step : any, whole_rows ? any : 2 * p.q_query_stride,
@@ -838,23 +848,30 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, uint32_t*
 
     const auto kernel = paged ? (bf16 ? latent_kernel<true, true> : latent_kernel<false, true>)
                               : (bf16 ? latent_kernel<true, false> : latent_kernel<false, false>);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<bool> prepared[4][AttendDevice::kMax];
+    cudaError_t e = allow_shared(kernel, kSmem, prepared[2 * paged + bf16][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention shared memory");
-    const int64_t groups = (static_cast<int64_t>(p.queries) * p.heads + kRows - 1) / kRows;
+    const int64_t groups = (all + kRows - 1) / kRows;
     const int64_t tiles = p.batch * groups * (p.max_len > kTile ? (p.max_len + int64_t{kTile} - 1) / kTile : 1);
-    const int device = pairs_of_device();
-    const int pairs = tiles < device ? static_cast<int>(tiles) : device;
+    const int64_t most = device.sms / 2 < kMaxPairs ? device.sms / 2 : kMaxPairs;
+    const int pairs = static_cast<int>(tiles < most ? tiles : most);
     const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
-    kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps, flags, scale_log2, p.scale < 0.f, whole_rows,
+    kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps, device.flags, scale_log2, p.scale < 0.f, whole_rows,
                                                   box_rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
     if (pairs > 1) {
-        const int64_t all = static_cast<int64_t>(p.queries) * p.heads;
-        const int part_rows = static_cast<int>(all < kRows ? all : kRows);
-        const dim3 grid(static_cast<unsigned>(pairs - 1), static_cast<unsigned>((part_rows + kJoinRows - 1) / kJoinRows));
-        (bf16 ? join_kernel<true> : join_kernel<false>)<<<grid, kJoinThreads, 0, stream>>>(p, pairs);
-        e = cudaGetLastError();
+        // Placed while the first kernel runs.
+        cudaLaunchAttribute attr = {};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(pairs - 1), 8 * static_cast<unsigned>(((all < kRows ? all : kRows) + 31) / 32));
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, bf16 ? join_kernel<true> : join_kernel<false>, p);
         if (e != cudaSuccess) return api_cuda_fail(e, "latent attention join launch");
     }
     return TOPK_OK;

@@ -21,6 +21,7 @@
 // 9 copies.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, uint32_t* flags, cudaStream_t stream) {
+topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream) {
     const bool bf16 = dtype == TOPK_BF16;
     PromptMaps maps;
     const auto map3 = [&](CUtensorMap* m, const void* base, int64_t width, int64_t head_stride, int64_t tokens,
@@ -391,7 +392,8 @@ topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, uint32_t*
     if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "prompt attention tensor map");
 
     const auto kernel = bf16 ? prompt_kernel<true> : prompt_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<bool> prepared[2][AttendDevice::kMax];
+    cudaError_t e = allow_shared(kernel, kSmem, prepared[bf16][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "prompt attention shared memory");
     // Every request adds at most one block to total / 256.
     const unsigned grid = static_cast<unsigned>(p.heads) *
@@ -400,7 +402,7 @@ topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, uint32_t*
     // largest score is always the largest exponent.
     // A scale of zero becomes the least normal number: hidden scores stay -inf.
     const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
-    kernel<<<grid, kThreads, kSmem, stream>>>(p, maps, flags, scale_log2, p.scale < 0.f);
+    kernel<<<grid, kThreads, kSmem, stream>>>(p, maps, device.flags, scale_log2, p.scale < 0.f);
     e = cudaGetLastError();
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "prompt attention launch");
 }

@@ -202,6 +202,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 32 bytes, a whole sector (32-byte aligned).
+__device__ __forceinline__ void store_v8(void* to, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 // Two floats to two-byte values, `lo` in the low half.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
