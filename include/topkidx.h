@@ -324,7 +324,8 @@ size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads
  *                     (strides of at least 576 where there is more than one).
  *   cache             device [num_slots][slot_stride], 576 values used.
  *   indices           device int32[rows][indices_stride], k used per row.
- *   rows, heads, k    >= 1; rows * heads <= 2^30.
+ *   rows, heads, k    >= 1; rows * heads <= 2^30, and less than 2^31 tiles of
+ *                     64 slots by 128 heads in all.
  *   out               device [rows][heads][512], contiguous, 32-byte aligned.
  *   lse_or_null       device float[rows][heads].
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_ENOSPACE, TOPK_EDEVICE, TOPK_ECUDA.
