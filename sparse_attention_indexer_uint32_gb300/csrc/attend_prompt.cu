@@ -18,7 +18,8 @@
 // eight 16 KB pieces (three of keys and two of values per step).
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one query a thread), 8 products,
-// 9 copies.
+// 9 copies.  The second product starts on the first half of a step's weights
+// while the second half is being computed.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -49,7 +50,7 @@ struct PromptMaps {
 struct Barriers {
     uint64_t full[kRing], empty[kRing];
     uint64_t query[2];
-    uint64_t score[2], weight[2], sum[2];
+    uint64_t score[2], weight[2][2], sum[2];  // weights by tile and half of the step's keys
     uint64_t end;
     uint32_t tmem;
     uint32_t gave_up;
@@ -127,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t) {
                 ptx::mbar_init(&bar.query[t], 1);
                 ptx::mbar_init(&bar.score[t], 1);
-                ptx::mbar_init(&bar.weight[t], 4);
+                ptx::mbar_init(&bar.weight[t][0], 4);
+                ptx::mbar_init(&bar.weight[t][1], 4);
                 ptx::mbar_init(&bar.sum[t], 1);
             }
             ptx::mbar_init(&bar.end, 1);
@@ -200,24 +202,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
         const uint32_t score_instr = tc::instruction(kBf16, kTile, kTile, negate, false);
         const uint32_t sum_instr = tc::instruction(kBf16, kTile, kValue, false, true);
+        const uint64_t query_at = tc::operand(queries), key_at = tc::operand(ring), value_at = tc::operand(ring, kPiece / 2);
         const auto scores = [&](int t, int j) {
             if (j == 0) wait.warp(&bar.query[t], 0);
+#pragma unroll
             for (int c = 0; c < kKeyPieces; ++c) {
                 const int i = j * kStepPieces + c;
                 wait.warp(&bar.full[i % kRing], (i / kRing) & 1);
-                if (lane == 0) {
-                    const uint64_t a = tc::operand(queries + (3 * t + c) * kPiece);
-                    const uint64_t b = tc::operand(ring + (i % kRing) * kPiece);
+                if (tc::elect()) {
+                    const uint64_t a = query_at + (3 * t + c) * (kPiece >> 4), b = key_at + (i % kRing) * (kPiece >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma<1>(tmem + t * kTile, a + 2 * k, b + 2 * k, score_instr, (c | k) != 0);
+                    if (c == kKeyPieces - 1) tc::commit<1>(&bar.score[t]);
                 }
+                __syncwarp();
             }
-            if (lane == 0) tc::commit<1>(&bar.score[t]);
         };
         const auto release = [&](int from, int count) {
-            if (lane == 0)
+            if (tc::elect())
                 for (int i = from; i < from + count; ++i) tc::commit<1>(&bar.empty[i % kRing]);
+            __syncwarp();
         };
         for (int t = 0; t < 2; ++t)
             if (steps[t]) scores(t, 0);
@@ -239,16 +244,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int t = 0; t < 2; ++t) {
                 if (j < steps[t]) {
-                    wait.warp(&bar.weight[t], j & 1);
-                    tc::fence_after();
-                    if (lane == 0) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint64_t b = tc::operand(ring + ((vi + (k >> 2)) % kRing) * kPiece, kPiece / 2);
-                            tc::mma_tmem(tmem + 256 + t * kValue, tmem + t * kTile + 8 * k, b + 128 * (k & 3), sum_instr,
-                                         j > 0 || k > 0);
+                    for (int half = 0; half < 2; ++half) {
+                        wait.warp(&bar.weight[t][half], j & 1);
+                        tc::fence_after();
+                        if (tc::elect()) {
+                            const uint64_t b = value_at + ((vi + half) % kRing) * (kPiece >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_tmem(tmem + 256 + t * kValue, tmem + t * kTile + 32 * half + 8 * k, b + 128 * k,
+                                             sum_instr, j > 0 || half > 0 || k > 0);
+                            if (half == 1) tc::commit<1>(&bar.sum[t]);
                         }
-                        tc::commit<1>(&bar.sum[t]);
+                        __syncwarp();
                     }
                 }
                 if (t == 1) release(vi, 2);
@@ -256,12 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (j + 1 < n) release((j + 1) * kStepPieces, kKeyPieces);
         }
-        if (lane == 0) {
+        if (tc::elect()) {
             tc::commit<1>(&bar.end);
             tc::Waits::drain(&bar.end, 0);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         const int t = warp >> 2, row = threadIdx.x & 127;
         const int query = first + t * kTile + row;
         const int limit = query < q1 ? seen(query) : 0;
@@ -284,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
-            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale_log2;
+            for (int i = 0; i < kTile; i += 2) top[(i >> 1) & 3] = tc::max3(top[(i >> 1) & 3], s[i], s[i + 1]);
+            const float tile_top = tc::max3(fmaxf(top[0], top[1]), top[2], top[3]) * scale_log2;
             const bool raise = tile_top > m + kLag || (m == -INFINITY && tile_top > m);
             if (__any_sync(~0u, raise)) {
                 const float next = raise ? tile_top : m;
@@ -307,25 +315,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float shift = m == -INFINITY ? 0.f : -m;
-            float add[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 scale2 = make_float2(scale_log2, scale_log2), shift2 = make_float2(shift, shift);
+            float2 add[2] = {};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int half = 0; half < 2; ++half) {
                 uint32_t w[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float a = tc::exp2_approx(fmaf(s[64 * c + 2 * i], scale_log2, shift));
-                    const float b = tc::exp2_approx(fmaf(s[64 * c + 2 * i + 1], scale_log2, shift));
-                    add[(2 * i) & 3] += a;
-                    add[(2 * i + 1) & 3] += b;
-                    w[i] = tc::pack<kBf16>(a, b);
+                    float2 x = tc::fma2(make_float2(s[64 * half + 2 * i], s[64 * half + 2 * i + 1]), scale2, shift2);
+                    x = make_float2(tc::exp2_approx(x.x), tc::exp2_approx(x.y));
+                    add[i & 1] = tc::add2(add[i & 1], x);
+                    w[i] = tc::pack<kBf16>(x.x, x.y);
                 }
-                tc::store32(score + 32 * c, w);
+                tc::store32(score + 32 * half, w);
+                tc::wait_store();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar.weight[t][half]);
             }
-            l += (add[0] + add[1]) + (add[2] + add[3]);
-            tc::wait_store();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bar.weight[t]);
+            l += (add[0].x + add[0].y) + (add[1].x + add[1].y);
         }
         if (steps[t]) {
             wait.warp(&bar.sum[t], (steps[t] - 1) & 1);
@@ -333,24 +341,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float by = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = static_cast<int64_t>(query) * p.heads + head;
-        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * kValue);
+        uint16_t* out = static_cast<uint16_t*>(p.out) + at * kValue;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
+        for (int c = 0; c < 2; ++c) {
+            uint32_t o[64];
             if (steps[t]) {
-                tc::load32(sums + 32 * c, o);
+                tc::load32(sums + 64 * c, o);
+                tc::load32(sums + 64 * c + 32, o + 32);
                 tc::wait_load();
             }
             if (query < q1) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4];
+                    uint32_t w[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float a = __uint_as_float(o[8 * i + 2 * k]) * by, b = __uint_as_float(o[8 * i + 2 * k + 1]) * by;
+                    for (int k = 0; k < 8; ++k) {
+                        const float a = __uint_as_float(o[16 * i + 2 * k]) * by, b = __uint_as_float(o[16 * i + 2 * k + 1]) * by;
                         w[k] = l == 0.f ? 0u : tc::pack<kBf16>(a, b);
                     }
-                    out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    tc::store_v8(out + 64 * c + 16 * i, w);
                 }
             }
             __syncwarp();
