@@ -40,6 +40,25 @@ cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<bool>& done) {
     return e;
 }
 
+// Launches a kernel that may be placed before the kernel ahead of it in the
+// stream has ended; it waits (griddepcontrol.wait) before its first access.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream,
+                         const Args&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 struct TablesParams {
     const int32_t* context;
     const int32_t* fresh;

@@ -57,41 +57,29 @@ constexpr int kThreads = 384;
 constexpr int kQueryWarp = 10, kPrefetchWarp = 11;
 constexpr int kMaxPairs = 80;
 constexpr int kPieces = kWidth / 64;             // 9
-constexpr int kQueryPiece = kHalfRows * 128;     // 64 rows of 64 values
-constexpr int kQueryBytes = kPieces * kQueryPiece;
+constexpr int kQueryBytes = kPieces * kHalfRows * 128;
 constexpr uint32_t kColumns = 512;
 constexpr uint32_t kScore = 256;  // column of the two score tiles; the sums have 0..255
 constexpr float kLag = 8.f;
 
-// A step: pages are walked 128 slots at a time with one place in shared memory,
-// whose thirds (keys) and halves (values) are freed and filled by themselves;
-// selected slots 64 at a time with two places.  The products of 128 slots are
-// 12 % cheaper per slot (32.9 cycles for N = 128 against 25.8 for N = 64), but
-// copies by threads take longer to land than copies by the engine, which one
-// place does not hide (4770 cycles per 128 slots with it).
-template <bool kPaged>
-struct Step {
-    static constexpr int kTile = kPaged ? 128 : 64;
-    static constexpr int kHalf = kTile / 2;         // slots of each block in the first product, of each thread in the softmax
-    static constexpr int kPlaces = kPaged ? 1 : 2;
-    static constexpr int kKeyGroups = kPaged ? 3 : 1, kValueGroups = kPaged ? 2 : 1;
-    static constexpr int kGroupPieces = kPieces / kKeyGroups;
-    static constexpr int kKeyPiece = kHalf * 128;   // a block's slots of 64 values
-    static constexpr int kValuePiece = kTile * 128; // all slots of 64 values
-    static constexpr int kKeyBytes = kPieces * kKeyPiece;
-    static constexpr int kValueBytes = 4 * kValuePiece;
-    static constexpr int kWeightBytes = kHalfRows * kTile * 2;
-    static constexpr int kWeightPiece = kHalfRows * 128;  // 64 rows of 64 weights
-    static constexpr int kLeast = kPaged ? 1 : 2;   // tiles of a run: a part of a row costs 256 KB written and read
-};
-constexpr int kMaxPlaces = 2;
+// A step is 128 slots (N = 128: 32.9 cycles a product, N = 64: 25.8).  Shared
+// memory has one place for it, which is freed and filled in parts: the keys by
+// thirds of the 576 values, the values by halves of the slots.
+constexpr int kTile = 128;
+constexpr int kHalf = kTile / 2;  // slots of each block in the first product, of each thread in the softmax
+constexpr int kKeyGroups = 3, kGroupPieces = kPieces / kKeyGroups;
+constexpr int kValueGroups = 2;
+constexpr int kKeyPiece = kHalf * 128;     // a block's slots of 64 values
+constexpr int kValuePiece = kTile * 128;   // all slots of 64 values
+constexpr int kWeightPiece = kHalfRows * 128;  // 64 rows of 64 weights
+constexpr int kKeyBytes = kPieces * kKeyPiece, kValueBytes = 4 * kValuePiece, kWeightBytes = 2 * kWeightPiece;
 
 struct Shared {
-    uint64_t query_full, query_empty;
+    uint64_t query_full[2], query_empty[2];
     // landed: in this block; full: in both (used in the first block).
-    uint64_t key_landed[3], key_full[3], key_empty[3];  // by place or by group
-    uint64_t value_landed[2], value_full[2], value_empty[2];
-    uint64_t score[2], weight[kMaxPlaces], sum[kMaxPlaces], end;
+    uint64_t key_landed[kKeyGroups], key_full[kKeyGroups], key_empty[kKeyGroups];
+    uint64_t value_landed[kValueGroups], value_full[kValueGroups], value_empty[kValueGroups];
+    uint64_t score[2], weight, sum, end;
     uint64_t mask_full[4];
     uint32_t mask[4][4];
     float exchange[2][kRows];
@@ -102,7 +90,7 @@ struct Shared {
     int32_t row, tile, length;  // where that lies: row of the batch, tile in the row, the row's length
     int32_t scan[kThreads / 32];
 };
-constexpr int kSmem = kQueryBytes + 9 * 8192 + 4 * 16384 + 16384 + 1024 + 2048;
+constexpr int kSmem = kQueryBytes + kKeyBytes + kValueBytes + kWeightBytes + 1024 + 2048;
 static_assert(sizeof(Shared) <= 2048, "barriers fit");
 static_assert(kSmem <= 232448, "shared memory of a block");
 
@@ -114,20 +102,18 @@ __device__ __forceinline__ int length_of(const LatentParams& p, int b) {
     return p.seq_lens ? min(max(p.seq_lens[b], 0), p.max_len) : p.max_len;
 }
 // Tiles of one group of 128 rows; an empty row has one, all of it hidden.
-template <bool kPaged>
 __device__ __forceinline__ int tiles_of(int length) {
-    return max(static_cast<int>((static_cast<uint32_t>(length) + Step<kPaged>::kTile - 1) / Step<kPaged>::kTile), 1);
+    return max(static_cast<int>((static_cast<uint32_t>(length) + kTile - 1) / kTile), 1);
 }
 __device__ __forceinline__ int groups_of(const LatentParams& p) { return (p.queries * p.heads + kRows - 1) / kRows; }
 
 // The runs of n pairs over all tiles (both below 2^31), as even as can be: the
-// first `more` pairs have one tile more than the others.  Runs are not shorter
-// than `least` tiles while there are fewer than n of that length: the pairs past
-// `used` have none.
+// first `more` pairs have one tile more than the others.  With fewer tiles than
+// pairs the last pairs, past `used`, have none.
 struct Runs {
     int each, more, used;
-    __device__ __forceinline__ Runs(int total, int n, int least) {
-        used = min(n, max(total / least, 1));
+    __device__ __forceinline__ Runs(int total, int n) {
+        used = min(n, total);
         each = total / used;
         more = total % used;
     }
@@ -142,14 +128,13 @@ struct Runs {
 
 // All threads of a block: the tiles of the whole batch, and where the run of
 // `pair` begins (for a pair without one: at the last tile).
-template <bool kPaged>
 __device__ void locate(const LatentParams& p, int pair, int pairs, Shared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int groups = groups_of(p);
     if (!p.seq_lens) {
         if (tid == 0) {
-            const int each = tiles_of<kPaged>(p.max_len) * groups, total = each * p.batch;
-            const int begin = Runs(total, pairs, Step<kPaged>::kLeast).start(pair), at = min(begin, total - 1);
+            const int each = tiles_of(p.max_len) * groups, total = each * p.batch;
+            const int begin = Runs(total, pairs).start(pair), at = min(begin, total - 1);
             sh.total = total;
             sh.begin = begin;
             sh.row = at / each;
@@ -163,7 +148,7 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, Shared& sh) {
     const int from = min(tid * per, p.batch), to = min(from + per, p.batch);
     int mine = 0;
 #pragma unroll 4
-    for (int b = from; b < to; ++b) mine += tiles_of<kPaged>(length_of(p, b));
+    for (int b = from; b < to; ++b) mine += tiles_of(length_of(p, b));
     mine *= groups;
     int upto = mine;
 #pragma unroll
@@ -181,12 +166,12 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, Shared& sh) {
         total += x;
     }
     before += upto - mine;
-    const int begin = Runs(total, pairs, Step<kPaged>::kLeast).start(pair), tile = min(begin, total - 1);
+    const int begin = Runs(total, pairs).start(pair), tile = min(begin, total - 1);
     if (tile >= before && tile < before + mine) {
         int at = before, b = from, length = 0;
         while (true) {
             length = length_of(p, b);
-            const int n = tiles_of<kPaged>(length) * groups;
+            const int n = tiles_of(length) * groups;
             if (tile < at + n) break;
             at += n;
             ++b;
@@ -204,14 +189,13 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, Shared& sh) {
 struct Segment {
     int row, group, first, last, tiles, length;
 };
-template <bool kPaged>
 struct Walk {
     const LatentParams& p;
     int left, row, group, first, groups, length;
 
     __device__ __forceinline__ Walk(const LatentParams& p, const Shared& sh, int pair, int pairs)
-        : p(p), left(Runs(sh.total, pairs, Step<kPaged>::kLeast).count(pair)), row(sh.row), groups(groups_of(p)), length(sh.length) {
-        const int tiles = tiles_of<kPaged>(length);
+        : p(p), left(Runs(sh.total, pairs).count(pair)), row(sh.row), groups(groups_of(p)), length(sh.length) {
+        const int tiles = tiles_of(length);
         group = sh.tile / tiles;
         first = sh.tile - group * tiles;
     }
@@ -220,7 +204,7 @@ struct Walk {
         s.row = row;
         s.group = group;
         s.length = length;
-        s.tiles = tiles_of<kPaged>(length);
+        s.tiles = tiles_of(length);
         s.first = first;
         s.last = min(s.tiles, first + left);
         left -= s.last - s.first;
@@ -248,6 +232,38 @@ __device__ __forceinline__ int slot_of(const LatentParams& p, int row, int lengt
                       (pos & ((1 << p.log2_page) - 1));
     return s >= 0 && s < p.num_slots ? static_cast<int>(s) : -1;
 }
+
+// One slot a tile of a run, fetched two tiles ahead of its use: loads wait
+// behind the copies that are under way.
+struct SlotAhead {
+    const LatentParams& p;
+    Walk& walk;
+    Segment& s;
+    int at, tiles, tile, slot[2];
+    bool more;
+
+    __device__ __forceinline__ SlotAhead(const LatentParams& p, Walk& walk, Segment& s, int at)
+        : p(p), walk(walk), s(s), at(at), tiles(walk.left), more(walk.next(s)) {
+        tile = s.first;
+        slot[0] = fetch();
+        slot[1] = fetch();
+    }
+    __device__ __forceinline__ int fetch() {
+        if (!more) return -1;
+        const int x = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at);
+        if (++tile == s.last) {
+            more = walk.next(s);
+            tile = s.first;
+        }
+        return x;
+    }
+    __device__ __forceinline__ int next() {
+        const int x = slot[0];
+        slot[0] = slot[1];
+        slot[1] = fetch();
+        return x;
+    }
+};
 
 // Workspace: what each pair but the first has to join (see Join), then partial
 // sums, two places a pair: 0 for a row begun by an earlier pair, 1 for a row
@@ -277,22 +293,23 @@ template <bool kBf16, bool kPaged>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_kernel(const LatentParams p, const __grid_constant__ LatentMaps maps, uint32_t* flags, float scale_log2,
                   bool negate, bool whole_rows, int box_rows) {
-    using S = Step<kPaged>;
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
-    const uint32_t queries = base, keys = queries + kQueryBytes, values = keys + S::kPlaces * S::kKeyBytes,
-                   weights = values + S::kPlaces * S::kValueBytes;
-    Shared& sh = *reinterpret_cast<Shared*>(raw + (weights + S::kPlaces * S::kWeightBytes - ptx::smem_addr(raw)));
+    const uint32_t queries = base, keys = queries + kQueryBytes, values = keys + kKeyBytes,
+                   weights = values + kValueBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(raw + (weights + kWeightBytes - ptx::smem_addr(raw)));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(ptx::cluster_ctarank());
     const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    // Up to 64 rows: 32 a block, two places for queries, and half of the
+    // softmax warps.
+    const bool few = p.queries * p.heads <= kHalfRows;
+    const int block_rows = few ? kHalfRows / 2 : kHalfRows, query_piece = block_rows * 128;
 
     if (threadIdx.x == 0) {
         sh.gave_up = 0;
         sh.copied = 0;
-        ptx::mbar_init(&sh.query_full, 1);
-        ptx::mbar_init(&sh.query_empty, 1);
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kKeyGroups; ++i) {
             ptx::mbar_init(&sh.key_landed[i], kPaged ? 1 : 64);
             ptx::mbar_init(&sh.key_full[i], 2);
             ptx::mbar_init(&sh.key_empty[i], 1);
@@ -302,15 +319,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh.value_full[i], 2);
             ptx::mbar_init(&sh.value_empty[i], 1);
             ptx::mbar_init(&sh.score[i], 1);
-            ptx::mbar_init(&sh.weight[i], 8);
-            ptx::mbar_init(&sh.sum[i], 1);
+            ptx::mbar_init(&sh.query_full[i], 1);
+            ptx::mbar_init(&sh.query_empty[i], 1);
         }
+        ptx::mbar_init(&sh.weight, few ? 4 : 8);
+        ptx::mbar_init(&sh.sum, 1);
         ptx::mbar_init(&sh.end, 1);
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh.mask_full[i], kPaged ? 1 : 2);
         ptx::fence_mbarrier_init();
     }
     if (warp == 4) tc::alloc<2>(ptx::smem_addr(&sh.tmem), kColumns);
-    locate<kPaged>(p, pair, pairs, sh);
+    ptx::grid_dependency_wait();
+    locate(p, pair, pairs, sh);
     // Both blocks' barriers and tensor memory are ready from the wait on; the
     // first slots are fetched before it.
     tc::fence_before();
@@ -323,84 +343,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     const uint32_t tmem = sh.tmem;
     const tc::Waits wait{&sh.gave_up};
-    Walk<kPaged> walk(p, sh, pair, pairs);
+    Walk walk(p, sh, pair, pairs);
     Segment s = {};
 
     if (!kPaged && (warp == 5 || warp == 8)) {
-        // Selected slots, first product: 16 of the block's 32 slots of each
+        // Selected slots, first product: 32 of the block's 64 slots of each
         // tile, all values; 16 bytes a lane, four rows at a time.
         const int part = warp == 8 ? 1 : 0, r = lane >> 3;
-        const int at = rank * S::kHalf + 16 * part + (lane & 15);
-        int n = 0;
-        bool more = walk.next(s);
-        int tile = s.first;
-        int next_slot = more ? slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * S::kTile + at) : -1;
+        SlotAhead ahead(p, walk, s, rank * kHalf + 32 * part + lane);
+        const int tiles = ahead.tiles;
         pair_ready();
-        while (more && !wait.over()) {
-            const int slot = next_slot;
-            // The next tile's slots are fetched while this one's copies wait.
-            if (++tile == s.last) {
-                more = walk.next(s);
-                tile = s.first;
-            }
-            if (more) next_slot = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * S::kTile + at);
-            const int place = n & 1;
-            if (n >= 2) wait.warp(&sh.key_empty[place], ((n >> 1) - 1) & 1);
-            const uint32_t to = keys + place * S::kKeyBytes + part * 2048 + r * 128;
-            const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int x = __shfl_sync(~0u, slot, 4 * q + r);
-                const uint8_t* from = static_cast<const uint8_t*>(p.cache) + max(x, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
-#pragma unroll
-                for (int c = 0; c < kPieces; ++c)
-                    tc::copy16((q & 1 ? odd : even) + q * 512 + c * S::kKeyPiece, from + 128 * c, x >= 0 ? 16 : 0);
-            }
-            tc::copy16_arrive(&sh.key_landed[place]);
-            ++n;
-            if (part == 0 && lane == 0) sh.copied = n;
-        }
-        tc::copy16_drain();
-    } else if (!kPaged && (warp == 6 || warp == 9)) {
-        // Selected slots, second product: 32 of each tile's 64 slots, values
-        // 256 rank...
-        const int part = warp == 9 ? 1 : 0, r = lane >> 3;
-        int n = 0;
-        bool more = walk.next(s);
-        int tile = s.first;
-        const int at = 32 * part + lane;
-        int next_slot = more ? slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * S::kTile + at) : -1;
-        pair_ready();
-        while (more && !wait.over()) {
-            const int slot = next_slot;
-            if (++tile == s.last) {
-                more = walk.next(s);
-                tile = s.first;
-            }
-            if (more) next_slot = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * S::kTile + at);
-            // One bit a slot that is seen.  Place n % 4 was last read for tile
-            // n - 4; the copies of tile n - 1 waited for the second product of
-            // tile n - 3.
-            const uint32_t bits = __ballot_sync(~0u, slot >= 0);
-            if (lane == 0) {
-                sh.mask[n & 3][part] = bits;
-                ptx::mbar_arrive(&sh.mask_full[n & 3]);
-            }
-            const int place = n & 1;
-            if (n >= 2) wait.warp(&sh.value_empty[place], ((n >> 1) - 1) & 1);
-            const uint32_t to = values + place * S::kValueBytes + part * 4096 + r * 128;
-            const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
-            const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + (lane & 7) * 16;
+        for (int n = 0; n < tiles && !wait.over(); ++n) {
+            const int slot = ahead.next();
+            const uint8_t* from[8];
+            uint32_t seen = 0;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const int x = __shfl_sync(~0u, slot, 4 * q + r);
-                const uint8_t* from = cache + max(x, 0) * (2 * p.slot_stride);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc::copy16((q & 1 ? odd : even) + q * 512 + c * S::kValuePiece, from + 128 * c, x >= 0 ? 16 : 0);
+                seen |= (x >= 0 ? 1u : 0u) << q;
+                from[q] = static_cast<const uint8_t*>(p.cache) + max(x, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
             }
-            tc::copy16_arrive(&sh.value_landed[place]);
-            ++n;
+            for (int g = 0; g < kKeyGroups; ++g) {
+                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
+                const uint32_t to = keys + kGroupPieces * g * kKeyPiece + part * 4096 + r * 128;
+                const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int c = 0; c < kGroupPieces; ++c)
+                        tc::copy16((q & 1 ? odd : even) + q * 512 + c * kKeyPiece, from[q] + 128 * (kGroupPieces * g + c),
+                                   ((seen >> q) & 1) * 16);
+                tc::copy16_arrive(&sh.key_landed[g]);
+            }
+            if (part == 0 && lane == 0) sh.copied = n + 1;
+        }
+        tc::copy16_drain();
+    } else if (!kPaged && (warp == 6 || warp == 9)) {
+        // Selected slots, second product: 32 of each half of the tile's
+        // slots, values 256 rank...
+        const int part = warp == 9 ? 1 : 0, r = lane >> 3;
+        Walk walk2 = walk;
+        Segment s2 = {};
+        SlotAhead ahead[kValueGroups] = {SlotAhead(p, walk, s, 32 * part + lane), SlotAhead(p, walk2, s2, kHalf + 32 * part + lane)};
+        const int tiles = ahead[0].tiles;
+        pair_ready();
+        for (int n = 0; n < tiles && !wait.over(); ++n) {
+            const int slots[kValueGroups] = {ahead[0].next(), ahead[1].next()};
+            // One bit a slot that is seen.  Place n % 4 was last read for tile
+            // n - 4; the copies of tile n - 1 waited for the second product of
+            // tile n - 2.
+#pragma unroll
+            for (int g = 0; g < kValueGroups; ++g) {
+                const uint32_t bits = __ballot_sync(~0u, slots[g] >= 0);
+                if (lane == 0) sh.mask[n & 3][2 * g + part] = bits;
+            }
+            if (lane == 0) ptx::mbar_arrive(&sh.mask_full[n & 3]);
+            const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + (lane & 7) * 16;
+#pragma unroll
+            for (int g = 0; g < kValueGroups; ++g) {
+                if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
+                const uint32_t to = values + g * (kHalf * 128) + part * 4096 + r * 128;
+                const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int x = __shfl_sync(~0u, slots[g], 4 * q + r);
+                    const uint8_t* from = cache + max(x, 0) * (2 * p.slot_stride);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc::copy16((q & 1 ? odd : even) + q * 512 + c * kValuePiece, from + 128 * c, x >= 0 ? 16 : 0);
+                }
+                tc::copy16_arrive(&sh.value_landed[g]);
+            }
         }
         tc::copy16_drain();
     } else if (kPaged && warp == 5) {
@@ -408,10 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int n = 0;
         bool more = walk.next(s);
         int tile = s.first;
-        const bool mine = lane * box_rows < S::kHalf;
+        const bool mine = lane * box_rows < kHalf;
         const auto fetch = [&]() {  // row of the cache at which box `lane` begins
             const int x = mine ? slot_of<true>(p, s.row, s.length,
-                                               static_cast<int64_t>(tile) * S::kTile + rank * S::kHalf + lane * box_rows)
+                                               static_cast<int64_t>(tile) * kTile + rank * kHalf + lane * box_rows)
                                : -1;
             return x < 0 ? p.num_slots : x;
         };
@@ -424,13 +437,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tile = s.first;
             }
             if (more) next_box = fetch();
-            for (int g = 0; g < S::kKeyGroups; ++g) {
+            for (int g = 0; g < kKeyGroups; ++g) {
                 if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], S::kGroupPieces * S::kKeyPiece);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], kGroupPieces * kKeyPiece);
                 __syncwarp();
                 if (mine)
-                    for (int c = S::kGroupPieces * g; c < S::kGroupPieces * (g + 1); ++c)
-                        tc::load_2d(keys + c * S::kKeyPiece + lane * box_rows * 128, &maps.cache, 64 * c, box,
+                    for (int c = kGroupPieces * g; c < kGroupPieces * (g + 1); ++c)
+                        tc::load_2d(keys + c * kKeyPiece + lane * box_rows * 128, &maps.cache, 64 * c, box,
                                     &sh.key_landed[g]);
             }
             ++n;
@@ -440,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kPieces; ++c) tc::prefetch_2d(&maps.cache, 64 * c, next_box);
         }
         if (n > 0 && wait.over())
-            for (int g = 0; g < S::kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
+            for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
     } else if (kPaged && warp == 6) {
         // Pages, second product: all slots of each tile, values 256 rank...
         int n = 0;
@@ -448,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int tile = s.first;
         const auto fetch = [&](int* slots) {  // slots lane, lane + 32, ..
             for (int i = 0; i < 4; ++i)
-                slots[i] = slot_of<true>(p, s.row, s.length, static_cast<int64_t>(tile) * S::kTile + 32 * i + lane);
+                slots[i] = slot_of<true>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
         };
         int next_slots[4];
         if (more) fetch(next_slots);
@@ -475,23 +488,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if ((at >> 5) == i) box = x;
             }
             if (box < 0) box = p.num_slots;
-            for (int g = 0; g < S::kValueGroups; ++g) {
+            for (int g = 0; g < kValueGroups; ++g) {
                 if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_landed[g], 2 * S::kValuePiece);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_landed[g], kValueBytes / kValueGroups);
                 __syncwarp();
-                if (at < S::kTile)
-                    for (int c = 2 * g; c < 2 * g + 2; ++c)
-                        tc::load_2d(values + c * S::kValuePiece + at * 128, &maps.cache, 256 * rank + 64 * c, box,
+                if (at / kHalf == g)
+                    for (int c = 0; c < 4; ++c)
+                        tc::load_2d(values + c * kValuePiece + at * 128, &maps.cache, 256 * rank + 64 * c, box,
                                     &sh.value_landed[g]);
             }
             ++n;
         }
         if (n > 0 && wait.over())
-            for (int g = 0; g < S::kValueGroups; ++g) tc::Waits::drain(&sh.value_landed[g], (n - 1) & 1);
+            for (int g = 0; g < kValueGroups; ++g) tc::Waits::drain(&sh.value_landed[g], (n - 1) & 1);
     } else if (warp == kQueryWarp) {
         if (lane == 0 && rank == 0 && pair > 0) {
-            const Runs runs(sh.total, pairs, S::kLeast);
-            const int tiles = tiles_of<kPaged>(walk.length), all = p.queries * p.heads;
+            const Runs runs(sh.total, pairs);
+            const int tiles = tiles_of(walk.length), all = p.queries * p.heads;
             const int start = sh.begin - walk.first;  // of the group's tiles
             Join join = {};
             if (walk.left > 0 && walk.first > 0 && runs.start(pair - 1) <= start) {
@@ -504,29 +517,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         pair_ready();
         if (lane == 0) {
-            const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full), 0);
+            const int places = few ? 2 : 1;
             for (int n = 0; walk.next(s); ++n) {
-                if (n > 0) wait(&sh.query_empty, (n - 1) & 1);
-                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full, 2 * kQueryBytes);
-                const int m = s.group * kRows + rank * kHalfRows;
+                const int place = n % places, round = n / places;
+                const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full[place]), 0),
+                               to = queries + place * kPieces * query_piece;
+                if (round > 0) wait(&sh.query_empty[place], (round - 1) & 1);
+                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full[place], 2 * kPieces * query_piece);
+                const int m = s.group * kRows + rank * block_rows;
                 for (int c = 0; c < kPieces; ++c) {
                     if (whole_rows) {
-                        tc::load_4d_pair(queries + c * kQueryPiece, &maps.q, 64 * c, m, 0, s.row, full);
+                        tc::load_4d_pair(to + c * query_piece, &maps.q, 64 * c, m, 0, s.row, full);
                     } else {
-                        for (int i = 0; i < kHalfRows; ++i)
-                            tc::load_4d_pair(queries + c * kQueryPiece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
+                        for (int i = 0; i < block_rows; ++i)
+                            tc::load_4d_pair(to + c * query_piece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
                                              (m + i) / p.heads, s.row, full);
                     }
                 }
                 if (*wait.gave_up) {
-                    if (rank == 0) tc::Waits::drain(&sh.query_full, n & 1);
+                    if (rank == 0) {
+                        if (n > 0 && places == 2) tc::Waits::drain(&sh.query_full[place ^ 1], ((n - 1) / 2) & 1);
+                        tc::Waits::drain(&sh.query_full[place], round & 1);
+                    }
                     break;
                 }
             }
         }
     } else if (!kPaged && warp == kPrefetchWarp) {
         // The rows of the tile after those being copied come to L2.
-        const int at = rank * S::kHalf + lane;
+        const int at = rank * kHalf + lane;
         int n = 0;
         uint32_t spins = 0;
         uint64_t since = 0;
@@ -534,14 +553,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pair_ready();
         while (!over && walk.next(s))
             for (int tile = s.first; tile < s.last && !over; ++tile, ++n) {
-                const int slot = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * S::kTile + at);
+                int slots[2];
+                for (int i = 0; i < 2; ++i)
+                    slots[i] = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at + 32 * i);
                 // Once the copies of the tile before are under way; a tile
                 // whose own copies are needs no more help.
                 while (!over && __any_sync(~0u, sh.copied < n)) over = wait.idle(spins, since);
                 spins = 0;
-                if (__any_sync(~0u, sh.copied > n) || slot < 0) continue;
-                const uint8_t* row = static_cast<const uint8_t*>(p.cache) + slot * (2 * p.slot_stride);
-                for (int c = 0; c < kPieces; ++c) ptx::prefetch_l2(row + 128 * c);
+                if (__any_sync(~0u, sh.copied > n)) continue;
+                for (int i = 0; i < 2; ++i) {
+                    if (slots[i] < 0) continue;
+                    const uint8_t* row = static_cast<const uint8_t*>(p.cache) + slots[i] * (2 * p.slot_stride);
+                    for (int c = 0; c < kPieces; ++c) ptx::prefetch_l2(row + 128 * c);
+                }
+                __syncwarp();
             }
     } else if (warp == 7) {
         // Tells the first block of each group of pieces that landed here,
@@ -554,33 +579,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint64_t since = 0;
         pair_ready();
         const auto ready = [](uint64_t* bar, int n) {
-            return __any_sync(~0u, ptx::mbar_test_wait(bar, static_cast<uint32_t>(n / S::kPlaces) & 1));
+            return __any_sync(~0u, ptx::mbar_test_wait(bar, static_cast<uint32_t>(n) & 1));
         };
         while (more && (keys_done < tiles || values_done < tiles)) {
-            const int k_at = (keys_done % S::kPlaces) * S::kKeyGroups + kg,
-                      v_place = values_done % S::kPlaces, v_at = v_place * S::kValueGroups + vg;
-            if (keys_done < tiles && ready(&sh.key_landed[k_at], keys_done)) {
+            if (keys_done < tiles && ready(&sh.key_landed[kg], keys_done)) {
                 tc::fence_async();
                 __syncwarp();
-                if (lane == 0) tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.key_full[k_at]), 0));
-                if (++kg == S::kKeyGroups) {
+                if (lane == 0) tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.key_full[kg]), 0));
+                if (++kg == kKeyGroups) {
                     kg = 0;
                     ++keys_done;
                 }
                 spins = 0;
-            } else if (values_done < tiles && ready(&sh.value_landed[v_at], values_done)) {
-                const int left = s.length - tile * S::kTile;
-                if (kPaged && left < S::kTile) {
+            } else if (values_done < tiles && ready(&sh.value_landed[vg], values_done)) {
+                const int left = s.length - tile * kTile - vg * kHalf;
+                if (kPaged && left < kHalf) {
                     // Rows past the sequence's end may hold anything, and a
                     // weight of zero would not hide a NaN.
-                    for (int i = max(left, 0) * 16 + lane; i < S::kTile * 16; i += 32)
-                        ptx::sts_u4(values + (2 * vg + ((i >> 3) & 1)) * S::kValuePiece + (i >> 4) * 128 + (i & 7) * 16,
+                    for (int i = max(left, 0) * 32 + lane; i < kHalf * 32; i += 32)
+                        ptx::sts_u4(values + ((i >> 3) & 3) * kValuePiece + (vg * kHalf + (i >> 5)) * 128 + (i & 7) * 16,
                                     make_uint4(0, 0, 0, 0));
                 }
                 tc::fence_async();
                 __syncwarp();
-                if (lane == 0) tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.value_full[v_at]), 0));
-                if (++vg == S::kValueGroups) {
+                if (lane == 0) tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.value_full[vg]), 0));
+                if (++vg == kValueGroups) {
                     vg = 0;
                     ++values_done;
                     if (++tile == s.last && values_done < tiles) {
@@ -596,16 +619,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 4) {
         pair_ready();
         if (rank == 0) {
-            const uint32_t score_instr = tc::instruction(kBf16, kRows, S::kTile, negate, false);
+            const uint32_t score_instr = tc::instruction(kBf16, kRows, kTile, negate, false);
             const uint32_t sum_instr = tc::instruction(kBf16, kRows, 256, false, true);
             const uint64_t query_at = tc::operand(queries), key_at = tc::operand(keys), weight_at = tc::operand(weights),
-                           value_at = tc::operand(values, S::kValuePiece);
+                           value_at = tc::operand(values, kValuePiece);
             // A group of the first product of tile `scored`, at most one ahead
             // of the second (there are two score tiles), or a group of the
             // second product of tile `summed`: whichever has its operands, so
             // that neither waits behind the other's copies.
             const auto ready = [](uint64_t* bar, int n) {
-                return __any_sync(~0u, ptx::mbar_test_wait(bar, static_cast<uint32_t>(n / S::kPlaces) & 1));
+                return __any_sync(~0u, ptx::mbar_test_wait(bar, static_cast<uint32_t>(n) & 1));
             };
             const int tiles = walk.left;
             int scored = 0, summed = 0, kg = 0, vg = 0, tile = 0, segment = -1;
@@ -613,27 +636,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t spins = 0;
             uint64_t since = 0;
             while (summed < tiles) {
-                const int sum_place = summed % S::kPlaces;
-                if (summed < scored && (vg > 0 || ready(&sh.weight[sum_place], summed)) &&
-                    ready(&sh.value_full[sum_place * S::kValueGroups + vg], summed)) {
+                if (summed < scored && (vg > 0 || ready(&sh.weight, summed)) && ready(&sh.value_full[vg], summed)) {
                     const bool add = !first[summed & 1];
-                    const uint64_t w = weight_at + sum_place * (S::kWeightBytes >> 4),
-                                   v = value_at + sum_place * (S::kValueBytes >> 4);
                     tc::fence_after();
                     if (tc::elect()) {
 #pragma unroll
-                        for (int a = 0; a < 2; ++a) {  // values 128 a.. of each block's 256
-                            if (S::kValueGroups == 2 && a != vg) continue;
+                        for (int a = 0; a < 2; ++a)  // values 128 a.. of each block's 256
 #pragma unroll
-                            for (int k = 0; k < S::kTile / 16; ++k)
-                                tc::mma<2>(tmem + 128 * a, w + (k >> 2) * (S::kWeightPiece >> 4) + 2 * (k & 3),
-                                           v + 2 * a * (S::kValuePiece >> 4) + 128 * k, sum_instr, add || k > 0);
-                        }
-                        tc::commit_pair(&sh.value_empty[sum_place * S::kValueGroups + vg]);
-                        if (vg == S::kValueGroups - 1) tc::commit_pair(&sh.sum[sum_place]);
+                            for (int k = 0; k < kHalf / 16; ++k)
+                                tc::mma<2>(tmem + 128 * a, weight_at + vg * (kWeightPiece >> 4) + 2 * k,
+                                           value_at + (2 * a * kValuePiece + vg * kHalf * 128 >> 4) + 128 * k, sum_instr,
+                                           add || vg > 0 || k > 0);
+                        tc::commit_pair(&sh.value_empty[vg]);
+                        if (vg == kValueGroups - 1) tc::commit_pair(&sh.sum);
                     }
                     __syncwarp();
-                    if (++vg == S::kValueGroups) {
+                    if (++vg == kValueGroups) {
                         vg = 0;
                         ++summed;
                     }
@@ -646,28 +664,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tile = s.first;
                         ++segment;
                     }
-                    const int place = scored % S::kPlaces;
+                    const int query_place = few ? segment & 1 : 0, query_round = few ? segment >> 1 : segment;
                     if ((kg > 0 || tile > s.first ||
-                         __any_sync(~0u, ptx::mbar_test_wait(&sh.query_full, static_cast<uint32_t>(segment) & 1))) &&
-                        ready(&sh.key_full[place * S::kKeyGroups + kg], scored)) {
-                        const uint32_t d = tmem + kScore + S::kHalf * (static_cast<uint32_t>(scored) & 1);
-                        const uint64_t k_at = key_at + place * (S::kKeyBytes >> 4);
+                         __any_sync(~0u, ptx::mbar_test_wait(&sh.query_full[query_place],
+                                                             static_cast<uint32_t>(query_round) & 1))) &&
+                        ready(&sh.key_full[kg], scored)) {
+                        const uint32_t d = tmem + kScore + kHalf * (static_cast<uint32_t>(scored) & 1);
+                        const uint64_t q_at = query_at + query_place * (kPieces * query_piece >> 4);
                         tc::fence_after();
                         if (tc::elect()) {
 #pragma unroll
-                            for (int k = 0; k < 4 * S::kGroupPieces; ++k) {
-                                const int c = S::kGroupPieces * kg + (k >> 2);
-                                tc::mma<2>(d, query_at + c * (kQueryPiece >> 4) + 2 * (k & 3),
-                                           k_at + c * (S::kKeyPiece >> 4) + 2 * (k & 3), score_instr, (kg | k) != 0);
+                            for (int k = 0; k < 4 * kGroupPieces; ++k) {
+                                const int c = kGroupPieces * kg + (k >> 2);
+                                tc::mma<2>(d, q_at + c * (query_piece >> 4) + 2 * (k & 3),
+                                           key_at + c * (kKeyPiece >> 4) + 2 * (k & 3), score_instr, (kg | k) != 0);
                             }
-                            tc::commit_pair(&sh.key_empty[place * S::kKeyGroups + kg]);
-                            if (kg == S::kKeyGroups - 1) {
+                            tc::commit_pair(&sh.key_empty[kg]);
+                            if (kg == kKeyGroups - 1) {
                                 tc::commit_pair(&sh.score[scored & 1]);
-                                if (tile == s.last - 1) tc::commit_pair(&sh.query_empty);
+                                if (tile == s.last - 1) tc::commit_pair(&sh.query_empty[query_place]);
                             }
                         }
                         __syncwarp();
-                        if (++kg == S::kKeyGroups) {
+                        if (++kg == kKeyGroups) {
                             kg = 0;
                             first[scored & 1] = tile == s.first;
                             ++tile;
@@ -684,36 +703,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::Waits::drain(&sh.end, 0);
             }
         }
-    } else if (warp < 4) {
+    } else if (warp < 4 && !(few && (warp & 1))) {
         const int r = threadIdx.x & 63, half = threadIdx.x >> 6;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
-        const uint32_t weight_full[2] = {ptx::map_rank(ptx::smem_addr(&sh.weight[0]), 0),
-                                         ptx::map_rank(ptx::smem_addr(&sh.weight[S::kPlaces - 1]), 0)};
-        // This thread's weights: row r of the piece its slots are in.
-        constexpr int kSixteens = S::kHalf / 8;
-        const uint32_t weight_row = weights + (kPaged ? half * S::kWeightPiece : 0) + r * 128;
-        const int sixteen0 = kPaged ? 0 : half * kSixteens;
+        const uint32_t weight_full = ptx::map_rank(ptx::smem_addr(&sh.weight), 0);
+        const uint32_t weight_row = weights + half * kWeightPiece + r * 128;
         const int all = p.queries * p.heads, part_rows = part_rows_of(all);
+        const int threads = few ? 64 : 128;
+        const auto softmax_sync = [&] { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); };
         int n = 0;
         pair_ready();
         while (walk.next(s)) {
-            const int m_row = s.group * kRows + rank * kHalfRows + r;
+            const int m_row = s.group * kRows + rank * block_rows + r;
             const int limit = s.length - (p.queries - 1 - min(m_row / p.heads, p.queries - 1));
             float m = -INFINITY, l = 0.f;
             for (int tile = s.first; tile < s.last; ++tile, ++n) {
                 wait.warp(&sh.mask_full[n & 3], (n >> 2) & 1);
                 wait.warp(&sh.score[n & 1], (n >> 1) & 1);
                 tc::fence_after();
-                uint32_t raw_s[S::kHalf];
+                uint32_t raw_s[kHalf];
 #pragma unroll
-                for (int c = 0; c < S::kHalf / 32; ++c)
-                    tc::load32(lanes + kScore + S::kHalf * (n & 1) + 32 * c, raw_s + 32 * c);
-                uint32_t seen[S::kHalf / 32];
+                for (int c = 0; c < kHalf / 32; ++c)
+                    tc::load32(lanes + kScore + kHalf * (n & 1) + 32 * c, raw_s + 32 * c);
+                uint32_t seen[kHalf / 32];
                 bool all_seen = true;
-                const int left = limit - tile * S::kTile - half * S::kHalf;  // of this thread's slots
+                const int left = limit - tile * kTile - half * kHalf;  // of this thread's slots
 #pragma unroll
-                for (int c = 0; c < S::kHalf / 32; ++c) {
-                    seen[c] = sh.mask[n & 3][half * (S::kHalf / 32) + c];
+                for (int c = 0; c < kHalf / 32; ++c) {
+                    seen[c] = sh.mask[n & 3][half * (kHalf / 32) + c];
                     const int here = left - 32 * c;
                     if (here < 32) seen[c] &= here <= 0 ? 0u : (~0u >> (32 - here));
                     all_seen = all_seen && seen[c] == ~0u;
@@ -722,27 +739,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float* x = reinterpret_cast<float*>(raw_s);
                 if (__any_sync(~0u, !all_seen)) {
 #pragma unroll
-                    for (int i = 0; i < S::kHalf; ++i)
+                    for (int i = 0; i < kHalf; ++i)
                         if (!((seen[i >> 5] >> (i & 31)) & 1)) x[i] = -INFINITY;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < S::kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+                for (int i = 0; i < kHalf; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
                 float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale_log2;
                 // The other half of the slots is with thread t ^ 64.
                 sh.exchange[n & 1][threadIdx.x] = tile_top;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                softmax_sync();
                 tile_top = fmaxf(tile_top, sh.exchange[n & 1][threadIdx.x ^ 64]);
-                const bool raise = tile_top > m + kLag || (m == -INFINITY && tile_top > m);
+                // (rows past the last see whatever is there)
+                const bool raise = m_row < all && (tile_top > m + kLag || (m == -INFINITY && tile_top > m));
                 const float next = raise ? tile_top : m;
                 const float by = raise ? tc::exp2_approx(m - next) : 1.f;
                 m = next;
                 l *= by;
                 const float shift = m == -INFINITY ? 0.f : -m;
-                uint32_t w[S::kHalf / 2];
+                uint32_t w[kHalf / 2];
                 float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < S::kHalf / 2; ++i) {
+                for (int i = 0; i < kHalf / 2; ++i) {
                     const float a = tc::exp2_approx(fmaf(x[2 * i], scale_log2, shift));
                     const float b = tc::exp2_approx(fmaf(x[2 * i + 1], scale_log2, shift));
                     add[(2 * i) & 3] += a;
@@ -750,12 +768,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     w[i] = tc::pack<kBf16>(a, b);
                 }
                 l += (add[0] + add[1]) + (add[2] + add[3]);
-                const int place = n % S::kPlaces;
-                // The weights' place is free once the second product that read
-                // it last is done, the sums once that of the tile before is.
-                if (n >= S::kPlaces) wait.warp(&sh.sum[place], (n / S::kPlaces - 1) & 1);
+                // The weights' place and the sums are free once the second
+                // product of the tile before is done.
+                if (n > 0) wait.warp(&sh.sum, (n - 1) & 1);
                 if (tile > s.first && __any_sync(~0u, raise)) {
-                    wait.warp(&sh.sum[(n - 1) % S::kPlaces], ((n - 1) / S::kPlaces) & 1);
                     tc::fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
@@ -769,20 +785,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc::wait_store();
                 }
 #pragma unroll
-                for (int i = 0; i < kSixteens; ++i)
-                    ptx::sts_u4(weight_row + place * S::kWeightBytes + (((sixteen0 + i) ^ (r & 7)) << 4),
+                for (int i = 0; i < 8; ++i)
+                    ptx::sts_u4(weight_row + ((i ^ (r & 7)) << 4),
                                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
                 tc::fence_async();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::arrive_cluster(weight_full[place]);
+                if (lane == 0) tc::arrive_cluster(weight_full);
             }
             // The sums of both halves, then the values 256 half.. of the row.
             sh.exchange[n & 1][threadIdx.x] = l;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            softmax_sync();
             l += sh.exchange[n & 1][threadIdx.x ^ 64];
             // exchange[n & 1] is written again by the next tile n.
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            softmax_sync();
             const bool whole = s.first == 0 && s.last == s.tiles;
             const int64_t at = static_cast<int64_t>(s.row) * all + m_row;
             const int r_part = m_row - s.group * kRows;
@@ -793,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             const float by = l == 0.f ? 0.f : 1.f / l;
             uint16_t* out = static_cast<uint16_t*>(p.out) + at * kLatent + 256 * half;
-            wait.warp(&sh.sum[(n - 1) % S::kPlaces], ((n - 1) / S::kPlaces) & 1);
+            wait.warp(&sh.sum, (n - 1) & 1);
             tc::fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -837,53 +853,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && sh.gave_up) atomicOr(flags, TOPK_FLAG_TIMEOUT);
 }
 
-// Joins the rows that several pairs shared: block (i, j) those of pair i + 1's
-// Join, 16 values of 32 rows by each warp, a row a lane.
-constexpr int kJoinThreads = 128;
+// Joins the rows that several pairs shared.  Every block reads all pairs' Joins
+// and takes its share of their units of 32 rows, a row a lane: with up to four
+// parts a unit has 16 values a warp (whole 32-byte sectors of the result), with
+// more of them four, so that a row of many parts has many threads; each has
+// eight loads in flight.
+constexpr int kJoinThreads = 256;
+constexpr int kFewParts = 4;
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentParams p) {
-    const int pair = static_cast<int>(blockIdx.x) + 1;
-    ptx::grid_dependency_wait();
-    const Join join = static_cast<const Join*>(p.workspace)[pair];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = static_cast<int>(blockIdx.y >> 3) * 32 + lane;
-    const int c0 = 4 * (static_cast<int>(blockIdx.y & 7) * (kJoinThreads / 32) + warp);  // float4 columns
-    if (r >= join.rows || join.parts == 0) return;
-    const int part_rows = part_rows_of(p.queries * p.heads);
-    const auto stats_of = [&](int i) {
-        const float* part = part_of(p, part_rows, 2 * (pair - 1 + i) + (i == 0 ? 1 : 0));
-        return reinterpret_cast<const float2*>(part + static_cast<int64_t>(part_rows) * kLatent)[r];
-    };
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < join.parts; ++i) m = fmaxf(m, stats_of(i).x);
-    if (m == -INFINITY) m = 0.f;
-    float l = 0.f, o[16] = {};
-#pragma unroll 4
-    for (int i = 0; i < join.parts; ++i) {
-        const float2 stats = stats_of(i);
-        const float4* from = reinterpret_cast<const float4*>(part_of(p, part_rows, 2 * (pair - 1 + i) + (i == 0 ? 1 : 0))) +
-                             static_cast<int64_t>(c0) * part_rows + r;
-        // A part that saw nothing has no sums.
-        const float by = stats.y == 0.f ? 0.f : exp2f(stats.x - m);
-        l += stats.y * by;
+// Values 4 c.. 4 (c + kColumns) of one row; kParts parts at a time.
+template <bool kBf16, int kColumns, int kParts>
+__device__ __forceinline__ void join_row(const LatentParams& p, const Join& join, int pair, int part_rows, int r, int c) {
+    const auto part_at = [&](int i) { return part_of(p, part_rows, 2 * (pair - 1 + i) + (i == 0 ? 1 : 0)); };
+    float m = -INFINITY, l = 0.f;
+    float4 o[kColumns] = {};
+    for (int i0 = 0; i0 < join.parts; i0 += kParts) {
+        float2 stats[kParts];
+        float4 x[kParts][kColumns];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float4 x = from[c * part_rows];
-            o[4 * c] += x.x * by;
-            o[4 * c + 1] += x.y * by;
-            o[4 * c + 2] += x.z * by;
-            o[4 * c + 3] += x.w * by;
+        for (int i = 0; i < kParts; ++i) {
+            stats[i] = make_float2(-INFINITY, 0.f);
+            if (i0 + i < join.parts) {
+                const float* part = part_at(i0 + i);
+                stats[i] = reinterpret_cast<const float2*>(part + static_cast<int64_t>(part_rows) * kLatent)[r];
+#pragma unroll
+                for (int k = 0; k < kColumns; ++k)
+                    x[i][k] = reinterpret_cast<const float4*>(part)[static_cast<int64_t>(c + k) * part_rows + r];
+            }
+        }
+        // The maximum may rise: what is summed so far is scaled back.
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) top = fmaxf(top, stats[i].x);
+        const float base = top == -INFINITY ? 0.f : top, back = exp2f(m - base);
+        m = top;
+        l *= back;
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k) o[k] = make_float4(o[k].x * back, o[k].y * back, o[k].z * back, o[k].w * back);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if (stats[i].y == 0.f) continue;  // a part that saw nothing
+            const float by = exp2f(stats[i].x - base);
+            l += stats[i].y * by;
+#pragma unroll
+            for (int k = 0; k < kColumns; ++k)
+                o[k] = make_float4(o[k].x + x[i][k].x * by, o[k].y + x[i][k].y * by, o[k].z + x[i][k].z * by,
+                                   o[k].w + x[i][k].w * by);
         }
     }
     const float by = l == 0.f ? 0.f : 1.f / l;
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = tc::pack<kBf16>(o[2 * i] * by, o[2 * i + 1] * by);
     const int64_t at = join.at + r;
-    tc::store_v8(static_cast<uint16_t*>(p.out) + at * kLatent + 4 * c0, w);
-    if (p.lse && c0 == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    uint32_t w[2 * kColumns];
+#pragma unroll
+    for (int k = 0; k < kColumns; ++k) {
+        w[2 * k] = tc::pack<kBf16>(o[k].x * by, o[k].y * by);
+        w[2 * k + 1] = tc::pack<kBf16>(o[k].z * by, o[k].w * by);
+    }
+    uint16_t* out = static_cast<uint16_t*>(p.out) + at * kLatent + 4 * c;
+    if constexpr (kColumns == 4)
+        tc::store_v8(out, w);
+    else
+        *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const LatentParams p, int pairs) {
+    __shared__ Join joins[kMaxPairs];
+    __shared__ int upto[kMaxPairs];  // units of the Joins up to and with one
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    if (warp == 0) {
+        constexpr int kRounds = (kMaxPairs + 31) / 32;
+        Join mine[kRounds] = {};
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k)
+            if (32 * k + lane > 0 && 32 * k + lane < pairs) mine[k] = static_cast<const Join*>(p.workspace)[32 * k + lane];
+        int before = 0;
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+            int units = mine[k].parts == 0 ? 0 : (mine[k].rows + 31) / 32 * (mine[k].parts <= kFewParts ? 4 : 16);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(~0u, units, d);
+                if (lane >= d) units += x;
+            }
+            units += before;
+            if (32 * k + lane < kMaxPairs) {
+                joins[32 * k + lane] = mine[k];
+                upto[32 * k + lane] = units;
+            }
+            before = __shfl_sync(~0u, units, 31);
+        }
+    }
+    __syncthreads();
+    const int part_rows = part_rows_of(p.queries * p.heads);
+    for (int unit = static_cast<int>(blockIdx.x); unit < upto[kMaxPairs - 1]; unit += static_cast<int>(gridDim.x)) {
+        int lo = 0, hi = kMaxPairs - 1;  // the first pair with upto > unit
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (upto[mid] > unit)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        const Join join = joins[lo];
+        const bool few = join.parts <= kFewParts;
+        const int in_join = unit - (lo > 0 ? upto[lo - 1] : 0), columns = few ? 4 : 16;
+        const int r = in_join / columns * 32 + lane, c = in_join % columns * 8 + warp;
+        if (r >= join.rows) continue;
+        if (few)
+            join_row<kBf16, 4, 2>(p, join, lo, part_rows, r, 4 * c);
+        else
+            join_row<kBf16, 1, 8>(p, join, lo, part_rows, r, c);
+    }
 }
 
 }  // namespace
@@ -907,7 +991,7 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const Att
     const int64_t q_dims[4] = {kWidth, rows, whole_rows ? 1 : p.queries, p.batch};
     const int64_t q_steps[3] = {rows > 1 ? 2 * row_step : any, whole_rows ? any : 2 * p.q_query_stride,
                                 p.batch > 1 ? 2 * p.q_row_stride : any};
-    CUresult r = encode_map(&maps.q, bf16, p.q, 4, q_dims, q_steps, 1, whole_rows ? kHalfRows : 1);
+    CUresult r = encode_map(&maps.q, bf16, p.q, 4, q_dims, q_steps, 1, !whole_rows ? 1 : all <= kHalfRows ? kHalfRows / 2 : kHalfRows);
     const int64_t c_dims[2] = {kWidth, p.num_slots}, c_steps[1] = {2 * p.slot_stride};
     // Pages of 16 slots or more go through the copy engine.
     const bool paged = !p.indices && p.log2_page >= 4;
@@ -921,28 +1005,18 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const Att
     cudaError_t e = allow_shared(kernel, kSmem, prepared[2 * paged + bf16][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention shared memory");
     const int64_t groups = (all + kRows - 1) / kRows;
-    const int64_t tile = paged ? Step<true>::kTile : Step<false>::kTile;
-    const int64_t tiles = p.batch * groups * (p.max_len > tile ? (p.max_len + tile - 1) / tile : 1);
+    const int64_t tiles = p.batch * groups * (p.max_len > kTile ? (p.max_len + int64_t{kTile} - 1) / kTile : 1);
     if (tiles > INT32_MAX) return TOPK_EINVAL;
     const int64_t most = device.sms / 2 < kMaxPairs ? device.sms / 2 : kMaxPairs;
     const int pairs = static_cast<int>(tiles < most ? tiles : most);
     const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
-    kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps, device.flags, scale_log2, p.scale < 0.f, whole_rows,
-                                                  box_rows);
-    e = cudaGetLastError();
+    e = launch_early(kernel, dim3(2 * pairs), kThreads, kSmem, stream, p, maps, device.flags, scale_log2, p.scale < 0.f,
+                     whole_rows, box_rows);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
     if (pairs > 1) {
-        // Placed while the first kernel runs.
-        cudaLaunchAttribute attr = {};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(pairs - 1), 8 * static_cast<unsigned>(((all < kRows ? all : kRows) + 31) / 32));
-        cfg.blockDim = dim3(kJoinThreads);
-        cfg.stream = stream;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, bf16 ? join_kernel<true> : join_kernel<false>, p);
+        const int units = (pairs - 1) * ((part_rows_of(all) + 31) / 32) * 16, blocks = 3 * device.sms;
+        e = launch_early(bf16 ? join_kernel<true> : join_kernel<false>, dim3(units < blocks ? units : blocks), kJoinThreads,
+                         0, stream, p, pairs);
         if (e != cudaSuccess) return api_cuda_fail(e, "latent attention join launch");
     }
     return TOPK_OK;

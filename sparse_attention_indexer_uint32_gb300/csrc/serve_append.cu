@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "attend_internal.h"
+#include "ptx.cuh"
 
 namespace topkidx {
 namespace {
@@ -60,6 +61,8 @@ __device__ __forceinline__ Eight<T> narrow(const float* f) {
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t token = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     if (token >= p.tokens) return;
@@ -134,11 +137,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendPara
 template <typename T>
 cudaError_t launch(const AppendParams& p, bool interleaved, cudaStream_t stream) {
     const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.tokens) + kThreads / 32 - 1) / (kThreads / 32));
-    if (interleaved)
-        cache_append_kernel<T, true><<<blocks, kThreads, 0, stream>>>(p);
-    else
-        cache_append_kernel<T, false><<<blocks, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(interleaved ? cache_append_kernel<T, true> : cache_append_kernel<T, false>, dim3(blocks), kThreads,
+                        0, stream, p);
 }
 
 }  // namespace

@@ -17,6 +17,7 @@
 #include <cstdint>
 
 #include "attend_internal.h"
+#include "ptx.cuh"
 
 namespace topkidx {
 namespace {
@@ -71,6 +72,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_tables_kernel(const TablesP
     int32_t* pages_before = sums + kChunk;  // [kChunk]
     __shared__ int64_t warp_tokens[32], warp_pages[32];
     __shared__ uint32_t all_flags;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t nb = gridDim.x, me = blockIdx.x;
     const int32_t page_mask = static_cast<int32_t>((int64_t{1} << p.log2_page) - 1);
@@ -188,8 +191,8 @@ cudaError_t launch_block_tables(const TablesParams& p, cudaStream_t stream) {
     int64_t blocks = (items + kChunk - 1) / kChunk;
     if (blocks < 1) blocks = 1;
     if (blocks > 152) blocks = 152;
-    block_tables_kernel<<<static_cast<unsigned>(blocks), kThreads, 2 * kChunk * sizeof(int32_t), stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(block_tables_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 2 * kChunk * sizeof(int32_t),
+                        stream, p);
 }
 
 }  // namespace topkidx
