@@ -139,8 +139,12 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         _check_tables(context_lens, new_lens, free_pages, page_table, max_tokens, out)
     batch, pages = shape
     if out is None:
-        buf = torch.empty(2 * batch + 3 + 3 * max_tokens, dtype=_I32, device=context_lens.device)
-        out = BlockTables(*buf.split([batch, batch + 1, max_tokens, max_tokens, max_tokens, 2]))
+        # One allocation; the token arrays start on 16 bytes, where the kernel writes four values at once.
+        room = (max_tokens + 3) // 4 * 4
+        buf = torch.empty(3 * room + 2 * batch + 3, dtype=_I32, device=context_lens.device)
+        at = 3 * room
+        out = BlockTables(buf[at:at + batch], buf[at + batch:at + 2 * batch + 1], buf[:max_tokens],
+                          buf[room:room + max_tokens], buf[2 * room:2 * room + max_tokens], buf[at + 2 * batch + 1:])
     status = _c.topk_block_tables(
         context_lens.data_ptr(), new_lens.data_ptr(), batch, page_size, free_pages.data_ptr(), free_pages.numel(),
         page_table.data_ptr(), page_table.stride(0) if batch > 1 else pages, pages, max_tokens, out[0].data_ptr(),

@@ -918,7 +918,7 @@ __device__ __forceinline__ void join_row(const LatentParams& p, const Join& join
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads, 3) join_kernel(const LatentParams p, int pairs) {
+__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const LatentParams p, int pairs) {
     __shared__ Join joins[kMaxPairs];
     __shared__ int upto[kMaxPairs];  // units of the Joins up to and with one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1014,7 +1014,7 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const Att
                      whole_rows, box_rows);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
     if (pairs > 1) {
-        const int units = (pairs - 1) * ((part_rows_of(all) + 31) / 32) * 16, blocks = 3 * device.sms;
+        const int units = (pairs - 1) * ((part_rows_of(all) + 31) / 32) * 16, blocks = 2 * device.sms;
         e = launch_early(bf16 ? join_kernel<true> : join_kernel<false>, dim3(units < blocks ? units : blocks), kJoinThreads,
                          0, stream, p, pairs);
         if (e != cudaSuccess) return api_cuda_fail(e, "latent attention join launch");
