@@ -2,11 +2,13 @@
 // latent rows in one pass.
 //
 // Mathematics: c' = c rsqrt(mean(c^2) + eps) w in fp32; the rotation turns
-// pair (a, b) by the angle of its position.  One warp holds one row in
-// registers (16 latent values a lane in two 16-byte loads; the 64 rotary
-// values in its first 8 or 4 lanes), so the row is read once and written once:
-// 1152 + 256 + 1152 bytes a token, bound by memory at large counts and by the
-// launch at small ones.
+// pair (a, b) by the angle of its position.  A warp holds a row in registers
+// (16 latent values a lane in two 16-byte loads, one rotary pair a lane), so the
+// row is read once and written once: 1152 + 256 + 1152 bytes a token, bound by
+// memory at large counts and by the launch at small ones.  Each warp walks
+// several rows with the weight kept, the row after the next and the next row's
+// cosines under way (a warp for one row or two took 43 us for 65536 rows: the
+// weight's second reading filled the L1 path).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,7 +22,7 @@ namespace topkidx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 2;  // of a warp, so that more loads are in flight
+constexpr int64_t kResident = 152 * 3;  // blocks that the GPU holds at once
 
 template <typename T>
 struct Pair;
@@ -60,106 +62,107 @@ __device__ __forceinline__ Eight<T> narrow(const float* f) {
     return x;
 }
 
+// One row on its way; a slot below 0 is not written.
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
-    ptx::grid_dependency_wait();
-    ptx::launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kTokens;
-    // Everything that does not hang on another load is asked for at once, that
-    // of a row without a slot too.
-    Eight<T> a[kTokens], b[kTokens], r0[kTokens], r1[kTokens];
-    int32_t slot[kTokens], position[kTokens];
-#pragma unroll
-    for (int k = 0; k < kTokens; ++k) {
-        slot[k] = -1;
-        position[k] = 0;
-        if (first + k >= p.tokens) continue;
-        slot[k] = p.slots[first + k];
-        if (p.cos_sin) position[k] = p.positions[first + k];
-        const Eight<T>* in = reinterpret_cast<const Eight<T>*>(static_cast<const T*>(p.rows) + (first + k) * p.row_stride);
-        a[k] = in[lane];
-        b[k] = in[lane + 32];
-        // Lanes 0..7 hold eight neighbouring rotary values each, or lanes 0..3
-        // eight of each half.
-        if (lane < 8) r0[k] = in[kLatent / 8 + lane];
-        if (!kInterleaved && lane < 4) r1[k] = in[kLatent / 8 + 4 + lane];
-    }
-    float4 c0[kTokens], s0[kTokens], c1[kTokens], s1[kTokens];
-#pragma unroll
-    for (int k = 0; k < kTokens; ++k) {
-        if (slot[k] >= p.num_slots || (p.cos_sin && (position[k] < 0 || position[k] >= p.num_positions))) slot[k] = -1;
-        if (slot[k] < 0 || !p.cos_sin || lane >= (kInterleaved ? 8 : 4)) continue;
-        const float4* turn = reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(position[k]) * kRope);
-        const int at = kInterleaved ? lane : 2 * lane;
-        c0[k] = turn[at];
-        s0[k] = turn[kRope / 8 + at];
-        if (!kInterleaved) {
-            c1[k] = turn[at + 1];
-            s1[k] = turn[kRope / 8 + at + 1];
+struct Row {
+    Eight<T> a, b;
+    typename Pair<T>::two pair;  // rotary values 2 lane, 2 lane + 1, or lane, lane + 32
+    int32_t slot, position;
+    float cosine, sine;
+
+    __device__ __forceinline__ void load(const AppendParams& p, int64_t token, int lane) {
+        slot = -1;
+        if (token >= p.tokens) return;
+        slot = p.slots[token];
+        if (p.cos_sin) position = p.positions[token];
+        const T* from = static_cast<const T*>(p.rows) + token * p.row_stride;
+        const Eight<T>* in = reinterpret_cast<const Eight<T>*>(from);
+        a = in[lane];
+        b = in[lane + 32];
+        if (kInterleaved) {
+            pair = reinterpret_cast<const typename Pair<T>::two*>(from + kLatent)[lane];
+        } else {
+            pair.x = from[kLatent + lane];
+            pair.y = from[kLatent + kRope / 2 + lane];
         }
     }
-#pragma unroll
-    for (int k = 0; k < kTokens; ++k) {
-        if (slot[k] < 0) continue;  // the whole warp
-        Eight<T>* out = reinterpret_cast<Eight<T>*>(static_cast<T*>(p.cache) + static_cast<int64_t>(slot[k]) * p.slot_stride);
+    __device__ __forceinline__ void load_turn(const AppendParams& p, int lane) {
+        if (slot >= p.num_slots) slot = -1;
+        if (slot < 0 || !p.cos_sin) return;
+        if (position < 0 || position >= p.num_positions) {
+            slot = -1;
+            return;
+        }
+        const float* turn = p.cos_sin + static_cast<int64_t>(position) * kRope;
+        cosine = turn[lane];
+        sine = turn[kRope / 2 + lane];
+    }
+    __device__ __forceinline__ void store(const AppendParams& p, const float* w, int lane) const {
+        if (slot < 0) return;  // the whole warp
+        T* to = static_cast<T*>(p.cache) + static_cast<int64_t>(slot) * p.slot_stride;
+        Eight<T>* out = reinterpret_cast<Eight<T>*>(to);
         if (p.weight) {
-            float x[16], w[16];
-            widen(a[k], x);
-            widen(b[k], x + 8);
+            float x[16];
+            widen(a, x);
+            widen(b, x + 8);
             float square = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) square += x[i] * x[i];
 #pragma unroll
             for (int d = 16; d; d >>= 1) square += __shfl_xor_sync(~0u, square, d);
             const float by = rsqrtf(square * (1.f / kLatent) + p.eps);
-            const Eight<T>* weight = static_cast<const Eight<T>*>(p.weight);
-            widen(weight[lane], w);
-            widen(weight[lane + 32], w + 8);
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = x[i] * by * w[i];
             out[lane] = narrow<T>(x);
             out[lane + 32] = narrow<T>(x + 8);
         } else {
-            out[lane] = a[k];
-            out[lane + 32] = b[k];
+            out[lane] = a;
+            out[lane + 32] = b;
         }
-        if (lane < 8) {
-            if (!p.cos_sin) {
-                out[kLatent / 8 + lane] = r0[k];
-            } else if (kInterleaved) {
-                float x[8], y[8];
-                widen(r0[k], x);
-                const float cs[4] = {c0[k].x, c0[k].y, c0[k].z, c0[k].w}, sn[4] = {s0[k].x, s0[k].y, s0[k].z, s0[k].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
-                    y[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
-                }
-                out[kLatent / 8 + lane] = narrow<T>(y);
-            } else if (lane < 4) {
-                float x[8], z[8], y[8], u[8];
-                widen(r0[k], x);
-                widen(r1[k], z);
-                const float cs[8] = {c0[k].x, c0[k].y, c0[k].z, c0[k].w, c1[k].x, c1[k].y, c1[k].z, c1[k].w};
-                const float sn[8] = {s0[k].x, s0[k].y, s0[k].z, s0[k].w, s1[k].x, s1[k].y, s1[k].z, s1[k].w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = x[i] * cs[i] - z[i] * sn[i];
-                    u[i] = x[i] * sn[i] + z[i] * cs[i];
-                }
-                out[kLatent / 8 + lane] = narrow<T>(y);
-                out[kLatent / 8 + 4 + lane] = narrow<T>(u);
-            }
+        typename Pair<T>::two y = pair;
+        if (p.cos_sin) {
+            const float2 x = Pair<T>::wide(pair);
+            y = Pair<T>::narrow(make_float2(x.x * cosine - x.y * sine, x.x * sine + x.y * cosine));
         }
-        __syncwarp();
+        if (kInterleaved) {
+            reinterpret_cast<typename Pair<T>::two*>(to + kLatent)[lane] = y;
+        } else {
+            to[kLatent + lane] = y.x;
+            to[kLatent + kRope / 2 + lane] = y.y;
+        }
+    }
+};
+
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendParams p) {
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    int64_t token = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    Row<T, kInterleaved> now, next, later;
+    now.load(p, token, lane);
+    next.load(p, token + step, lane);
+    float w[16];
+    if (p.weight) {
+        const Eight<T>* weight = static_cast<const Eight<T>*>(p.weight);
+        widen(weight[lane], w);
+        widen(weight[lane + 32], w + 8);
+    }
+    now.load_turn(p, lane);
+    for (; token < p.tokens; token += step) {
+        later.load(p, token + 2 * step, lane);
+        next.load_turn(p, lane);
+        now.store(p, w, lane);
+        now = next;
+        next = later;
     }
 }
 
 template <typename T>
 cudaError_t launch(const AppendParams& p, bool interleaved, cudaStream_t stream) {
-    constexpr int kBlockTokens = kThreads / 32 * kTokens;
-    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.tokens) + kBlockTokens - 1) / kBlockTokens);
+    const int64_t needed = (static_cast<int64_t>(p.tokens) + kThreads / 32 - 1) / (kThreads / 32);
+    const unsigned blocks = static_cast<unsigned>(needed < kResident ? needed : kResident);
     return launch_early(interleaved ? cache_append_kernel<T, true> : cache_append_kernel<T, false>, dim3(blocks), kThreads,
                         0, stream, p);
 }
