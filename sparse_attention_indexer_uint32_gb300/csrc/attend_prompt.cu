@@ -48,7 +48,7 @@ struct PromptMaps {
 };
 
 struct Barriers {
-    uint64_t full[kRing], empty[kRing];
+    uint64_t key_full[2], key_empty[2], value_full[2], value_empty[2];  // by step mod 2
     uint64_t query[2];
     uint64_t score[2], weight[2][2], sum[2];  // weights by tile and half of the step's keys
     uint64_t end;
@@ -67,6 +67,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t queries = base, ring = base + 6 * kPiece;
     Barriers& bar = *reinterpret_cast<Barriers*>(raw + (base - ptx::smem_addr(raw)) + (6 + kRing) * kPiece);
+    if (threadIdx.x == 0) {
+        tc::prefetch_map(&maps.q);
+        tc::prefetch_map(&maps.k_nope);
+        tc::prefetch_map(&maps.k_rope);
+        tc::prefetch_map(&maps.v);
+    }
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -129,11 +135,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar.range = range;
             bar.block = block;
             bar.gave_up = 0;
-            for (int i = 0; i < kRing; ++i) {
-                ptx::mbar_init(&bar.full[i], 1);
-                ptx::mbar_init(&bar.empty[i], 1);
-            }
             for (int t = 0; t < 2; ++t) {
+                ptx::mbar_init(&bar.key_full[t], 1);
+                ptx::mbar_init(&bar.key_empty[t], 1);
+                ptx::mbar_init(&bar.value_full[t], 1);
+                ptx::mbar_init(&bar.value_empty[t], 1);
                 ptx::mbar_init(&bar.query[t], 1);
                 ptx::mbar_init(&bar.score[t], 1);
                 ptx::mbar_init(&bar.weight[t][0], 4);
@@ -168,14 +174,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 9) {
         if (lane == 0) {
-            int issued = 0;
-            const auto take = [&](uint32_t bytes) {  // the next free piece of the ring
-                const int s = issued % kRing;
-                if (issued >= kRing) wait(&bar.empty[s], ((issued / kRing) - 1) & 1);
-                ptx::mbar_arrive_expect_tx(&bar.full[s], bytes);
-                ++issued;
-                return s;
+            // The ring's pieces i - 8 must have been used before pieces i are
+            // filled: whole groups are waited for, the keys or the values of
+            // the step in which they were.
+            const auto room = [&](int last) {
+                const int used = last - kRing;
+                if (used < 0) return;
+                const int step = used / kStepPieces;
+                wait(used % kStepPieces < kKeyPieces ? &bar.key_empty[step & 1] : &bar.value_empty[step & 1], (step >> 1) & 1);
             };
+            int key_steps = 0, value_steps = 0;
             const int q_head = p.q_head_stride ? head : 0, k_head = p.k_head_stride ? head : 0,
                       v_head = p.v_head_stride ? head : 0;
             const auto load_queries = [&](int t) {
@@ -185,24 +193,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (steps[0]) load_queries(0);
             for (int j = 0; j < n && !bar.gave_up; ++j) {
-                const int row = k0 + j * kTile;
-                for (int c = 0; c < 2; ++c) {
-                    const int s = take(kPiece);
-                    tc::load_3d(ring + s * kPiece, &maps.k_nope, 64 * c, k_head, row, &bar.full[s]);
-                }
-                const int s = take(kPiece);
-                tc::load_2d(ring + s * kPiece, &maps.k_rope, 0, row, &bar.full[s]);
+                const int row = k0 + j * kTile, piece = j * kStepPieces;
+                const auto at = [&](int i) { return ring + (piece + i) % kRing * kPiece; };
+                room(piece);
+                room(piece + 2);
+                uint64_t* full = &bar.key_full[j & 1];
+                ptx::mbar_arrive_expect_tx(full, kKeyPieces * kPiece);
+                for (int c = 0; c < 2; ++c) tc::load_3d(at(c), &maps.k_nope, 64 * c, k_head, row, full);
+                tc::load_2d(at(2), &maps.k_rope, 0, row, full);
+                ++key_steps;
                 if (j == 0 && steps[1]) load_queries(1);
-                for (int c = 0; c < 2; ++c) {  // 64 keys by 128 values
-                    const int s = take(kPiece);
+                room(piece + 3);
+                room(piece + 4);
+                full = &bar.value_full[j & 1];
+                ptx::mbar_arrive_expect_tx(full, 2 * kPiece);
+                for (int c = 0; c < 2; ++c)  // 64 keys by 128 values
                     for (int d = 0; d < 2; ++d)
-                        tc::load_3d(ring + s * kPiece + d * (kPiece / 2), &maps.v, 64 * d, v_head, row + 64 * c,
-                                    &bar.full[s]);
-                }
+                        tc::load_3d(at(3 + c) + d * (kPiece / 2), &maps.v, 64 * d, v_head, row + 64 * c, full);
+                ++value_steps;
             }
             if (bar.gave_up) {  // what is in flight lands before the block ends
-                for (int i = max(0, issued - kRing); i < issued; ++i)
-                    tc::Waits::drain(&bar.full[i % kRing], (i / kRing) & 1);
+                for (int i = max(0, key_steps - 2); i < key_steps; ++i) tc::Waits::drain(&bar.key_full[i & 1], (i >> 1) & 1);
+                for (int i = max(0, value_steps - 2); i < value_steps; ++i)
+                    tc::Waits::drain(&bar.value_full[i & 1], (i >> 1) & 1);
                 for (int t = 0; t < 2; ++t)
                     if (steps[t]) tc::Waits::drain(&bar.query[t], 0);
             }
@@ -211,39 +224,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t score_instr = tc::instruction(kBf16, kTile, kTile, negate, false);
         const uint32_t sum_instr = tc::instruction(kBf16, kTile, kValue, false, true);
         const uint64_t query_at = tc::operand(queries), key_at = tc::operand(ring), value_at = tc::operand(ring, kPiece / 2);
-        const auto scores = [&](int t, int j) {
+        const auto scores = [&](int t, int j) {  // and, after the second tile's, the keys are free
             if (j == 0) wait.warp(&bar.query[t], 0);
+            wait.warp(&bar.key_full[j & 1], (j >> 1) & 1);
+            const int piece = j * kStepPieces;
+            const uint64_t a = query_at + 3 * t * (kPiece >> 4);
+            const uint64_t b[3] = {key_at + piece % kRing * (kPiece >> 4), key_at + (piece + 1) % kRing * (kPiece >> 4),
+                                   key_at + (piece + 2) % kRing * (kPiece >> 4)};
+            if (tc::elect()) {
 #pragma unroll
-            for (int c = 0; c < kKeyPieces; ++c) {
-                const int i = j * kStepPieces + c;
-                wait.warp(&bar.full[i % kRing], (i / kRing) & 1);
-                if (tc::elect()) {
-                    const uint64_t a = query_at + (3 * t + c) * (kPiece >> 4), b = key_at + (i % kRing) * (kPiece >> 4);
+                for (int c = 0; c < kKeyPieces; ++c)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tc::mma<1>(tmem + t * kTile, a + 2 * k, b + 2 * k, score_instr, (c | k) != 0);
-                    if (c == kKeyPieces - 1) tc::commit<1>(&bar.score[t]);
-                }
-                __syncwarp();
+                        tc::mma<1>(tmem + t * kTile, a + c * (kPiece >> 4) + 2 * k, b[c] + 2 * k, score_instr, (c | k) != 0);
+                tc::commit<1>(&bar.score[t]);
+                if (t == 1 || j >= steps[1]) tc::commit<1>(&bar.key_empty[j & 1]);
             }
-        };
-        const auto release = [&](int from, int count) {
-            if (tc::elect())
-                for (int i = from; i < from + count; ++i) tc::commit<1>(&bar.empty[i % kRing]);
             __syncwarp();
         };
+        const auto sums = [&](int t, int j, int half) {
+            wait.warp(&bar.weight[t][half], j & 1);
+            tc::fence_after();
+            const uint64_t b = value_at + (j * kStepPieces + kKeyPieces + half) % kRing * (kPiece >> 4);
+            if (tc::elect()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_tmem(tmem + 256 + t * kValue, tmem + t * kTile + 32 * half + 8 * k, b + 128 * k, sum_instr,
+                                 j > 0 || half > 0 || k > 0);
+                if (half == 1) {
+                    tc::commit<1>(&bar.sum[t]);
+                    if (t == 1 || j >= steps[1]) tc::commit<1>(&bar.value_empty[j & 1]);
+                }
+            }
+            __syncwarp();
+        };
+        // The first tile may see one step less than the second (causal), or
+        // the second have no queries; so the last of the two in a step frees
+        // its keys and values.
         for (int t = 0; t < 2; ++t)
             if (steps[t]) scores(t, 0);
-        if (n) release(0, kKeyPieces);
         for (int j = 0; j < n; ++j) {
-            const int vi = j * kStepPieces + kKeyPieces;
-            for (int c = 0; c < 2; ++c) wait.warp(&bar.full[(vi + c) % kRing], ((vi + c) / kRing) & 1);
+            wait.warp(&bar.value_full[j & 1], (j >> 1) & 1);
             const int left = keys - j * kTile;
             if (left < kTile) {
                 // Rows past the request's keys belong to others or to nobody
                 // and may hold anything: a weight of zero would not hide a NaN.
                 for (int i = left * 16 + lane; i < kTile * 16; i += 32) {
-                    const int row = i >> 4, piece = (vi + (row >> 6)) % kRing;
+                    const int row = i >> 4, piece = (j * kStepPieces + kKeyPieces + (row >> 6)) % kRing;
                     ptx::sts_u4(ring + piece * kPiece + ((i >> 3) & 1) * (kPiece / 2) + (row & 63) * 128 + (i & 7) * 16,
                                 make_uint4(0, 0, 0, 0));
                 }
@@ -252,25 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int t = 0; t < 2; ++t) {
                 if (j < steps[t]) {
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait.warp(&bar.weight[t][half], j & 1);
-                        tc::fence_after();
-                        if (tc::elect()) {
-                            const uint64_t b = value_at + ((vi + half) % kRing) * (kPiece >> 4);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma_tmem(tmem + 256 + t * kValue, tmem + t * kTile + 32 * half + 8 * k, b + 128 * k,
-                                             sum_instr, j > 0 || half > 0 || k > 0);
-                            if (half == 1) tc::commit<1>(&bar.sum[t]);
-                        }
-                        __syncwarp();
-                    }
+                    sums(t, j, 0);
+                    sums(t, j, 1);
                 }
-                if (t == 1) release(vi, 2);
                 if (j + 1 < steps[t]) scores(t, j + 1);
             }
-            if (j + 1 < n) release((j + 1) * kStepPieces, kKeyPieces);
         }
         if (tc::elect()) {
             tc::commit<1>(&bar.end);
