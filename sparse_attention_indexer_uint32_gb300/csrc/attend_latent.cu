@@ -623,81 +623,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t sum_instr = tc::instruction(kBf16, kRows, 256, false, true);
             const uint64_t query_at = tc::operand(queries), key_at = tc::operand(keys), weight_at = tc::operand(weights),
                            value_at = tc::operand(values, kValuePiece);
-            // A group of the first product of tile `scored`, at most one ahead
-            // of the second (there are two score tiles), or a group of the
-            // second product of tile `summed`: whichever has its operands, so
-            // that neither waits behind the other's copies.
-            const auto ready = [](uint64_t* bar, int n) {
-                return __any_sync(~0u, ptx::mbar_test_wait(bar, static_cast<uint32_t>(n) & 1));
-            };
+            // The first product of tile n goes before the second of tile n - 1:
+            // while that runs, the keys' last third of tile n + 1 lands and the
+            // softmax of tile n is done (taken as their operands came instead,
+            // pages were 2 to 4 % slower).
             const int tiles = walk.left;
-            int scored = 0, summed = 0, kg = 0, vg = 0, tile = 0, segment = -1;
-            bool first[2] = {};  // whether tiles n - 1 and n, by n mod 2, begin their segments
-            uint32_t spins = 0;
-            uint64_t since = 0;
-            while (summed < tiles) {
-                if (summed < scored && (vg > 0 || ready(&sh.weight, summed)) && ready(&sh.value_full[vg], summed)) {
-                    const bool add = !first[summed & 1];
-                    tc::fence_after();
+            int n = 0, segment = 0;
+            bool add = false;  // whether the sums of tile n - 1 are added to
+            const auto sums = [&](int m) {
+                wait.warp(&sh.weight, static_cast<uint32_t>(m) & 1);
+                tc::fence_after();
+                for (int g = 0; g < kValueGroups; ++g) {
+                    wait.warp(&sh.value_full[g], static_cast<uint32_t>(m) & 1);
                     if (tc::elect()) {
 #pragma unroll
                         for (int a = 0; a < 2; ++a)  // values 128 a.. of each block's 256
 #pragma unroll
                             for (int k = 0; k < kHalf / 16; ++k)
-                                tc::mma<2>(tmem + 128 * a, weight_at + vg * (kWeightPiece >> 4) + 2 * k,
-                                           value_at + (2 * a * kValuePiece + vg * kHalf * 128 >> 4) + 128 * k, sum_instr,
-                                           add || vg > 0 || k > 0);
-                        tc::commit_pair(&sh.value_empty[vg]);
-                        if (vg == kValueGroups - 1) tc::commit_pair(&sh.sum);
+                                tc::mma<2>(tmem + 128 * a, weight_at + g * (kWeightPiece >> 4) + 2 * k,
+                                           value_at + ((2 * a * kValuePiece + g * kHalf * 128) >> 4) + 128 * k, sum_instr,
+                                           add || g > 0 || k > 0);
+                        tc::commit_pair(&sh.value_empty[g]);
+                        if (g == kValueGroups - 1) tc::commit_pair(&sh.sum);
                     }
                     __syncwarp();
-                    if (++vg == kValueGroups) {
-                        vg = 0;
-                        ++summed;
-                    }
-                    spins = 0;
-                    continue;
                 }
-                if (scored < tiles && scored - summed < 2) {
-                    if (tile == s.last) {
-                        walk.next(s);
-                        tile = s.first;
-                        ++segment;
+            };
+            for (; walk.next(s); ++segment) {
+                const int place = few ? segment & 1 : 0;
+                const uint32_t round = static_cast<uint32_t>(few ? segment >> 1 : segment) & 1;
+                const uint64_t q_at = query_at + place * (kPieces * query_piece >> 4);
+                for (int tile = s.first; tile < s.last; ++tile, ++n) {
+                    bool summed = n == 0;
+                    if (tile == s.first) {
+                        // Queries that are still on their way need not hold up
+                        // the last sums of the segment before.
+                        if (n > 0 && !__any_sync(~0u, ptx::mbar_test_wait(&sh.query_full[place], round))) {
+                            sums(n - 1);
+                            summed = true;
+                        }
+                        wait.warp(&sh.query_full[place], round);
                     }
-                    const int query_place = few ? segment & 1 : 0, query_round = few ? segment >> 1 : segment;
-                    if ((kg > 0 || tile > s.first ||
-                         __any_sync(~0u, ptx::mbar_test_wait(&sh.query_full[query_place],
-                                                             static_cast<uint32_t>(query_round) & 1))) &&
-                        ready(&sh.key_full[kg], scored)) {
-                        const uint32_t d = tmem + kScore + kHalf * (static_cast<uint32_t>(scored) & 1);
-                        const uint64_t q_at = query_at + query_place * (kPieces * query_piece >> 4);
-                        tc::fence_after();
+                    for (int g = 0; g < kKeyGroups; ++g) {
+                        wait.warp(&sh.key_full[g], static_cast<uint32_t>(n) & 1);
                         if (tc::elect()) {
 #pragma unroll
                             for (int k = 0; k < 4 * kGroupPieces; ++k) {
-                                const int c = kGroupPieces * kg + (k >> 2);
-                                tc::mma<2>(d, q_at + c * (query_piece >> 4) + 2 * (k & 3),
-                                           key_at + c * (kKeyPiece >> 4) + 2 * (k & 3), score_instr, (kg | k) != 0);
+                                const int c = kGroupPieces * g + (k >> 2);
+                                tc::mma<2>(tmem + kScore + kHalf * (n & 1), q_at + c * (query_piece >> 4) + 2 * (k & 3),
+                                           key_at + c * (kKeyPiece >> 4) + 2 * (k & 3), score_instr, (g | k) != 0);
                             }
-                            tc::commit_pair(&sh.key_empty[kg]);
-                            if (kg == kKeyGroups - 1) {
-                                tc::commit_pair(&sh.score[scored & 1]);
-                                if (tile == s.last - 1) tc::commit_pair(&sh.query_empty[query_place]);
+                            tc::commit_pair(&sh.key_empty[g]);
+                            if (g == kKeyGroups - 1) {
+                                tc::commit_pair(&sh.score[n & 1]);
+                                if (tile == s.last - 1) tc::commit_pair(&sh.query_empty[place]);
                             }
                         }
                         __syncwarp();
-                        if (++kg == kKeyGroups) {
-                            kg = 0;
-                            first[scored & 1] = tile == s.first;
-                            ++tile;
-                            ++scored;
-                        }
-                        spins = 0;
-                        continue;
                     }
+                    if (!summed) sums(n - 1);
+                    add = tile > s.first;
                 }
-                if (wait.idle(spins, since)) break;
             }
+            if (tiles > 0) sums(n - 1);
             if (tc::elect()) {
                 tc::commit<2>(&sh.end);
                 tc::Waits::drain(&sh.end, 0);
