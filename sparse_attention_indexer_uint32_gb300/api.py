@@ -96,6 +96,11 @@ def _is(t: torch.Tensor, dtype: torch.dtype, gpu: int, shape: tuple) -> bool:
     return t.dtype is dtype and t.get_device() == gpu and t.shape == shape and t.is_contiguous()
 
 
+def _line(t: torch.Tensor, n: int, gpu: int) -> bool:
+    """n int32 values in a row."""
+    return t.dtype is _I32 and t.numel() == n and t.get_device() == gpu and t.is_contiguous()
+
+
 class BlockTables(NamedTuple):
     """Outputs of :func:`block_tables` (int32 cuda); ``status`` holds the pages taken and the flag bits."""
 
@@ -130,14 +135,15 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     """Runs ``topk_block_tables``: writes the new pages into ``page_table`` ([batch, pages], in place) and returns
     the step's lengths, offsets and slot map (in ``out``, where the result of an earlier call is given)."""
     gpu, shape = context_lens.get_device(), page_table.shape
+    batch, num_free = shape[0] if shape else 0, free_pages.numel()
     if not (gpu >= 0 and len(shape) == 2 and page_table.dtype is _I32 and page_table.get_device() == gpu
-            and (shape[1] <= 1 or page_table.stride(1) == 1) and _is(context_lens, _I32, gpu, shape[:1])
-            and _is(new_lens, _I32, gpu, shape[:1]) and _is(free_pages, _I32, gpu, (free_pages.numel(),))
-            and (out is None or (_is(out[0], _I32, gpu, shape[:1]) and _is(out[1], _I32, gpu, (shape[0] + 1,))
-                                 and _is(out[2], _I32, gpu, (max_tokens,)) and _is(out[3], _I32, gpu, (max_tokens,))
-                                 and _is(out[4], _I32, gpu, (max_tokens,)) and _is(out[5], _I32, gpu, (2,))))):
+            and (shape[1] <= 1 or page_table.stride(1) == 1) and _line(context_lens, batch, gpu)
+            and _line(new_lens, batch, gpu) and _line(free_pages, num_free, gpu)
+            and (out is None or (_line(out[0], batch, gpu) and _line(out[1], batch + 1, gpu)
+                                 and _line(out[2], max_tokens, gpu) and _line(out[3], max_tokens, gpu)
+                                 and _line(out[4], max_tokens, gpu) and _line(out[5], 2, gpu)))):
         _check_tables(context_lens, new_lens, free_pages, page_table, max_tokens, out)
-    batch, pages = shape
+    pages = shape[1]
     if out is None:
         # One allocation; the token arrays start on 16 bytes, where the kernel writes four values at once.
         room = (max_tokens + 3) // 4 * 4
@@ -146,7 +152,7 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         out = BlockTables(buf[at:at + batch], buf[at + batch:at + 2 * batch + 1], buf[:max_tokens],
                           buf[room:room + max_tokens], buf[2 * room:2 * room + max_tokens], buf[at + 2 * batch + 1:])
     status = _c.topk_block_tables(
-        context_lens.data_ptr(), new_lens.data_ptr(), batch, page_size, free_pages.data_ptr(), free_pages.numel(),
+        context_lens.data_ptr(), new_lens.data_ptr(), batch, page_size, free_pages.data_ptr(), num_free,
         page_table.data_ptr(), page_table.stride(0) if batch > 1 else pages, pages, max_tokens, out[0].data_ptr(),
         out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), out[5].data_ptr(),
         _lib.stream_handle(stream, gpu))
@@ -177,17 +183,17 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     ``cache`` [num_slots, 576], normed by ``norm_weight`` [512] and rotated by ``cos_sin`` (float32
     [num_positions, 64]: cosines, sines) at ``positions``, where these are given."""
     gpu, dtype, shape, places = cache.get_device(), cache.dtype, rows.shape, cache.shape
-    code = _DTYPES.get(dtype)
+    code, tokens, positions_n = _DTYPES.get(dtype), shape[0] if shape else 0, 0 if cos_sin is None else cos_sin.shape[0]
     if not (gpu >= 0 and code is not None and rows.dtype is dtype and rows.get_device() == gpu and len(shape) == 2
             and len(places) == 2 and shape[1] == _WIDTH == places[1] and rows.stride(1) == 1 == cache.stride(1)
-            and _is(slots, _I32, gpu, shape[:1]) and (positions is None or _is(positions, _I32, gpu, shape[:1]))
+            and _line(slots, tokens, gpu) and (positions is None or _line(positions, tokens, gpu))
             and (norm_weight is None or _is(norm_weight, dtype, gpu, (_LATENT,)))
-            and (cos_sin is None or _is(cos_sin, _F32, gpu, (len(cos_sin), _ROPE)))):
+            and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))):
         _check_append(rows, slots, cache, norm_weight, cos_sin, positions)
     status = _c.topk_cache_append(
-        rows.data_ptr(), rows.stride(0) if shape[0] > 1 else _WIDTH, shape[0],
+        rows.data_ptr(), rows.stride(0) if tokens > 1 else _WIDTH, tokens,
         None if norm_weight is None else norm_weight.data_ptr(), eps, None if cos_sin is None else cos_sin.data_ptr(),
-        0 if cos_sin is None else len(cos_sin), None if positions is None else positions.data_ptr(), interleaved,
+        positions_n, None if positions is None else positions.data_ptr(), interleaved,
         slots.data_ptr(), cache.data_ptr(), cache.stride(0) if places[0] > 1 else _WIDTH, places[0], code,
         _lib.stream_handle(stream, gpu))
     if status:
@@ -232,7 +238,7 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
     code = _DTYPES.get(dtype)
     if not (code is not None and len(shape) == 3 and len(listed) == 2 and listed[0] == shape[0]
             and indices.dtype is _I32 and indices.get_device() == gpu and (listed[1] <= 1 or indices.stride(1) == 1)
-            and (seq_lens is None or _is(seq_lens, _I32, gpu, shape[:1]))
+            and (seq_lens is None or _line(seq_lens, shape[0], gpu))
             and _fits(q, cache, out, lse, gpu, dtype, shape)):
         if q.dim() != 3 or indices.dim() != 2 or indices.shape[0] != q.shape[0]:
             raise ValueError(f"q and indices must be [rows, heads, ..] and [rows, k]: got {tuple(q.shape)} and "
@@ -269,7 +275,7 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
     code = _DTYPES.get(dtype)
     if not (code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
             and page_table.dtype is _I32 and page_table.get_device() == gpu
-            and (listed[1] <= 1 or page_table.stride(1) == 1) and _is(seq_lens, _I32, gpu, shape[:1])
+            and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, shape[0], gpu)
             and _fits(q, cache, out, lse, gpu, dtype, shape)):
         if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
             raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
@@ -334,7 +340,7 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
             and k_nope.stride(2) == 1 and v.dtype is dtype and v.get_device() == gpu
             and v.shape == tokens + (shape[1], _VALUE) and v.stride(2) == 1 and k_rope.dtype is dtype
             and k_rope.get_device() == gpu and k_rope.shape == tokens + (_ROPE,) and k_rope.stride(1) == 1
-            and len(marks) == 1 and _is(cu_q, _I32, gpu, marks) and _is(cu_k, _I32, gpu, marks)
+            and len(marks) == 1 and _line(cu_q, marks[0], gpu) and _line(cu_k, marks[0], gpu)
             and (out is None or _is(out, dtype, gpu, shape[:2] + (_VALUE,)))
             and (lse is None or _is(lse, _F32, gpu, shape[:2]))):
         _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse)
