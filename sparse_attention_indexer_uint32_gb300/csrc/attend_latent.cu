@@ -218,20 +218,32 @@ struct Walk {
     }
 };
 
-// Slot of a position, -1 where it is not seen.
+// A position's slot on its way: the index or the page as it is loaded (-1 past
+// the row's end), looked at only when the slot is needed, so that the load's
+// latency passes behind other work.
 template <bool kPaged>
-__device__ __forceinline__ int slot_of(const LatentParams& p, int row, int length, int64_t at) {
-    if (at >= length) return -1;
-    if (!kPaged && p.indices) {
-        const int32_t s = p.indices[static_cast<int64_t>(row) * p.indices_stride + at];
-        return s < p.num_slots ? s : -1;
+struct Slot {
+    int32_t value, offset;
+
+    __device__ __forceinline__ void fetch(const LatentParams& p, int row, int length, int64_t at) {
+        value = -1;
+        offset = 0;
+        if (at >= length) return;
+        if (!kPaged && p.indices) {
+            value = p.indices[static_cast<int64_t>(row) * p.indices_stride + at];
+        } else {
+            const int pos = static_cast<int>(at);
+            value = p.table[static_cast<int64_t>(row) * p.table_stride + (pos >> p.log2_page)];
+            offset = pos & ((1 << p.log2_page) - 1);
+        }
     }
-    const int pos = static_cast<int>(at);
-    const int64_t s = (static_cast<int64_t>(p.table[static_cast<int64_t>(row) * p.table_stride + (pos >> p.log2_page)])
-                       << p.log2_page) +
-                      (pos & ((1 << p.log2_page) - 1));
-    return s >= 0 && s < p.num_slots ? static_cast<int>(s) : -1;
-}
+    // The slot, -1 where it is not seen.
+    __device__ __forceinline__ int get(const LatentParams& p) const {
+        if (!kPaged && p.indices) return value >= 0 && value < p.num_slots ? value : -1;
+        const int64_t s = (static_cast<int64_t>(value) << p.log2_page) + offset;
+        return s >= 0 && s < p.num_slots ? static_cast<int>(s) : -1;
+    }
+};
 
 // One slot a tile of a run, fetched two tiles ahead of its use: loads wait
 // behind the copies that are under way.
@@ -239,28 +251,27 @@ struct SlotAhead {
     const LatentParams& p;
     Walk& walk;
     Segment& s;
-    int at, tiles, tile, slot[2];
+    int at, tiles, tile;
+    Slot<false> slot[2];
     bool more;
 
     __device__ __forceinline__ SlotAhead(const LatentParams& p, Walk& walk, Segment& s, int at)
         : p(p), walk(walk), s(s), at(at), tiles(walk.left), more(walk.next(s)) {
         tile = s.first;
-        slot[0] = fetch();
-        slot[1] = fetch();
+        fetch(slot[0]);
+        fetch(slot[1]);
     }
-    __device__ __forceinline__ int fetch() {
-        if (!more) return -1;
-        const int x = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at);
-        if (++tile == s.last) {
+    __device__ __forceinline__ void fetch(Slot<false>& x) {
+        x.fetch(p, s.row, more ? s.length : 0, static_cast<int64_t>(tile) * kTile + at);
+        if (more && ++tile == s.last) {
             more = walk.next(s);
             tile = s.first;
         }
-        return x;
     }
     __device__ __forceinline__ int next() {
-        const int x = slot[0];
+        const int x = slot[0].get(p);
         slot[0] = slot[1];
-        slot[1] = fetch();
+        fetch(slot[1]);
         return x;
     }
 };
@@ -422,21 +433,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool more = walk.next(s);
         int tile = s.first;
         const bool mine = lane * box_rows < kHalf;
-        const auto fetch = [&]() {  // row of the cache at which box `lane` begins
-            const int x = mine ? slot_of<true>(p, s.row, s.length,
-                                               static_cast<int64_t>(tile) * kTile + rank * kHalf + lane * box_rows)
-                               : -1;
+        Slot<true> next;  // at which box `lane` of the next tile begins
+        const auto fetch = [&]() {
+            next.fetch(p, s.row, more && mine ? s.length : 0, static_cast<int64_t>(tile) * kTile + rank * kHalf + lane * box_rows);
+        };
+        const auto row_of = [&]() {  // outside the cache: copied as zeros
+            const int x = next.get(p);
             return x < 0 ? p.num_slots : x;
         };
-        int next_box = more ? fetch() : 0;
+        fetch();
         pair_ready();
         while (more && !wait.over()) {
-            const int box = next_box;
+            const int box = row_of();
             if (++tile == s.last) {
                 more = walk.next(s);
                 tile = s.first;
             }
-            if (more) next_box = fetch();
+            fetch();
             for (int g = 0; g < kKeyGroups; ++g) {
                 if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
                 if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], kGroupPieces * kKeyPiece);
@@ -450,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // The rows of the next tile come to L2 while this one's are used:
             // shared memory has room for one tile only.
             if (more && mine)
-                for (int c = 0; c < kPieces; ++c) tc::prefetch_2d(&maps.cache, 64 * c, next_box);
+                for (int c = 0, row = row_of(); c < kPieces; ++c) tc::prefetch_2d(&maps.cache, 64 * c, row);
         }
         if (n > 0 && wait.over())
             for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
@@ -459,20 +472,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int n = 0;
         bool more = walk.next(s);
         int tile = s.first;
-        const auto fetch = [&](int* slots) {  // slots lane, lane + 32, ..
+        Slot<true> next[4];  // slots lane, lane + 32, .. of the next tile
+        const auto fetch = [&]() {
+#pragma unroll
             for (int i = 0; i < 4; ++i)
-                slots[i] = slot_of<true>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
+                next[i].fetch(p, s.row, more ? s.length : 0, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
         };
-        int next_slots[4];
-        if (more) fetch(next_slots);
+        fetch();
         pair_ready();
         while (more && !wait.over()) {
-            const int slots[4] = {next_slots[0], next_slots[1], next_slots[2], next_slots[3]};
+            const int slots[4] = {next[0].get(p), next[1].get(p), next[2].get(p), next[3].get(p)};
             if (++tile == s.last) {
                 more = walk.next(s);
                 tile = s.first;
             }
-            if (more) fetch(next_slots);
+            fetch();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // as for selected slots
                 const uint32_t bits = __ballot_sync(~0u, slots[i] >= 0);
@@ -553,17 +567,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pair_ready();
         while (!over && walk.next(s))
             for (int tile = s.first; tile < s.last && !over; ++tile, ++n) {
-                int slots[2];
+                Slot<false> slots[2];
+#pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    slots[i] = slot_of<false>(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at + 32 * i);
+                    slots[i].fetch(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at + 32 * i);
                 // Once the copies of the tile before are under way; a tile
                 // whose own copies are needs no more help.
                 while (!over && __any_sync(~0u, sh.copied < n)) over = wait.idle(spins, since);
                 spins = 0;
                 if (__any_sync(~0u, sh.copied > n)) continue;
+#pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (slots[i] < 0) continue;
-                    const uint8_t* row = static_cast<const uint8_t*>(p.cache) + slots[i] * (2 * p.slot_stride);
+                    const int x = slots[i].get(p);
+                    if (x < 0) continue;
+                    const uint8_t* row = static_cast<const uint8_t*>(p.cache) + x * (2 * p.slot_stride);
                     for (int c = 0; c < kPieces; ++c) ptx::prefetch_l2(row + 128 * c);
                 }
                 __syncwarp();
