@@ -346,6 +346,8 @@ topk_status_t topk_attend_selected(const void* q, int64_t q_row_stride, int64_t 
  * count as max_seq_len, negative ones as 0).
  *   q                 device [batch][q_row_stride], query i at
  *                     i * q_query_stride, head h at h * q_head_stride.
+ * What slots past a request's length hold is not used; the rows of its own
+ * newest tokens, which its earlier queries do not see, must be finite.
  *   page_table        as in topk_transform; page_table_stride >=
  *                     ceil(max_seq_len / page_size).
  *   out               device [batch][queries][heads][512], contiguous, 32-byte

@@ -92,6 +92,17 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _empty(shape: tuple, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """New memory for a call on ``stream``: out of that stream's own pool, so that nothing else uses it meanwhile."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _lib.stream_handle(stream, device.index)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _is(t: torch.Tensor, dtype: torch.dtype, gpu: int, shape: tuple) -> bool:
     return t.dtype is dtype and t.get_device() == gpu and t.shape == shape and t.is_contiguous()
 
@@ -147,7 +158,7 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     if out is None:
         # One allocation; the token arrays start on 16 bytes, where the kernel writes four values at once.
         room = (max_tokens + 3) // 4 * 4
-        buf = torch.empty(3 * room + 2 * batch + 3, dtype=_I32, device=context_lens.device)
+        buf = _empty((3 * room + 2 * batch + 3,), _I32, context_lens.device, stream)
         at = 3 * room
         out = BlockTables(buf[at:at + batch], buf[at + batch:at + 2 * batch + 1], buf[:max_tokens],
                           buf[room:room + max_tokens], buf[2 * room:2 * room + max_tokens], buf[at + 2 * batch + 1:])
@@ -221,10 +232,10 @@ def _fits(q, cache, out, lse, gpu, dtype, shape) -> bool:
             and (lse is None or _is(lse, _F32, gpu, shape[:-1])))
 
 
-def _attend_workspace(workspace, batch, queries, heads, device):
+def _attend_workspace(workspace, batch, queries, heads, device, stream):
     need = _c.topk_attend_workspace_bytes(batch, queries, heads)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty((need,), torch.uint8, device, stream)
     return workspace
 
 
@@ -249,10 +260,10 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
         _check_attend(q, cache, out, lse)
     rows, heads, _ = shape
     if out is None:
-        out = torch.empty((rows, heads, _LATENT), dtype=dtype, device=q.device)
+        out = _empty((rows, heads, _LATENT), dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((rows, heads), dtype=_F32, device=q.device)
-    workspace = _attend_workspace(workspace, rows, 1, heads, q.device)
+        lse = _empty((rows, heads), _F32, q.device, stream)
+    workspace = _attend_workspace(workspace, rows, 1, heads, q.device, stream)
     slots = cache.shape[0]
     status = _c.topk_attend_selected(
         q.data_ptr(), _step(q, 0, _WIDTH), _step(q, 1, _WIDTH), cache.data_ptr(),
@@ -292,10 +303,10 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
     elif max_seq_len > listed[1] * page_size:
         raise ValueError(f"max_seq_len {max_seq_len} is over {listed[1]} pages of {page_size}")
     if out is None:
-        out = torch.empty((batch, queries, heads, _LATENT), dtype=dtype, device=q.device)
+        out = _empty((batch, queries, heads, _LATENT), dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((batch, queries, heads), dtype=_F32, device=q.device)
-    workspace = _attend_workspace(workspace, batch, queries, heads, q.device)
+        lse = _empty((batch, queries, heads), _F32, q.device, stream)
+    workspace = _attend_workspace(workspace, batch, queries, heads, q.device, stream)
     slots = cache.shape[0]
     status = _c.topk_attend_paged(
         q.data_ptr(), _step(q, 0, _WIDTH), _step(q, 1, _WIDTH), _step(q, 2, _WIDTH), cache.data_ptr(),
@@ -346,9 +357,9 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
         _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse)
     total_q, heads, _ = shape
     if out is None:
-        out = torch.empty((total_q, heads, _VALUE), dtype=dtype, device=q.device)
+        out = _empty((total_q, heads, _VALUE), dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((total_q, heads), dtype=_F32, device=q.device)
+        lse = _empty((total_q, heads), _F32, q.device, stream)
     status = _c.topk_attend_prompt(
         q.data_ptr(), _step(q, 0, _NOPE + _ROPE), _step(q, 1, _NOPE + _ROPE), k_nope.data_ptr(),
         _step(k_nope, 0, _NOPE), _step(k_nope, 1, _NOPE), k_rope.data_ptr(), _step(k_rope, 0, _ROPE), v.data_ptr(),

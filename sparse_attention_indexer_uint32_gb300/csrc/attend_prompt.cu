@@ -109,12 +109,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Blocks before this request's: of the requests that come first.
             const int mine = (q_end - q_start + kBlockRows - 1) / kBlockRows, length = k_end - k_start;
-            int ahead = before;
+            int ahead = 0;
+            if (p.batch <= 32) {
 #pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-                const int blocks = __shfl_sync(~0u, mine, i), other = __shfl_sync(~0u, length, i);
-                const bool first = p.batch <= 32 ? other > length || (other == length && i < lane) : i < lane;
-                if (first) ahead += blocks;
+                for (int i = 0; i < 32; ++i) {
+                    const int blocks = __shfl_sync(~0u, mine, i), other = __shfl_sync(~0u, length, i);
+                    if (other > length || (other == length && i < lane)) ahead += blocks;
+                }
+            } else {
+                int upto = mine;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(~0u, upto, d);
+                    if (lane >= d) upto += x;
+                }
+                ahead = before + upto - mine;
             }
             const unsigned here = __ballot_sync(~0u, index >= ahead && index < ahead + mine);
             if (here) {

@@ -115,6 +115,24 @@ def test_attend_prompt_refusals(lib):
         assert call(**bad) == lib.TOPK_EALIGN, bad
 
 
+def test_read_attend_flags_refusal(lib):
+    assert lib.library().topk_read_attend_flags(None, 0, None) == lib.TOPK_EINVAL
+
+
+def test_cpu_tensors_are_refused(api):
+    i32, bf = torch.zeros(3, dtype=torch.int32), dict(dtype=torch.bfloat16)
+    cache, table = torch.zeros(10, 576, **bf), torch.zeros(3, 4, dtype=torch.int32)
+    calls = (lambda: api.block_tables(i32, i32, i32, table, 16, 8),
+             lambda: api.cache_append(torch.zeros(3, 576, **bf), i32, cache),
+             lambda: api.attend_selected(torch.zeros(3, 2, 576, **bf), cache, table, 0.1),
+             lambda: api.attend_paged(torch.zeros(3, 1, 2, 576, **bf), cache, i32, table, 16, 0.1),
+             lambda: api.attend_prompt(torch.zeros(5, 2, 192, **bf), torch.zeros(6, 2, 128, **bf),
+                                       torch.zeros(6, 64, **bf), torch.zeros(6, 2, 128, **bf), i32, i32, 0.1))
+    for call in calls:
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()
+
+
 def test_tensor_checks(api):
     """The conveniences name the argument that is wrong (CPU tensors: nothing reaches a kernel)."""
     i32 = torch.zeros(3, dtype=torch.int32)

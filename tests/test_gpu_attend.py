@@ -312,3 +312,43 @@ def test_selection_feeds_attention(api):
     out, lse, _ = api.attend_selected(q, cache, slots, SCALE, seq_lens=lens)
     want, _, _ = oracle.topk_transform(wl.scores, wl.seq_lens, wl.page_table, wl.page_size, wl.k)
     check_selected(q, cache, torch.from_numpy(want).cuda(), None, out, lse)
+
+
+def test_prompt_without_keys_and_many_requests(api):
+    """No key at all; more requests than the 32 that are put in order of their length."""
+    q, kn, kr, v, cu_q, cu_k = prompt_inputs(71, [200, 3], [0, 0], 2, torch.bfloat16)
+    out, lse = api.attend_prompt(q, kn, kr, v, i32(cu_q), i32(cu_k), SCALE)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    lens = [(7 * r) % 60 for r in range(70)]
+    q, kn, kr, v, cu_q, cu_k = prompt_inputs(72, lens, lens[::-1], 1, torch.float16)
+    out, lse = api.attend_prompt(q, kn, kr, v, i32(cu_q), i32(cu_k), SCALE, causal=False)
+    check_prompt(q, kn, kr, v, cu_q, cu_k, False, out, lse)
+
+
+def test_selected_odd_heads_in_parts(api):
+    """Rows that several blocks share, with numbers of heads that are no multiple of four."""
+    cache = randn(81, 9000, WIDTH, dtype=torch.float16)
+    for heads in (1, 7, 33, 63, 65, 127):
+        q = randn(82, 2, heads, WIDTH, dtype=torch.float16)
+        indices = i32(torch.randperm(9000, device="cuda")[:3001].repeat(2, 1))
+        out, lse, _ = api.attend_selected(q, cache, indices, SCALE)
+        check_selected(q, cache, indices, None, out, lse)
+
+
+def test_query_layouts_of_several_queries(api):
+    """Queries whose heads are not next to their neighbours' (copied a row at a time) and heads before queries."""
+    page, batch = 64, 3
+    table = i32(torch.arange(batch * 5, device="cuda").reshape(batch, 5))
+    cache, lens = randn(83, batch * 5 * page, WIDTH), i32([300, 2, 190])
+    wide = randn(84, batch, 3, 12, WIDTH)
+    for q in (wide[:, :, :10], wide.transpose(1, 2)[:, :6]):
+        out, lse, _ = api.attend_paged(q, cache, lens, table, page, SCALE)
+        check_paged(q, cache, lens, table, page, out, lse)
+
+
+def test_no_wait_gave_up(api):
+    """The flag word of the attention kernels, after everything above."""
+    from sparse_attention_indexer_uint32_gb300 import _lib
+
+    assert _lib.topk_read_attend_flags() == 0
+    assert _lib.topk_read_attend_flags(clear=True) == 0
