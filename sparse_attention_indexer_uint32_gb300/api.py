@@ -1,6 +1,7 @@
 """Tensor-level conveniences over the C ABI (allocation and marshalling only)."""
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple
 
 import torch
@@ -78,11 +79,6 @@ def _whole(shape: tuple, **tensors) -> None:
 def _on_gpu(t: torch.Tensor) -> None:
     if not t.is_cuda:
         raise ValueError(f"the tensors must be on a GPU: got {t.device}")
-
-
-def _step(t: torch.Tensor, dim: int, least: int) -> int:
-    """Stride of a dimension; `least` where there is one entry, whose stride means nothing."""
-    return t.stride(dim) if t.shape[dim] > 1 else least
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -223,20 +219,29 @@ def _check_attend(q, cache, out, lse):
     _on_gpu(q)
 
 
-def _fits(q, cache, out, lse, gpu, dtype, shape) -> bool:
-    """Whether they are what both cache attentions take."""
-    rows = cache.shape
-    return (gpu >= 0 and shape[-1] == _WIDTH and q.stride(-1) == 1 and cache.dtype is dtype
-            and cache.get_device() == gpu and len(rows) == 2 and rows[1] == _WIDTH and cache.stride(1) == 1
-            and (out is None or _is(out, dtype, gpu, shape[:-1] + (_LATENT,)))
-            and (lse is None or _is(lse, _F32, gpu, shape[:-1])))
+def _fits(cache, places, out, lse, gpu, dtype, lead) -> bool:
+    """Whether they are what both cache attentions take; ``lead``: q's dimensions but the last."""
+    return (gpu >= 0 and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
+            and places[1] == _WIDTH and cache.stride(1) == 1
+            and (out is None or _is(out, dtype, gpu, lead + (_LATENT,)))
+            and (lse is None or _is(lse, _F32, gpu, lead)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(batch: int, queries: int, heads: int) -> int:
+    return _lib.topk_attend_workspace_bytes(batch, queries, heads)
 
 
 def _attend_workspace(workspace, batch, queries, heads, device, stream):
-    need = _c.topk_attend_workspace_bytes(batch, queries, heads)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = _empty((need,), torch.uint8, device, stream)
-    return workspace
+    """The workspace and its bytes."""
+    need = _workspace_bytes(batch, queries, heads)
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {device}: got {workspace.device}")
+        room = workspace.numel() * workspace.element_size()
+        if room >= need:
+            return workspace, room
+    return _empty((need,), torch.uint8, device, stream), need
 
 
 def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor, scale: float,
@@ -245,12 +250,13 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
     """Runs ``topk_attend_selected``: ``q`` [rows, heads, 576] over the slots ``indices`` [rows, k] (int32, as
     :func:`topk_transform` writes them) of ``cache`` [num_slots, 576].  ``seq_lens`` [rows], where given, bounds
     the slots looked at.  Returns ``(out [rows, heads, 512], lse [rows, heads], workspace)``."""
-    gpu, dtype, shape, listed = q.get_device(), q.dtype, q.shape, indices.shape
+    gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, indices.shape, cache.shape, q.stride()
     code = _DTYPES.get(dtype)
     if not (code is not None and len(shape) == 3 and len(listed) == 2 and listed[0] == shape[0]
-            and indices.dtype is _I32 and indices.get_device() == gpu and (listed[1] <= 1 or indices.stride(1) == 1)
+            and shape[2] == _WIDTH and steps[2] == 1 and indices.dtype is _I32 and indices.get_device() == gpu
+            and (listed[1] <= 1 or indices.stride(1) == 1)
             and (seq_lens is None or _line(seq_lens, shape[0], gpu))
-            and _fits(q, cache, out, lse, gpu, dtype, shape)):
+            and _fits(cache, places, out, lse, gpu, dtype, (shape[0], shape[1]))):
         if q.dim() != 3 or indices.dim() != 2 or indices.shape[0] != q.shape[0]:
             raise ValueError(f"q and indices must be [rows, heads, ..] and [rows, k]: got {tuple(q.shape)} and "
                              f"{tuple(indices.shape)}")
@@ -263,14 +269,14 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
         out = _empty((rows, heads, _LATENT), dtype, q.device, stream)
     if lse is None:
         lse = _empty((rows, heads), _F32, q.device, stream)
-    workspace = _attend_workspace(workspace, rows, 1, heads, q.device, stream)
-    slots = cache.shape[0]
+    workspace, room = _attend_workspace(workspace, rows, 1, heads, q.device, stream)
+    slots = places[0]
     status = _c.topk_attend_selected(
-        q.data_ptr(), _step(q, 0, _WIDTH), _step(q, 1, _WIDTH), cache.data_ptr(),
+        q.data_ptr(), steps[0] if rows > 1 else _WIDTH, steps[1] if heads > 1 else _WIDTH, cache.data_ptr(),
         cache.stride(0) if slots > 1 else _WIDTH, slots, indices.data_ptr(),
         indices.stride(0) if rows > 1 else listed[1], None if seq_lens is None else seq_lens.data_ptr(), rows, heads,
-        listed[1], scale, code, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _lib.stream_handle(stream, gpu))
+        listed[1], scale, code, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room,
+        _lib.stream_handle(stream, gpu))
     if status:
         _lib.check("topk_attend_selected", status)
     return out, lse, workspace
@@ -282,12 +288,12 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
     """Runs ``topk_attend_paged``: ``q`` [batch, queries, heads, 576], the newest tokens' queries, over each
     request's positions through ``page_table`` [batch, pages].  Returns ``(out [batch, queries, heads, 512],
     lse [batch, queries, heads], workspace)``."""
-    gpu, dtype, shape, listed = q.get_device(), q.dtype, q.shape, page_table.shape
+    gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
     code = _DTYPES.get(dtype)
     if not (code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
-            and page_table.dtype is _I32 and page_table.get_device() == gpu
+            and shape[3] == _WIDTH and steps[3] == 1 and page_table.dtype is _I32 and page_table.get_device() == gpu
             and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, shape[0], gpu)
-            and _fits(q, cache, out, lse, gpu, dtype, shape)):
+            and _fits(cache, places, out, lse, gpu, dtype, (shape[0], shape[1], shape[2]))):
         if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
             raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
                              f"{tuple(q.shape)} and {tuple(page_table.shape)}")
@@ -306,13 +312,13 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
         out = _empty((batch, queries, heads, _LATENT), dtype, q.device, stream)
     if lse is None:
         lse = _empty((batch, queries, heads), _F32, q.device, stream)
-    workspace = _attend_workspace(workspace, batch, queries, heads, q.device, stream)
-    slots = cache.shape[0]
+    workspace, room = _attend_workspace(workspace, batch, queries, heads, q.device, stream)
+    slots = places[0]
     status = _c.topk_attend_paged(
-        q.data_ptr(), _step(q, 0, _WIDTH), _step(q, 1, _WIDTH), _step(q, 2, _WIDTH), cache.data_ptr(),
-        cache.stride(0) if slots > 1 else _WIDTH, slots, seq_lens.data_ptr(), page_table.data_ptr(),
-        page_table.stride(0) if batch > 1 else listed[1], page_size, max_seq_len, batch, queries, heads, scale, code,
-        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        q.data_ptr(), steps[0] if batch > 1 else _WIDTH, steps[1] if queries > 1 else _WIDTH,
+        steps[2] if heads > 1 else _WIDTH, cache.data_ptr(), cache.stride(0) if slots > 1 else _WIDTH, slots,
+        seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else listed[1], page_size,
+        max_seq_len, batch, queries, heads, scale, code, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room,
         _lib.stream_handle(stream, gpu))
     if status:
         _lib.check("topk_attend_paged", status)
@@ -345,26 +351,30 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
     [total_k, 64], ``v`` [total_k, heads, 128], requests by the offsets ``cu_q`` and ``cu_k`` [batch + 1].
     Returns ``(out [total_q, heads, 128], lse [total_q, heads])``."""
     gpu, dtype, shape, marks = q.get_device(), q.dtype, q.shape, cu_q.shape
-    code, tokens = _DTYPES.get(dtype), v.shape[:1]
-    if not (gpu >= 0 and code is not None and len(shape) == 3 and shape[2] == _NOPE + _ROPE and q.stride(2) == 1
-            and k_nope.dtype is dtype and k_nope.get_device() == gpu and k_nope.shape == tokens + (shape[1], _NOPE)
-            and k_nope.stride(2) == 1 and v.dtype is dtype and v.get_device() == gpu
-            and v.shape == tokens + (shape[1], _VALUE) and v.stride(2) == 1 and k_rope.dtype is dtype
-            and k_rope.get_device() == gpu and k_rope.shape == tokens + (_ROPE,) and k_rope.stride(1) == 1
+    code, tokens = _DTYPES.get(dtype), k_rope.shape[0] if k_rope.dim() else 0
+    q_step, k_step, r_step, v_step = q.stride(), k_nope.stride(), k_rope.stride(), v.stride()
+    if not (gpu >= 0 and code is not None and len(shape) == 3 and shape[2] == _NOPE + _ROPE
+            and k_nope.dtype is dtype and k_nope.get_device() == gpu and k_nope.shape == (tokens, shape[1], _NOPE)
+            and v.dtype is dtype and v.get_device() == gpu and v.shape == (tokens, shape[1], _VALUE)
+            and k_rope.dtype is dtype and k_rope.get_device() == gpu and k_rope.shape == (tokens, _ROPE)
+            and q_step[2] == k_step[2] == r_step[1] == v_step[2] == 1
             and len(marks) == 1 and _line(cu_q, marks[0], gpu) and _line(cu_k, marks[0], gpu)
-            and (out is None or _is(out, dtype, gpu, shape[:2] + (_VALUE,)))
-            and (lse is None or _is(lse, _F32, gpu, shape[:2]))):
+            and (out is None or _is(out, dtype, gpu, (shape[0], shape[1], _VALUE)))
+            and (lse is None or _is(lse, _F32, gpu, (shape[0], shape[1])))):
         _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse)
     total_q, heads, _ = shape
     if out is None:
         out = _empty((total_q, heads, _VALUE), dtype, q.device, stream)
     if lse is None:
         lse = _empty((total_q, heads), _F32, q.device, stream)
+    # The stride of a dimension of one entry means nothing.
+    many_q, many_k, many_heads = total_q > 1, tokens > 1, heads > 1
     status = _c.topk_attend_prompt(
-        q.data_ptr(), _step(q, 0, _NOPE + _ROPE), _step(q, 1, _NOPE + _ROPE), k_nope.data_ptr(),
-        _step(k_nope, 0, _NOPE), _step(k_nope, 1, _NOPE), k_rope.data_ptr(), _step(k_rope, 0, _ROPE), v.data_ptr(),
-        _step(v, 0, _VALUE), _step(v, 1, _VALUE), cu_q.data_ptr(), cu_k.data_ptr(), marks[0] - 1, total_q, tokens[0],
-        heads, scale, causal, code, out.data_ptr(), lse.data_ptr(), _lib.stream_handle(stream, gpu))
+        q.data_ptr(), q_step[0] if many_q else _NOPE + _ROPE, q_step[1] if many_heads else _NOPE + _ROPE,
+        k_nope.data_ptr(), k_step[0] if many_k else _NOPE, k_step[1] if many_heads else _NOPE, k_rope.data_ptr(),
+        r_step[0] if many_k else _ROPE, v.data_ptr(), v_step[0] if many_k else _VALUE,
+        v_step[1] if many_heads else _VALUE, cu_q.data_ptr(), cu_k.data_ptr(), marks[0] - 1, total_q, tokens, heads,
+        scale, causal, code, out.data_ptr(), lse.data_ptr(), _lib.stream_handle(stream, gpu))
     if status:
         _lib.check("topk_attend_prompt", status)
     return out, lse
