@@ -77,11 +77,14 @@ def measured_peak():
 
 
 def source_digest() -> str:
-    """Digest of the CUDA sources' code (comments and blank space left out, so
-    that a comment edit keeps a profile valid)."""
+    """Digest of the selection's CUDA sources (comments and blank space left out, so
+    that a comment edit keeps a profile valid; without the files of the serving
+    operators around it, which no timed kernel here is built from)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "sparse_attention_indexer_uint32_gb300", "csrc")
     for name in sorted(os.listdir(csrc)):
+        if name.startswith(("attend_", "serve_", "tc.", "tensor_map.")):
+            continue
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
