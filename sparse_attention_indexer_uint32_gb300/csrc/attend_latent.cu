@@ -33,6 +33,13 @@
 // joins them, in the order of the slots (no atomics: equal calls give equal
 // bits).
 //
+// Measured (with the join): 16 rows of 32768 to 131072 tokens, pages of 64, 128
+// heads 301 us, 5.0 TB/s (74 % of the measured copy rate) and 1.21 PFLOP/s, bound
+// by the copies' way into shared memory and, for long calls, the power limit;
+// 2048 rows of up to 512 slots, 16 heads 245 us, 4.9 TB/s; 128 rows of 2048 slots,
+// 128 heads 84 us, of which about 8 us pass before the first product and 11 in the
+// join; one such row 14.5 us, four fifths of it waiting for memory in turn.
+//
 // Warps of each block: 0-3 softmax and results (thread t: row t & 63, half t >> 6
 // of the tile's slots, values 256 (t >> 6).. of the sums), 4 products (first
 // block only), 5 and 8 copies for the first product, 6 and 9 for the second, 7

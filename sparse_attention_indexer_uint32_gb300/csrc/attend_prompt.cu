@@ -17,6 +17,14 @@
 // cores work on the other tile.  Shared memory: 96 KB of queries, and a ring of
 // eight 16 KB pieces (three of keys and two of values per step).
 //
+// Measured: a prompt of 8192 tokens, 32 heads, causal 478 us, 1.44 PFLOP/s (75 %
+// of the measured burst rate, 84 % of the sustained one, at the power limit); 8
+// pieces of up to 1024 tokens after up to 4096 cached ones, 16 heads 104 us.  A
+// step takes 3150 cycles for 2560 of products: the first product reads 128 bytes a
+// cycle from shared memory, all there is, beside the copies' writes (92 cycles in
+// place of 64).  Pairs of blocks with products of M = 256, which read less, were 3 %
+// faster on the one prompt and 14 % slower on the pieces (blocks of 512 queries).
+//
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one query a thread), 8 products,
 // 9 copies.  The second product starts on the first half of a step's weights
 // while the second half is being computed.

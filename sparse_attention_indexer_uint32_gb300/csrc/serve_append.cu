@@ -7,8 +7,9 @@
 // row is read once and written once: 1152 + 256 + 1152 bytes a token, bound by
 // memory at large counts and by the launch at small ones.  Each warp walks
 // several rows with the weight kept, the row after the next and the next row's
-// cosines under way (a warp for one row or two took 43 us for 65536 rows: the
-// weight's second reading filled the L1 path).
+// cosines under way: 65536 rows take 31.6 us, 5.3 TB/s or 79 % of the measured
+// copy rate (a warp for one row or two took 43 us, the weight's second reading
+// filled the L1 path); 64 rows 7.9 us a call, most of it the host's.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -11,7 +11,10 @@
 // 12 written per token), so there is one launch and no pass between blocks:
 // every block scans all requests itself (4096 at a time, 4 per thread, kept
 // as two arrays of sums in shared memory) and writes its own slice of the
-// outputs, finding a token's request by bisection in shared memory.
+// outputs, finding the request of four neighbouring tokens by one bisection in
+// shared memory.  32 requests with a token each 8.7 us a call, most of it the
+// host's; 4096 requests with 1.05 M tokens in buffers for 1.18 M 11.6 us
+// (one token a thread: 15.3 us).
 #include <cuda_runtime.h>
 
 #include <cstdint>
