@@ -42,21 +42,46 @@ cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<bool>& done) {
 
 // Launches a kernel that may be placed before the kernel ahead of it in the
 // stream has ended; it waits (griddepcontrol.wait) before its first access.
+// `cluster`: blocks of a cluster, 0 for what the kernel itself says.
 template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream,
-                         const Args&... args) {
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_early_clusters(void (*kernel)(Params...), dim3 grid, int cluster, int threads, size_t shared,
+                                  cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = shared;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
     return e == cudaSuccess ? cudaGetLastError() : e;
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream,
+                         const Args&... args) {
+    return launch_early_clusters(kernel, grid, 0, threads, shared, stream, args...);
+}
+
+// Clusters of a kernel that the current device holds at once.
+template <typename Kernel>
+cudaError_t clusters_at_once(int* count, Kernel kernel, int threads, size_t shared, int cluster) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
 }
 
 struct TablesParams {

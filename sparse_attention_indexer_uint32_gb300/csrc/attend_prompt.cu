@@ -29,6 +29,11 @@
 // place of 64).  Pairs of blocks with products of M = 256, which read less, were 3 %
 // faster on the one prompt and 14 % slower on the pieces (blocks of 512 queries).
 //
+// With few pieces of work and long keys the blocks of a cluster share a piece:
+// each takes a range of its keys, and the sums are joined through the cluster's
+// shared memory, a row's parts in the order of the keys (one query of 16 heads on
+// 8192 keys: 115 us by a block a piece, 32 by six).
+//
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (one query a thread), 8 products,
 // 9 copies, 10 finds the next piece of work.  The second product starts on the
 // first half of a step's weights while the second half is being computed.
@@ -54,16 +59,23 @@ constexpr int kKeyPieces = 3, kStepPieces = 5;
 constexpr int kThreads = 352;
 constexpr uint32_t kColumns = 512;
 constexpr float kLag = 8.f;
+constexpr int kMaxSplit = 8;   // blocks of a cluster
+// Up to 4 steps are not shared (8 heads of 512 tokens: 16.4 us alone, 18.4 in two
+// parts); longer ones are, in parts of 2 steps or more (4 requests of 64 queries
+// on 1024 keys: 22.5 us alone, 18.4 in parts of 4 steps, 16.4 in parts of 2).
+constexpr int kAloneSteps = 4, kLeastSteps = 2;
 
 struct PromptMaps {
     CUtensorMap q, k_nope, k_rope, v;
 };
 
-// A piece of work: 256 queries of one head.
+// A piece of work: 256 queries of one head and, in a cluster that shares it, a
+// range of its keys: those from range.z on, as many steps as `most`.
 struct Item {
     int4 range;     // the request's first query, the end of its queries, the same of its keys
     int32_t block;  // of the request's queries, -1: there is no more work
     int32_t head;
+    int32_t most, parts;  // blocks that share it
 
     __device__ __forceinline__ int first(int t) const { return range.x + block * kBlockRows + t * kTile; }  // query of tile t
     __device__ __forceinline__ int keys() const { return range.w - range.z; }
@@ -73,7 +85,7 @@ struct Item {
     }
     __device__ __forceinline__ int steps(bool causal, int t) const {
         const int last = min(first(t) + kTile, range.y) - 1;
-        return last < first(t) ? 0 : (seen(causal, last) + kTile - 1) / kTile;
+        return last < first(t) ? 0 : min((seen(causal, last) + kTile - 1) / kTile, most);
     }
 };
 
@@ -152,10 +164,83 @@ struct Barriers {
 };
 constexpr int kSmem = 6 * kPiece + kRing * kPiece + static_cast<int>(sizeof(Barriers)) + 1024;
 
+// All threads of a cluster whose blocks have taken a part of the same piece of
+// work each.  The parts' sums go to shared memory (queries, keys and values are
+// not needed any more) as [128 / 4][256 rows] float4 and (maximum, sum) by row;
+// then each thread of the first eight warps joins 16 values of a row at a time,
+// taken in turn by the whole cluster.
 template <bool kBf16>
+__device__ __forceinline__ void join(const PromptParams& p, const Item& w, uint32_t base, uint32_t sums, float m, float l,
+                                     int split) {
+    const int warp = threadIdx.x >> 5, rows = min(w.range.y - w.first(0), kBlockRows);
+    const uint32_t stats = base + kBlockRows * kValue * 4;
+    if (warp < 8 && (warp << 5) < rows) {
+        const uint32_t from = sums + (static_cast<uint32_t>(warp & 3) << 21) + (warp >> 2) * kValue;
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stats + 8 * threadIdx.x), "f"(m), "f"(l) : "memory");
+        if (w.steps(p.causal, warp >> 2)) {
+#pragma unroll 1
+            for (int c = 0; c < kValue / 32; ++c) {
+                uint32_t o[32];
+                tc::load32(from + 32 * c, o);
+                tc::wait_load();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    ptx::sts_u4(base + ((8 * c + i) * kBlockRows + threadIdx.x) * 16,
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+            }
+        }
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+    constexpr int kColumns = kValue / 16;
+    const int rank = static_cast<int>(ptx::cluster_ctarank());
+    if (warp < 8)
+        for (int unit = rank * 256 + static_cast<int>(threadIdx.x); unit < rows * kColumns; unit += split * 256) {
+            const int r = unit % rows, c = unit / rows;
+            float2 part[kMaxSplit];
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kMaxSplit; ++i)
+                if (i < w.parts) {
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                                 : "=f"(part[i].x), "=f"(part[i].y)
+                                 : "r"(ptx::map_rank(stats + 8 * r, i)));
+                    top = fmaxf(top, part[i].x);
+                }
+            const float shift = top == -INFINITY ? 0.f : top;
+            float sum = 0.f, o[16] = {};
+#pragma unroll
+            for (int i = 0; i < kMaxSplit; ++i) {
+                if (i >= w.parts || part[i].y == 0.f) continue;  // a part that saw nothing
+                const uint32_t at = ptx::map_rank(base + (4 * c * kBlockRows + r) * 16, i);
+                const float by = exp2f(part[i].x - shift);
+                sum += part[i].y * by;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 x = ptx::ld_cluster_v4(at + k * kBlockRows * 16);
+                    o[4 * k] += __uint_as_float(x.x) * by;
+                    o[4 * k + 1] += __uint_as_float(x.y) * by;
+                    o[4 * k + 2] += __uint_as_float(x.z) * by;
+                    o[4 * k + 3] += __uint_as_float(x.w) * by;
+                }
+            }
+            const float by = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t at = static_cast<int64_t>(w.first(0) + r) * p.heads + w.head;
+            uint32_t pairs[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) pairs[k] = tc::pack<kBf16>(o[2 * k] * by, o[2 * k + 1] * by);
+            tc::store_v8(static_cast<uint16_t*>(p.out) + at * kValue + 16 * c, pairs);
+            if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        }
+    __syncwarp();
+    ptx::cluster_sync();  // no block ends while others read its parts
+}
+
+// kSplit: each cluster of `split` blocks takes one piece of work.
+template <bool kBf16, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const PromptParams p, const __grid_constant__ PromptMaps maps, uint32_t* flags, float scale_log2,
-                  bool negate) {
+                  bool negate, int split) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t queries = base, ring = base + 6 * kPiece;
@@ -209,22 +294,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         return !wait.over() && item.block >= 0;
     };
 
+    float m_part = -INFINITY, l_part = 0.f;  // what a softmax thread brings to the join
     if (warp == 10) {
         // Pieces are dealt out in turn, every other round backwards, so that
         // no block gets the longest of each.
         for (int k = 0;; ++k) {
             if (k >= 2) wait.warp(&bar.item_empty[k & 1], ((k >> 1) - 1) & 1);
-            const int64_t in_round = k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-            const int64_t number = static_cast<int64_t>(k) * gridDim.x + in_round, index = number / p.heads;
+            const int takers = static_cast<int>(gridDim.x) / split, taker = static_cast<int>(blockIdx.x) / split;
+            const int in_round = k & 1 ? takers - 1 - taker : taker;
+            const int64_t number = static_cast<int64_t>(k) * takers + in_round, index = number / p.heads;
             int4 range;
             int block = -1;
-            if (index <= p.total_q) find(p, lane, static_cast<int>(index), range, block);
+            if ((!kSplit || k == 0) && index <= p.total_q) find(p, lane, static_cast<int>(index), range, block);
+            Item item = {range, block, static_cast<int32_t>(number % p.heads), INT32_MAX, 1};
+            if (kSplit && block >= 0) {
+                const int rank = static_cast<int>(blockIdx.x) % split;
+                const int steps = max(item.steps(p.causal, 0), item.steps(p.causal, 1));
+                item.parts = steps > kAloneSteps ? min(split, (steps + kLeastSteps - 1) / kLeastSteps) : 1;
+                item.most = (steps + item.parts - 1) / item.parts;
+                item.range.z = static_cast<int32_t>(
+                    min(static_cast<int64_t>(range.z) + static_cast<int64_t>(rank) * item.most * kTile, static_cast<int64_t>(range.w)));
+                if (rank >= item.parts) {
+                    item.most = 0;  // joins in the join only
+                    if (item.parts == 1) item.block = -1;
+                }
+            }
             if (lane == 0) {
-                bar.item[k & 1] = {range, block, static_cast<int32_t>(number % p.heads)};
+                bar.item[k & 1] = item;
                 ptx::mbar_arrive(&bar.item_full[k & 1]);
             }
             __syncwarp();
-            if (block < 0 || wait.over()) break;
+            if (item.block < 0 || wait.over()) break;
         }
     } else if (warp == 9) {
         // The ring's pieces i - 8 must have been used before pieces i are
@@ -373,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const uint32_t score = lanes + t * kTile, sums = lanes + 256 + t * kValue;
         int done = 0;  // steps of the work before
-        for (int k = 0;; ++k) {
+        for (int k = 0; !kSplit || k < 1; ++k) {
             int steps, limit;
             {
                 Item w;
@@ -450,6 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait.warp(&bar.sum[t], (done + steps - 1) & 1);
                 tc::fence_after();
             }
+            if (kSplit && bar.item[0].parts > 1) {
+                m_part = m;
+                l_part = l;
+                break;
+            }
             const int3 kept = bar.kept[warp];
             __syncwarp();
             const int query = kept.x + (threadIdx.x & 127);
@@ -483,6 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
+    if (kSplit && bar.item[0].parts > 1) {  // the same for all blocks of a cluster
+        tc::fence_after();
+        join<kBf16>(p, bar.item[0], base, tmem + 256, m_part, l_part, split);
+        tc::fence_before();
+        __syncthreads();
+    }
     if (warp == 8) {
         tc::fence_after();
         tc::dealloc<1>(tmem, kColumns);
@@ -515,19 +626,41 @@ topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, const Att
         r = map3(&maps.v, p.total_k ? p.v : any, kValue, p.v_head_stride, p.total_k, p.v_token_stride, kTile / 2);
     if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "prompt attention tensor map");
 
-    const auto kernel = bf16 ? prompt_kernel<true> : prompt_kernel<false>;
-    static std::atomic<bool> prepared[2][AttendDevice::kMax];
-    cudaError_t e = allow_shared(kernel, kSmem, prepared[bf16][device.index]);
+    // Each request with queries has at most (queries + 255) / 256 blocks.
+    const int64_t requests = p.batch < p.total_q ? p.batch : p.total_q;
+    const int64_t most = p.heads * ((p.total_q + (kBlockRows - 1) * requests) / kBlockRows);
+    const auto kernel = bf16 ? prompt_kernel<true, false> : prompt_kernel<false, false>;
+    const auto split_kernel = bf16 ? prompt_kernel<true, true> : prompt_kernel<false, true>;
+    static std::atomic<bool> prepared[2][2][AttendDevice::kMax];
+    cudaError_t e = cudaSuccess;
+    // As many blocks a piece as leave all clusters on the device at once (15 of
+    // 8 blocks, 23 of 6, 36 of 4, 76 of 2), if a request can have keys for them.
+    int split = 1;
+    if (2 * most <= device.sms && p.total_k > kAloneSteps * kTile) {
+        static std::atomic<int> fitting[2][kMaxSplit + 1][AttendDevice::kMax];  // clusters, plus 1; 0: not known yet
+        e = allow_shared(split_kernel, kSmem, prepared[bf16][1][device.index]);
+        for (int n = kMaxSplit; e == cudaSuccess && split == 1 && n > 1; --n) {
+            std::atomic<int>& known = fitting[bf16][n][device.index];
+            int fit = known.load(std::memory_order_relaxed) - 1;
+            if (fit < 0) {
+                e = clusters_at_once(&fit, split_kernel, kThreads, kSmem, n);
+                if (e == cudaSuccess) known.store(fit + 1, std::memory_order_relaxed);
+            }
+            if (e == cudaSuccess && most <= fit) split = n;
+        }
+    }
+    if (e == cudaSuccess && split == 1) e = allow_shared(kernel, kSmem, prepared[bf16][0][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "prompt attention shared memory");
-    // Every request adds at most one block to total / 256.
-    const int64_t most = static_cast<int64_t>(p.heads) *
-                         (p.total_q / kBlockRows + (p.batch < p.total_q ? p.batch : p.total_q));
-    const unsigned grid = static_cast<unsigned>(most < device.sms ? most : device.sms);
+    const unsigned grid = static_cast<unsigned>(split > 1 ? most * split : most < device.sms ? most : device.sms);
     // Scores of a negative scale come from negated queries, so that the
     // largest score is always the largest exponent.
     // A scale of zero becomes the least normal number: hidden scores stay -inf.
     const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
-    e = launch_early(kernel, dim3(grid), kThreads, kSmem, stream, p, maps, device.flags, scale_log2, p.scale < 0.f);
+    if (split > 1)
+        e = launch_early_clusters(split_kernel, dim3(grid), split, kThreads, kSmem, stream, p, maps, device.flags, scale_log2,
+                                  p.scale < 0.f, split);
+    else
+        e = launch_early(kernel, dim3(grid), kThreads, kSmem, stream, p, maps, device.flags, scale_log2, p.scale < 0.f, 1);
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "prompt attention launch");
 }
 

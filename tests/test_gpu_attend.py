@@ -352,3 +352,63 @@ def test_no_wait_gave_up(api):
 
     assert _lib.topk_read_attend_flags() == 0
     assert _lib.topk_read_attend_flags(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("paged", [False, True])
+def test_short_rows_after_rows_of_nan(api, dtype, paged):
+    """Rows that end anywhere in a tile and follow, in the same block, rows whose cache entries are all NaN."""
+    page, lens = 64, [0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 79, 80, 81, 112, 113, 127, 128, 129, 145]
+    batch = 2 * 8 * len(lens)
+    cache = randn(101, 64 * page, WIDTH, dtype=dtype)
+    cache[32 * page:] = math.nan
+    seen = [lens[r // 2 % len(lens)] if r % 2 else 256 for r in range(batch)]
+    q = randn(102, batch, 16, WIDTH, dtype=dtype)
+    first = torch.tensor([0 if r % 2 else 32 for r in range(batch)], device="cuda")[:, None]
+    table = i32(first + torch.arange(4, device="cuda")[None] * 5 + torch.arange(batch, device="cuda")[:, None] % 7)
+    slots = i32((table[..., None] * page + torch.arange(page, device="cuda")).reshape(batch, -1))
+    if paged:
+        out, lse, _ = api.attend_paged(q[:, None], cache, i32(seen), table, page, SCALE)
+        out, lse = out[:, 0], lse[:, 0]
+    else:
+        out, lse, _ = api.attend_selected(q, cache, slots, SCALE, seq_lens=i32(seen))
+    assert torch.isnan(out[::2]).all() and torch.isnan(lse[::2]).all()
+    for r in range(1, batch, 2):
+        k = cache[slots[r, :seen[r]].long()]
+        o, l, ob, lb = attend(q[r], k, k[:, :512], SCALE, dtype)
+        check(out[r], o, ob, f"out of row {r}")
+        check(lse[r], l, lb, f"lse of row {r}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,heads", [
+    ([1], [5000], 1), ([1], [257], 2), ([100], [2049], 16), ([300, 2], [4100, 130], 2), ([1, 17, 256], [2049, 700, 3], 3),
+    ([257], [1500], 1), ([700], [600], 1), ([200, 0, 3], [0, 900, 1281], 5), ([129], [3000], 30)])
+def test_prompt_few_queries_long_keys(api, dtype, causal, lq, lk, heads):
+    """Calls with few pieces of work, whose keys several blocks share: parts with no, one or some of the steps, rows
+    that see nothing of a part, requests with too few keys to share beside long ones."""
+    q, kn, kr, v, cu_q, cu_k = prompt_inputs(111, lq, lk, heads, dtype, gap=5)
+    out = torch.full((q.shape[0], heads, 128), 7.0, dtype=dtype, device="cuda")
+    lse = torch.full((q.shape[0], heads), 7.0, device="cuda")
+    api.attend_prompt(q, kn, kr, v, i32(cu_q), i32(cu_k), SCALE, causal=causal, out=out, lse=lse)
+    check_prompt(q, kn, kr, v, cu_q, cu_k, causal, out, lse)
+    for t in (out, lse):
+        assert (t[:5] == 7).all() and (t[-5:] == 7).all()
+    again = api.attend_prompt(q, kn, kr, v, i32(cu_q), i32(cu_k), SCALE, causal=causal)
+    assert torch.equal(out[5:-5], again[0][5:-5]) and torch.equal(lse[5:-5], again[1][5:-5])
+
+
+def test_prompt_parts_of_infinities(api):
+    """Keys that several blocks share: scores of -inf and +inf, and NaN, in one part of the keys only."""
+    q, kn, kr, v, cu_q, cu_k = prompt_inputs(121, [3], [3000], 1, torch.float16)
+    q[:, 0, 0] = 1
+    for bad in (-math.inf, math.inf, math.nan):
+        keys = kn.clone()
+        keys[1500, 0, 0] = bad
+        out, lse = api.attend_prompt(q, keys, kr, v, i32(cu_q), i32(cu_k), SCALE, causal=False)
+        if bad == -math.inf:  # as if the key were not there
+            rest = [i for i in range(3000) if i != 1500]
+            check_prompt(q, kn[rest], kr[rest], v[rest], [0, 3], [0, 2999], False, out, lse)
+        else:
+            assert torch.isnan(out).all() and not torch.isfinite(lse).any()
