@@ -654,19 +654,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int tiles = walk.left;
             int n = 0, segment = 0;
             bool add = false;  // whether the sums of tile n - 1 are added to
+            int left = 0;      // its slots, up to the row's end
             const auto sums = [&](int m) {
                 wait.warp(&sh.weight, static_cast<uint32_t>(m) & 1);
                 tc::fence_after();
                 for (int g = 0; g < kValueGroups; ++g) {
                     wait.warp(&sh.value_full[g], static_cast<uint32_t>(m) & 1);
                     if (tc::elect()) {
+                        // Weights past the row's end are zero: nothing to
+                        // add (1662 rows of up to 41 slots: 76.6 -> 72.6 us;
+                        // not copying those slots either: 73.7, and rows of
+                        // 512 slots 2 % slower).
+                        if (g * kHalf < left) {
 #pragma unroll
-                        for (int a = 0; a < 2; ++a)  // values 128 a.. of each block's 256
+                            for (int a = 0; a < 2; ++a)  // values 128 a.. of each block's 256
 #pragma unroll
-                            for (int k = 0; k < kHalf / 16; ++k)
-                                tc::mma<2>(tmem + 128 * a, weight_at + g * (kWeightPiece >> 4) + 2 * k,
-                                           value_at + ((2 * a * kValuePiece + g * kHalf * 128) >> 4) + 128 * k, sum_instr,
-                                           add || g > 0 || k > 0);
+                                for (int k = 0; k < kHalf / 16; ++k)
+                                    tc::mma<2>(tmem + 128 * a, weight_at + g * (kWeightPiece >> 4) + 2 * k,
+                                               value_at + ((2 * a * kValuePiece + g * kHalf * 128) >> 4) + 128 * k,
+                                               sum_instr, add || g > 0 || k > 0);
+                        }
                         tc::commit_pair(&sh.value_empty[g]);
                         if (g == kValueGroups - 1) tc::commit_pair(&sh.sum);
                     }
@@ -707,6 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (!summed) sums(n - 1);
                     add = tile > s.first;
+                    left = s.length - tile * kTile;
                 }
             }
             if (tiles > 0) sums(n - 1);
