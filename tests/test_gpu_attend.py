@@ -412,3 +412,20 @@ def test_prompt_parts_of_infinities(api):
             check_prompt(q, kn[rest], kr[rest], v[rest], [0, 3], [0, 2999], False, out, lse)
         else:
             assert torch.isnan(out).all() and not torch.isfinite(lse).any()
+
+
+def test_prompt_few_queries_in_graph(api):
+    """Pieces that several blocks share, replayed from a graph on another stream with other inputs and lengths."""
+    q, kn, kr, v, cu_q, cu_k = prompt_inputs(131, [70], [2500], 2, torch.bfloat16)
+    marks_q, marks_k = i32(cu_q), i32(cu_k)
+    out, lse = api.attend_prompt(q, kn, kr, v, marks_q, marks_k, SCALE)  # looks up the device
+    out.zero_(), lse.zero_()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        api.attend_prompt(q, kn, kr, v, marks_q, marks_k, SCALE, out=out, lse=lse, stream=stream)
+    for length in (2500, 1111, 300):
+        marks_k[1] = length
+        q.neg_()
+        graph.replay()
+        check_prompt(q, kn, kr, v, cu_q, [0, length], True, out, lse)
