@@ -263,7 +263,10 @@ typedef enum {
  *   positions_or_null, rows_or_null  device int32[max_tokens]: each token's
  *                     position and request, -1 past the last token.
  *   status            device int32[2]: pages taken, TOPK_TABLES_* bits.
- * Outputs other than page_table overlap no input.
+ * No output may overlap context_lens, new_lens, free_pages or page_table, nor
+ * page_table the other three (TOPK_EINVAL): the lengths are read again after
+ * seq_lens is written.  A loop in which seq_lens becomes the next step's
+ * context_lens takes two sets of outputs in turn.
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
  */
 topk_status_t topk_block_tables(const int32_t* context_lens, const int32_t* new_lens, int32_t batch,

@@ -136,11 +136,30 @@ def _check_tables(context_lens, new_lens, free_pages, page_table, max_tokens, ou
     _on_gpu(context_lens)
 
 
+def _check_overlap(context_lens, new_lens, free_pages, page_table, out):
+    """Names the pair where an output, or the table, lies over an input (the C call refuses it)."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else -1
+        return t.data_ptr(), t.data_ptr() + 4 * (last + 1)
+
+    inputs = dict(context_lens=context_lens, new_lens=new_lens, free_pages=free_pages)
+    table = dict(page_table=page_table)
+    for name, t in {**{f"out.{n}": x for n, x in out._asdict().items()}, **table}.items():
+        a, b = span(t)
+        for other, x in {**inputs, **({} if t is page_table else table)}.items():
+            c, d = span(x)
+            if a < d and c < b:
+                raise ValueError(f"{name} must not lie over {other} (the result of one call and the lengths of the next: "
+                                 "take two results in turn)")
+
+
 def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
                  page_table: torch.Tensor, page_size: int, max_tokens: int, out: BlockTables | None = None,
                  stream=None) -> BlockTables:
     """Runs ``topk_block_tables``: writes the new pages into ``page_table`` ([batch, pages], in place) and returns
-    the step's lengths, offsets and slot map (in ``out``, where the result of an earlier call is given)."""
+    the step's lengths, offsets and slot map (in ``out``, where the result of an earlier call is given).  ``out`` must
+    not hold this call's inputs: where ``seq_lens`` becomes the next step's ``context_lens``, two results are taken
+    in turn."""
     gpu, shape = context_lens.get_device(), page_table.shape
     batch, num_free = shape[0] if shape else 0, free_pages.numel()
     if not (gpu >= 0 and len(shape) == 2 and page_table.dtype is _I32 and page_table.get_device() == gpu
@@ -164,6 +183,8 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), out[5].data_ptr(),
         _lib.stream_handle(stream, gpu))
     if status:
+        if status == _lib.TOPK_EINVAL:
+            _check_overlap(context_lens, new_lens, free_pages, page_table, out)
         _lib.check("topk_block_tables", status)
     return out
 

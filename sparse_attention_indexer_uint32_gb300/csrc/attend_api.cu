@@ -35,6 +35,24 @@ bool token_stride_ok(int64_t stride, int64_t least, int64_t count) {
 
 constexpr int64_t kMaxQueryHeads = int64_t{1} << 30;
 
+// int32 values at an address: `rows` rows of n, `stride` apart (4-byte aligned).
+struct Span {
+    const int32_t* at;
+    int64_t n;
+    int64_t rows = 1, stride = 0;
+};
+
+// Whether a row of values and rows of values have one in common: the first of
+// the rows that ends behind the start of `a` begins before its end.
+bool overlap(const Span& a, const Span& b) {
+    if (!a.at || !b.at || a.n <= 0 || b.n <= 0) return false;
+    const auto address = [](const Span& s) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(s.at) / 4); };
+    const int64_t from = address(a) - address(b);
+    const int64_t past = from - b.n;  // rows that begin up to here end before `a`
+    const int64_t row = past < 0 ? 0 : b.rows > 1 ? past / b.stride + 1 : 1;
+    return row < b.rows && row * b.stride < from + a.n;
+}
+
 // The word in which the attention kernels note a wait that gave up, one per GPU.
 __device__ uint32_t g_attend_flags;
 
@@ -84,6 +102,19 @@ topk_status_t topk_block_tables(const int32_t* context_lens, const int32_t* new_
         misaligned(page_table, 4) || misaligned(seq_lens, 4) || misaligned(cu_new, 4) || misaligned(slots, 4) ||
         misaligned(positions_or_null, 4) || misaligned(rows_or_null, 4) || misaligned(status, 4))
         return TOPK_EALIGN;
+    // Lengths, pages and the list are read again after outputs are written, by
+    // every block: an output in their place would change them under way.
+    const Span inputs[] = {{context_lens, batch}, {new_lens, batch}, {free_pages, num_free}};
+    const Span table = {page_table, pages_per_row, batch, page_table_stride};
+    const Span outputs[] = {{seq_lens, batch},           {cu_new, int64_t{batch} + 1}, {slots, max_tokens},
+                            {positions_or_null, max_tokens}, {rows_or_null, max_tokens},   {status, 2}};
+    for (const Span& in : inputs)
+        if (overlap(in, table)) return TOPK_EINVAL;
+    for (const Span& out : outputs) {
+        if (overlap(out, table)) return TOPK_EINVAL;
+        for (const Span& in : inputs)
+            if (overlap(out, in)) return TOPK_EINVAL;
+    }
     const topk_status_t dev = api_check_device();
     if (dev != TOPK_OK) return dev;
     TablesParams p = {context_lens, new_lens,   batch,  log2_of(page_size), free_pages, num_free,
