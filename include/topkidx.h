@@ -322,7 +322,8 @@ size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads
  * cache that are not seen are never used, whatever they hold.  A row that
  * sees nothing gets zeros and an lse of -inf.  Products of two-byte values
  * are exact and summed in fp32; the weights p are rounded to the cache's type
- * before the second product.
+ * before the second product (bf16: to 8 bits; fp16: to 11 bits down to 2^-21
+ * of a row's largest weight, by up to 2^-32 of it below).
  *   q                 device [rows][q_row_stride], head h at h * q_head_stride
  *                     (strides of at least 576 where there is more than one).
  *   cache             device [num_slots][slot_stride], 576 values used.

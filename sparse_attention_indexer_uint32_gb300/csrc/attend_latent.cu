@@ -67,7 +67,6 @@ constexpr int kPieces = kWidth / 64;             // 9
 constexpr int kQueryBytes = kPieces * kHalfRows * 128;
 constexpr uint32_t kColumns = 512;
 constexpr uint32_t kScore = 256;  // column of the two score tiles; the sums have 0..255
-constexpr float kLag = 8.f;
 
 // A step is 128 slots (N = 128: 32.9 cycles a product, N = 64: 25.8).  Shared
 // memory has one place for it, which is freed and filled in parts: the keys by
@@ -771,8 +770,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 softmax_sync();
                 tile_top = fmaxf(tile_top, sh.exchange[n & 1][threadIdx.x ^ 64]);
                 // (rows past the last see whatever is there)
-                const bool raise = m_row < all && (tile_top > m + kLag || (m == -INFINITY && tile_top > m));
-                const float next = raise ? tile_top : m;
+                const bool raise = m_row < all && (tile_top > m + (tc::kHead<kBf16> + tc::kLag) || (m == -INFINITY && tile_top > m));
+                const float next = raise ? tile_top - tc::kHead<kBf16> : m;
                 const float by = raise ? tc::exp2_approx(m - next) : 1.f;
                 m = next;
                 l *= by;

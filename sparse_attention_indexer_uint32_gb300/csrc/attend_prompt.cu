@@ -2,10 +2,10 @@
 // not) on the tensor cores.
 //
 // Mathematics: o = sum_j p_j v_j, p = softmax(scale (q_n.k_n + q_r.k_r)), with a
-// running maximum m and sum l per query: a tile of keys adds
-// 2^(x_j - m) v_j, x = scale log2(e) s, and when a tile's maximum passes m by
-// more than 8 (a factor of 256 that fp32 sums and two-byte weights hold with
-// room) the sums so far are multiplied by 2^(m - m').  The rotary part is
+// running reference m and sum l per query: a tile of keys adds
+// 2^(x_j - m) v_j, x = scale log2(e) s, and when a tile's maximum has passed m
+// by far enough (kHead and kLag of tc.cuh say how far, and what the two-byte
+// weights are off by) the sums so far are multiplied by 2^(m - m').  The rotary part is
 // one more 64-wide chunk of the first product, read once for all heads'
 // blocks, so keys are never put together in memory.
 //
@@ -58,7 +58,6 @@ constexpr int kRing = 8;
 constexpr int kKeyPieces = 3, kStepPieces = 5;
 constexpr int kThreads = 352;
 constexpr uint32_t kColumns = 512;
-constexpr float kLag = 8.f;
 constexpr int kMaxSplit = 8;   // blocks of a cluster
 // Up to 4 steps are not shared (8 heads of 512 tokens: 16.4 us alone, 18.4 in two
 // parts); longer ones are, in parts of 2 steps or more (4 requests of 64 queries
@@ -505,9 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kTile; i += 2) top[(i >> 1) & 3] = tc::max3(top[(i >> 1) & 3], s[i], s[i + 1]);
                 const float tile_top = tc::max3(fmaxf(top[0], top[1]), top[2], top[3]) * scale_log2;
-                const bool raise = tile_top > m + kLag || (m == -INFINITY && tile_top > m);
+                const bool raise = tile_top > m + (tc::kHead<kBf16> + tc::kLag) || (m == -INFINITY && tile_top > m);
                 if (__any_sync(~0u, raise)) {
-                    const float next = raise ? tile_top : m;
+                    const float next = raise ? tile_top - tc::kHead<kBf16> : m;
                     const float by = raise ? tc::exp2_approx(m - next) : 1.f;
                     m = next;
                     l *= by;

@@ -254,6 +254,18 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return r;
 }
 
+// Softmax weights are 2^(x - m) for a running reference m that follows the
+// largest x so far: set to kHead below it, and raised when a tile's largest
+// passes that by more than kLag (a rise scales the sums so far).  So the
+// largest weight is between 2^kHead and 2^(kHead + kLag).
+// bf16 has the range of fp32.  fp16 is 2^-14 to 65504 (steps of 2^-24 below):
+// with the largest at 2^7 to 2^15 a weight keeps its 11 bits down to 2^-21 of
+// the largest and is off by at most 2^-32 of it below that (at 1 to 2^8: by
+// 2^-25, and 2000 slots 26 bits below one in their first tile were lost).
+constexpr float kLag = 8.f;
+template <bool kBf16>
+constexpr float kHead = kBf16 ? 0.f : 7.f;
+
 // ------------------------------------------------------------ bounded waits
 // A wait gives up after kLimitNs and sets the block's flag; from then on
 // every wait of the block returns at once, so that the block runs to its end
