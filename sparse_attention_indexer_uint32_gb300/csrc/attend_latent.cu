@@ -81,8 +81,8 @@ constexpr int kWeightPiece = kHalfRows * 128;  // 64 rows of 64 weights
 constexpr int kKeyBytes = kPieces * kKeyPiece, kValueBytes = 4 * kValuePiece, kWeightBytes = 2 * kWeightPiece;
 
 struct Shared {
-    uint64_t query_full[2], query_empty[2];
     // landed: in this block; full: in both (used in the first block).
+    uint64_t query_landed[2], query_full[2], query_empty[2];
     uint64_t key_landed[kKeyGroups], key_full[kKeyGroups], key_empty[kKeyGroups];
     uint64_t value_landed[kValueGroups], value_full[kValueGroups], value_empty[kValueGroups];
     uint64_t score[2], weight, sum, end;
@@ -336,7 +336,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh.value_full[i], 2);
             ptx::mbar_init(&sh.value_empty[i], 1);
             ptx::mbar_init(&sh.score[i], 1);
-            ptx::mbar_init(&sh.query_full[i], 1);
+            ptx::mbar_init(&sh.query_landed[i], 1);
+            ptx::mbar_init(&sh.query_full[i], 2);
             ptx::mbar_init(&sh.query_empty[i], 1);
         }
         ptx::mbar_init(&sh.weight, few ? 4 : 8);
@@ -370,7 +371,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         SlotAhead ahead(p, walk, s, rank * kHalf + 32 * part + lane);
         const int tiles = ahead.tiles;
         pair_ready();
-        for (int n = 0; n < tiles && !wait.over(); ++n) {
+        bool on = true;
+        for (int n = 0; n < tiles && on; ++n) {
             const int slot = ahead.next();
             const uint8_t* from[8];
             uint32_t seen = 0;
@@ -381,7 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 from[q] = static_cast<const uint8_t*>(p.cache) + max(x, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
             }
             for (int g = 0; g < kKeyGroups; ++g) {
-                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
+                on = n == 0 || wait.all(&sh.key_empty[g], (n - 1) & 1);
+                if (!on) break;
                 const uint32_t to = keys + kGroupPieces * g * kKeyPiece + part * 4096 + r * 128;
                 const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
 #pragma unroll
@@ -392,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    ((seen >> q) & 1) * 16);
                 tc::copy16_arrive(&sh.key_landed[g]);
             }
-            if (part == 0 && lane == 0) sh.copied = n + 1;
+            if (on && part == 0 && lane == 0) sh.copied = n + 1;
         }
         tc::copy16_drain();
     } else if (!kPaged && (warp == 6 || warp == 9)) {
@@ -404,7 +407,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         SlotAhead ahead[kValueGroups] = {SlotAhead(p, walk, s, 32 * part + lane), SlotAhead(p, walk2, s2, kHalf + 32 * part + lane)};
         const int tiles = ahead[0].tiles;
         pair_ready();
-        for (int n = 0; n < tiles && !wait.over(); ++n) {
+        bool on = true;
+        for (int n = 0; n < tiles && on; ++n) {
             const int slots[kValueGroups] = {ahead[0].next(), ahead[1].next()};
             // One bit a slot that is seen.  Place n % 4 was last read for tile
             // n - 4; the copies of tile n - 1 waited for the second product of
@@ -418,7 +422,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + (lane & 7) * 16;
 #pragma unroll
             for (int g = 0; g < kValueGroups; ++g) {
-                if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
+                on = n == 0 || wait.all(&sh.value_empty[g], (n - 1) & 1);
+                if (!on) break;
                 const uint32_t to = values + g * (kHalf * 128) + part * 4096 + r * 128;
                 const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
 #pragma unroll
@@ -449,7 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         fetch();
         pair_ready();
-        while (more && !wait.over()) {
+        int stopped = kKeyGroups;  // the group that was not copied any more
+        while (more && stopped == kKeyGroups) {
             const int box = row_of();
             if (++tile == s.last) {
                 more = walk.next(s);
@@ -457,7 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             fetch();
             for (int g = 0; g < kKeyGroups; ++g) {
-                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
+                if (n > 0 && !wait.all(&sh.key_empty[g], (n - 1) & 1)) {
+                    stopped = g;
+                    break;
+                }
                 if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.key_landed[g], kGroupPieces * kKeyPiece);
                 __syncwarp();
                 if (mine)
@@ -465,14 +474,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tc::load_2d(keys + c * kKeyPiece + lane * box_rows * 128, &maps.cache, 64 * c, box,
                                     &sh.key_landed[g]);
             }
+            if (stopped < kKeyGroups) break;
             ++n;
             // The rows of the next tile come to L2 while this one's are used:
             // shared memory has room for one tile only.
             if (more && mine)
                 for (int c = 0, row = row_of(); c < kPieces; ++c) tc::prefetch_2d(&maps.cache, 64 * c, row);
         }
-        if (n > 0 && wait.over())
-            for (int g = 0; g < kKeyGroups; ++g) tc::Waits::drain(&sh.key_landed[g], (n - 1) & 1);
+        for (int g = 0; g < kKeyGroups; ++g) {
+            const int copied = stopped < kKeyGroups && g < stopped ? n + 1 : n;
+            if (copied > 0) tc::Waits::drain(&sh.key_landed[g], (copied - 1) & 1);
+        }
     } else if (kPaged && warp == 6) {
         // Pages, second product: all slots of each tile, values 256 rank...
         int n = 0;
@@ -486,7 +498,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         fetch();
         pair_ready();
-        while (more && !wait.over()) {
+        int stopped = kValueGroups;
+        while (more && stopped == kValueGroups) {
             const int slots[4] = {next[0].get(p), next[1].get(p), next[2].get(p), next[3].get(p)};
             if (++tile == s.last) {
                 more = walk.next(s);
@@ -509,7 +522,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (box < 0) box = p.num_slots;
             for (int g = 0; g < kValueGroups; ++g) {
-                if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
+                if (n > 0 && !wait.all(&sh.value_empty[g], (n - 1) & 1)) {
+                    stopped = g;
+                    break;
+                }
                 if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.value_landed[g], kValueBytes / kValueGroups);
                 __syncwarp();
                 if (at / kHalf == g)
@@ -517,10 +533,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tc::load_2d(values + c * kValuePiece + at * 128, &maps.cache, 256 * rank + 64 * c, box,
                                     &sh.value_landed[g]);
             }
+            if (stopped < kValueGroups) break;
             ++n;
         }
-        if (n > 0 && wait.over())
-            for (int g = 0; g < kValueGroups; ++g) tc::Waits::drain(&sh.value_landed[g], (n - 1) & 1);
+        for (int g = 0; g < kValueGroups; ++g) {
+            const int copied = stopped < kValueGroups && g < stopped ? n + 1 : n;
+            if (copied > 0) tc::Waits::drain(&sh.value_landed[g], (copied - 1) & 1);
+        }
     } else if (warp == kQueryWarp) {
         if (lane == 0 && rank == 0 && pair > 0) {
             const Runs runs(sh.total, pairs);
@@ -540,27 +559,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int places = few ? 2 : 1;
             for (int n = 0; walk.next(s); ++n) {
                 const int place = n % places, round = n / places;
-                const uint32_t full = ptx::map_rank(ptx::smem_addr(&sh.query_full[place]), 0),
-                               to = queries + place * kPieces * query_piece;
-                if (round > 0) wait(&sh.query_empty[place], (round - 1) & 1);
-                if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.query_full[place], 2 * kPieces * query_piece);
+                const uint32_t to = queries + place * kPieces * query_piece;
+                uint64_t* landed = &sh.query_landed[place];
+                if (round > 0 && !wait(&sh.query_empty[place], (round - 1) & 1)) break;
+                ptx::mbar_arrive_expect_tx(landed, kPieces * query_piece);
                 const int m = s.group * kRows + rank * block_rows;
                 for (int c = 0; c < kPieces; ++c) {
                     if (whole_rows) {
-                        tc::load_4d_pair(to + c * query_piece, &maps.q, 64 * c, m, 0, s.row, full);
+                        tc::load_4d(to + c * query_piece, &maps.q, 64 * c, m, 0, s.row, landed);
                     } else {
                         for (int i = 0; i < block_rows; ++i)
-                            tc::load_4d_pair(to + c * query_piece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
-                                             (m + i) / p.heads, s.row, full);
+                            tc::load_4d(to + c * query_piece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
+                                        (m + i) / p.heads, s.row, landed);
                     }
                 }
-                if (*wait.gave_up) {
-                    if (rank == 0) {
-                        if (n > 0 && places == 2) tc::Waits::drain(&sh.query_full[place ^ 1], ((n - 1) / 2) & 1);
-                        tc::Waits::drain(&sh.query_full[place], round & 1);
-                    }
+                if (!wait(landed, round & 1)) {
+                    tc::Waits::drain(landed, round & 1);
                     break;
                 }
+                tc::fence_async();
+                tc::arrive_cluster(ptx::map_rank(ptx::smem_addr(&sh.query_full[place]), 0));
             }
         }
     } else if (!kPaged && warp == kPrefetchWarp) {
@@ -654,12 +672,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int n = 0, segment = 0;
             bool add = false;  // whether the sums of tile n - 1 are added to
             int left = 0;      // its slots, up to the row's end
+            // Given up: nothing is issued or announced any more, so that the
+            // other block, which has a flag of its own, is told the truth.
+            bool on = true;
             const auto sums = [&](int m) {
-                wait.warp(&sh.weight, static_cast<uint32_t>(m) & 1);
+                on &= wait.warp(&sh.weight, static_cast<uint32_t>(m) & 1);
                 tc::fence_after();
                 for (int g = 0; g < kValueGroups; ++g) {
-                    wait.warp(&sh.value_full[g], static_cast<uint32_t>(m) & 1);
-                    if (tc::elect()) {
+                    on &= wait.warp(&sh.value_full[g], static_cast<uint32_t>(m) & 1);
+                    if (tc::elect() && on) {
                         // Weights past the row's end are zero: nothing to
                         // add (1662 rows of up to 41 slots: 76.6 -> 72.6 us;
                         // not copying those slots either: 73.7, and rows of
@@ -692,11 +713,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             sums(n - 1);
                             summed = true;
                         }
-                        wait.warp(&sh.query_full[place], round);
+                        on &= wait.warp(&sh.query_full[place], round);
                     }
                     for (int g = 0; g < kKeyGroups; ++g) {
-                        wait.warp(&sh.key_full[g], static_cast<uint32_t>(n) & 1);
-                        if (tc::elect()) {
+                        on &= wait.warp(&sh.key_full[g], static_cast<uint32_t>(n) & 1);
+                        if (tc::elect() && on) {
 #pragma unroll
                             for (int k = 0; k < 4 * kGroupPieces; ++k) {
                                 const int c = kGroupPieces * g + (k >> 2);
@@ -731,6 +752,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int threads = few ? 64 : 128;
         const auto softmax_sync = [&] { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); };
         int n = 0;
+        // These warps wait for one another, so all of them go through all
+        // tiles, also after one has given up.
         pair_ready();
         while (walk.next(s)) {
             const int m_row = s.group * kRows + rank * block_rows + r;

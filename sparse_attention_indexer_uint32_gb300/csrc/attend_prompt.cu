@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // each at its own time: copies for the next begin while the last results of
     // this one are being written.
     const auto take = [&](int k, Item& item) {  // by a whole warp; false: there is no more
-        wait.warp(&bar.item_full[k & 1], (k >> 1) & 1);
+        if (!wait.all(&bar.item_full[k & 1], (k >> 1) & 1)) return false;
         item = bar.item[k & 1];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bar.item_empty[k & 1]);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Pieces are dealt out in turn, every other round backwards, so that
         // no block gets the longest of each.
         for (int k = 0;; ++k) {
-            if (k >= 2) wait.warp(&bar.item_empty[k & 1], ((k >> 1) - 1) & 1);
+            if (k >= 2 && !wait.all(&bar.item_empty[k & 1], ((k >> 1) - 1) & 1)) break;
             const int takers = static_cast<int>(gridDim.x) / split, taker = static_cast<int>(blockIdx.x) / split;
             const int in_round = k & 1 ? takers - 1 - taker : taker;
             const int64_t number = static_cast<int64_t>(k) * takers + in_round, index = number / p.heads;
@@ -329,13 +329,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The ring's pieces i - 8 must have been used before pieces i are
         // filled: whole groups are waited for, the keys or the values of
         // the step in which they were.
+        // Once a wait of the block has given up, the products announce what
+        // they did not wait for (a condition on them cost 2 % of a long
+        // prompt), with the flag set before: nothing is copied after it.
+        const auto free_by = [&](uint64_t* empty, uint32_t parity) { return wait(empty, parity) && !*wait.gave_up; };
         const auto room = [&](int last) {
             const int used = last - kRing;
-            if (used < 0) return;
+            if (used < 0) return true;
             const int step = used / kStepPieces;
-            wait(used % kStepPieces < kKeyPieces ? &bar.key_empty[step & 1] : &bar.value_empty[step & 1], (step >> 1) & 1);
+            return free_by(used % kStepPieces < kKeyPieces ? &bar.key_empty[step & 1] : &bar.value_empty[step & 1],
+                           (step >> 1) & 1);
         };
-        int key_steps = 0, loaded[2] = {0, 0};
+        int key_steps = 0, value_steps = 0, loaded[2] = {0, 0};
         Item w;
         for (int k = 0; take(k, w); ++k) {
             if (lane == 0) {
@@ -343,41 +348,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int q_head = p.q_head_stride ? w.head : 0, k_head = p.k_head_stride ? w.head : 0,
                           v_head = p.v_head_stride ? w.head : 0;
                 const auto load_queries = [&](int t) {
-                    if (loaded[t] > 0) wait(&bar.query_empty[t], (loaded[t] - 1) & 1);
+                    if (loaded[t] > 0 && !free_by(&bar.query_empty[t], (loaded[t] - 1) & 1)) return false;
                     ptx::mbar_arrive_expect_tx(&bar.query_full[t], 3 * kPiece);
                     for (int c = 0; c < 3; ++c)
                         tc::load_3d(queries + (3 * t + c) * kPiece, &maps.q, 64 * c, q_head, w.first(t),
                                     &bar.query_full[t]);
                     ++loaded[t];
+                    return true;
                 };
-                if (steps[0]) load_queries(0);
-                for (int j = 0; j < n && !bar.gave_up; ++j) {
-                    const int row = w.range.z + j * kTile, piece = key_steps * kStepPieces;
+                const bool on = steps[0] == 0 || load_queries(0);
+                for (int j = 0; j < n && on; ++j) {
+                    const int row = w.range.z + j * kTile, step = key_steps, piece = step * kStepPieces;
                     const auto at = [&](int i) { return ring + (piece + i) % kRing * kPiece; };
-                    room(piece);
-                    room(piece + 2);
-                    uint64_t* full = &bar.key_full[key_steps & 1];
+                    if (!room(piece) || !room(piece + 2)) break;
+                    uint64_t* full = &bar.key_full[step & 1];
                     ptx::mbar_arrive_expect_tx(full, kKeyPieces * kPiece);
                     for (int c = 0; c < 2; ++c) tc::load_3d(at(c), &maps.k_nope, 64 * c, k_head, row, full);
                     tc::load_2d(at(2), &maps.k_rope, 0, row, full);
-                    if (j == 0 && steps[1]) load_queries(1);
-                    room(piece + 3);
-                    room(piece + 4);
-                    full = &bar.value_full[key_steps & 1];
+                    ++key_steps;
+                    if (j == 0 && steps[1] && !load_queries(1)) break;
+                    if (!room(piece + 3) || !room(piece + 4)) break;
+                    full = &bar.value_full[step & 1];
                     ptx::mbar_arrive_expect_tx(full, 2 * kPiece);
                     for (int c = 0; c < 2; ++c)  // 64 keys by 128 values
                         for (int d = 0; d < 2; ++d)
                             tc::load_3d(at(3 + c) + d * (kPiece / 2), &maps.v, 64 * d, v_head, row + 64 * c, full);
-                    ++key_steps;
+                    ++value_steps;
                 }
             }
             __syncwarp();
         }
-        if (lane == 0 && bar.gave_up) {  // what is in flight lands before the block ends
-            for (int i = max(0, key_steps - 2); i < key_steps; ++i) {
-                tc::Waits::drain(&bar.key_full[i & 1], (i >> 1) & 1);
+        if (lane == 0) {  // what is in flight lands before the block ends
+            for (int i = max(0, key_steps - 2); i < key_steps; ++i) tc::Waits::drain(&bar.key_full[i & 1], (i >> 1) & 1);
+            for (int i = max(0, value_steps - 2); i < value_steps; ++i)
                 tc::Waits::drain(&bar.value_full[i & 1], (i >> 1) & 1);
-            }
             for (int t = 0; t < 2; ++t)
                 if (loaded[t]) tc::Waits::drain(&bar.query_full[t], (loaded[t] - 1) & 1);
         }

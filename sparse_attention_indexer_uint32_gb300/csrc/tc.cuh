@@ -180,14 +180,11 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
-// Copies of a block pair: the bytes are counted on a barrier of either block
-// (a shared::cluster address).
-__device__ __forceinline__ void load_4d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                             uint32_t bar) {
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
         "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(ptx::smem_addr(bar))
         : "memory");
 }
 // 16 bytes, or zeros where `bytes` is 0 (then nothing is read).
@@ -267,22 +264,32 @@ template <bool kBf16>
 constexpr float kHead = kBf16 ? 0.f : 7.f;
 
 // ------------------------------------------------------------ bounded waits
-// A wait gives up after kLimitNs and sets the block's flag; from then on
-// every wait of the block returns at once, so that the block runs to its end
-// on whatever its buffers hold.
+// A wait gives up after kLimitNs, sets the block's flag and says so; from then
+// on every wait of the block whose phase is not complete does the same at
+// once, and the block goes on to its end on whatever its buffers hold.  What a
+// copy is let loose by stays true meanwhile: a warp that copies stops where
+// its wait gave up, and never sees room that was announced after a wait that
+// did (each kernel says how).  So no barrier is armed twice, and each has at
+// most one phase in flight to drain before the block ends.
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 struct Waits {
     volatile uint32_t* gave_up;  // in shared memory
 
-    __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
-        if (ptx::mbar_test_wait(bar, parity)) return;
-        slow(bar, parity);
+    // Whether the phase is complete; false: given up.
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        return ptx::mbar_test_wait(bar, parity) || slow(bar, parity);
     }
-    // By a whole warp, which goes on together.
-    __device__ __forceinline__ void warp(uint64_t* bar, uint32_t parity) const {
-        (*this)(bar, parity);
+    // By a whole warp, which goes on together.  Each lane has its own answer, so
+    // none may leave a loop by it (a vote cost 4 % of a long prompt).
+    __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+        const bool done = (*this)(bar, parity);
         __syncwarp();
+        return done;
+    }
+    // The same with one answer for the warp.
+    __device__ __forceinline__ bool all(uint64_t* bar, uint32_t parity) const {
+        return __all_sync(~0u, (*this)(bar, parity));
     }
     // For a warp that polls several barriers: counts a poll in which none was
     // ready, looks at the clock and the flag now and then, and says whether to
@@ -296,16 +303,15 @@ struct Waits {
         return over();
     }
     __device__ __forceinline__ bool over() const { return __any_sync(~0u, *gave_up != 0u); }
-    __device__ __forceinline__ void slow(uint64_t* bar, uint32_t parity) const {
+    __device__ __forceinline__ bool slow(uint64_t* bar, uint32_t parity) const {
         const uint64_t t0 = ptx::global_timer_ns();
-        while (!*gave_up && !ptx::mbar_try_wait_sleep(bar, parity, 20000u)) {
-            if (ptx::global_timer_ns() - t0 >= kLimitNs) {
-                *gave_up = 1u;
-                return;
-            }
+        while (!*gave_up) {
+            if (ptx::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+            if (ptx::global_timer_ns() - t0 >= kLimitNs) *gave_up = 1u;
         }
+        return false;
     }
-    // For copies or products still in flight when a block ends early.
+    // For copies or products that may still be in flight when a block ends.
     __device__ __forceinline__ static void drain(uint64_t* bar, uint32_t parity) {
         (void)ptx::mbar_wait_bounded(bar, parity, kLimitNs);
     }
