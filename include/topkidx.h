@@ -476,7 +476,10 @@ typedef struct {
                                            for one bulk copy of scores before it gives up, sets
                                            TOPK_FLAG_TIMEOUT (the call's output is then void) and
                                            stops issuing copies; the call still returns, and the
-                                           block waits for its copies in flight before it exits  */
+                                           block waits for its copies in flight before it exits.
+                                           The attention kernels take it for each of their waits
+                                           (topk_read_attend_flags); up to 100 there they give
+                                           up at the first wait that is not over already         */
     int32_t single_block_kernel;        /* 0: automatic (shape 2 for rows of 16K..64K from
                                            stream_batch_min rows on, when two blocks fit an SM);
                                            1: the single-role kernel; 2 / 3: the warp-specialised

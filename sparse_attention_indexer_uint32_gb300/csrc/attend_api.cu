@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "attend_internal.h"
+#include "topk_internal.h"
 #include "topkidx.h"
 
 using namespace topkidx;
@@ -51,6 +52,13 @@ bool overlap(const Span& a, const Span& b) {
     const int64_t past = from - b.n;  // rows that begin up to here end before `a`
     const int64_t row = past < 0 ? 0 : b.rows > 1 ? past / b.stride + 1 : 1;
     return row < b.rows && row * b.stride < from + a.n;
+}
+
+WaitLimit wait_limit() {
+    topk_tuning_t t;
+    (void)topk_get_tuning(&t);
+    const uint64_t ns = t.wait_limit_us > 0 ? 1000ull * static_cast<uint64_t>(t.wait_limit_us) : kDefaultWaitLimitNs;
+    return {ns, ns <= 100000ull ? 1u : 0u};
 }
 
 // The word in which the attention kernels note a wait that gave up, one per GPU.
@@ -172,9 +180,10 @@ topk_status_t check_latent(const LatentParams& p, topk_dtype_t dtype, size_t wor
     return TOPK_OK;
 }
 
-topk_status_t run_latent(const LatentParams& p, topk_dtype_t dtype, cudaStream_t stream) {
+topk_status_t run_latent(LatentParams& p, topk_dtype_t dtype, cudaStream_t stream) {
     AttendDevice device;
     const topk_status_t st = attend_device(&device);
+    p.wait = wait_limit();
     return st == TOPK_OK ? launch_latent(p, dtype, device, stream) : st;
 }
 
@@ -267,7 +276,7 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
     if (total_q == 0) return TOPK_OK;
     PromptParams p = {q,      q_token_stride, q_head_stride, k_nope, k_token_stride, k_head_stride, k_rope,
                       k_rope_stride, v,       v_token_stride, v_head_stride, cu_q,   cu_k,          batch,
-                      total_q, total_k, heads, scale,        causal, out,            lse_or_null};
+                      total_q, total_k, heads, scale,        causal, out,            lse_or_null,   wait_limit()};
     return launch_prompt(p, dtype, device, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -22,6 +22,14 @@ constexpr int kValue = TOPK_VALUE_DIM;
 topk_status_t api_check_device();
 topk_status_t api_cuda_fail(cudaError_t e, const char* where);
 
+// How long a wait of a kernel may take (the tuning's wait_limit_us).  A
+// sleeping probe outlasts a short limit, and polling for it cost 2 to 5 % of a
+// call: up to 100 us there is none, and blocks begin as if one had given up.
+struct WaitLimit {
+    uint64_t ns;
+    uint32_t none;
+};
+
 // The current device, as the attention launches need it.
 struct AttendDevice {
     static constexpr int kMax = 64;
@@ -140,6 +148,7 @@ struct LatentParams {
     void* out;
     float* lse;  // or null
     void* workspace;
+    WaitLimit wait;
 };
 size_t latent_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
 topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
@@ -160,6 +169,7 @@ struct PromptParams {
     int32_t causal;
     void* out;
     float* lse;  // or null
+    WaitLimit wait;
 };
 topk_status_t launch_prompt(const PromptParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
 

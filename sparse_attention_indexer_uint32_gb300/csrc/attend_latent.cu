@@ -324,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int block_rows = few ? kHalfRows / 2 : kHalfRows, query_piece = block_rows * 128;
 
     if (threadIdx.x == 0) {
-        sh.gave_up = 0;
+        sh.gave_up = p.wait.none;
         sh.copied = 0;
         for (int i = 0; i < kKeyGroups; ++i) {
             ptx::mbar_init(&sh.key_landed[i], kPaged ? 1 : 64);
@@ -360,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::fence_after();
     };
     const uint32_t tmem = sh.tmem;
-    const tc::Waits wait{&sh.gave_up};
+    const tc::Waits wait{&sh.gave_up, p.wait.ns};
     Walk walk(p, sh, pair, pairs);
     Segment s = {};
 

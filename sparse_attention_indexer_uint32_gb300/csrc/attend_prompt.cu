@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            bar.gave_up = 0;
+            bar.gave_up = p.wait.none;
             for (int t = 0; t < 2; ++t) {
                 ptx::mbar_init(&bar.key_full[t], 1);
                 ptx::mbar_init(&bar.key_empty[t], 1);
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = bar.tmem;
-    const tc::Waits wait{&bar.gave_up};
+    const tc::Waits wait{&bar.gave_up, p.wait.ns};
 
     // The warps that copy, multiply and compute take the same pieces of work,
     // each at its own time: copies for the next begin while the last results of

@@ -10,6 +10,7 @@
 
 #include <cstdint>
 
+#include "attend_internal.h"
 #include "ptx.cuh"
 
 namespace topkidx {
@@ -264,17 +265,19 @@ template <bool kBf16>
 constexpr float kHead = kBf16 ? 0.f : 7.f;
 
 // ------------------------------------------------------------ bounded waits
-// A wait gives up after kLimitNs, sets the block's flag and says so; from then
-// on every wait of the block whose phase is not complete does the same at
-// once, and the block goes on to its end on whatever its buffers hold.  What a
-// copy is let loose by stays true meanwhile: a warp that copies stops where
-// its wait gave up, and never sees room that was announced after a wait that
-// did (each kernel says how).  So no barrier is armed twice, and each has at
-// most one phase in flight to drain before the block ends.
-constexpr uint64_t kLimitNs = 2000000000ull;
+// A wait gives up after a limit (2 s unless the tuning says otherwise), sets
+// the block's flag and says so; from then on every wait of the block whose
+// phase is not complete does the same at once, and the block goes on to its
+// end on whatever its buffers hold.  What a copy is let loose by stays true
+// meanwhile: a warp that copies stops where its wait gave up, and never sees
+// room that was announced after a wait that did (each kernel says how).  So no
+// barrier is armed twice, and each has at most one phase in flight to drain
+// before the block ends.
+constexpr uint64_t kDrainNs = 2000000000ull;  // whatever the limit of a wait is
 
 struct Waits {
     volatile uint32_t* gave_up;  // in shared memory
+    uint64_t limit_ns;
 
     // Whether the phase is complete; false: given up.
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
@@ -298,7 +301,7 @@ struct Waits {
         if ((++spins & 255) != 0) return false;
         const uint64_t now = ptx::global_timer_ns();
         if (spins == 256) since = now;
-        if (now - since >= kLimitNs) *gave_up = 1u;
+        if (now - since >= limit_ns) *gave_up = 1u;
         __syncwarp();
         return over();
     }
@@ -307,13 +310,13 @@ struct Waits {
         const uint64_t t0 = ptx::global_timer_ns();
         while (!*gave_up) {
             if (ptx::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-            if (ptx::global_timer_ns() - t0 >= kLimitNs) *gave_up = 1u;
+            if (ptx::global_timer_ns() - t0 >= limit_ns) *gave_up = 1u;
         }
         return false;
     }
     // For copies or products that may still be in flight when a block ends.
     __device__ __forceinline__ static void drain(uint64_t* bar, uint32_t parity) {
-        (void)ptx::mbar_wait_bounded(bar, parity, kLimitNs);
+        (void)ptx::mbar_wait_bounded(bar, parity, kDrainNs);
     }
 };
 
