@@ -371,8 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         SlotAhead ahead(p, walk, s, rank * kHalf + 32 * part + lane);
         const int tiles = ahead.tiles;
         pair_ready();
-        bool on = true;
-        for (int n = 0; n < tiles && on; ++n) {
+        for (int n = 0; n < tiles && !wait.over(); ++n) {
             const int slot = ahead.next();
             const uint8_t* from[8];
             uint32_t seen = 0;
@@ -383,8 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 from[q] = static_cast<const uint8_t*>(p.cache) + max(x, 0) * (2 * p.slot_stride) + (lane & 7) * 16;
             }
             for (int g = 0; g < kKeyGroups; ++g) {
-                on = n == 0 || wait.all(&sh.key_empty[g], (n - 1) & 1);
-                if (!on) break;
+                if (n > 0) wait.warp(&sh.key_empty[g], (n - 1) & 1);
                 const uint32_t to = keys + kGroupPieces * g * kKeyPiece + part * 4096 + r * 128;
                 const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
 #pragma unroll
@@ -395,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                    ((seen >> q) & 1) * 16);
                 tc::copy16_arrive(&sh.key_landed[g]);
             }
-            if (on && part == 0 && lane == 0) sh.copied = n + 1;
+            if (part == 0 && lane == 0) sh.copied = n + 1;
         }
         tc::copy16_drain();
     } else if (!kPaged && (warp == 6 || warp == 9)) {
@@ -407,8 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         SlotAhead ahead[kValueGroups] = {SlotAhead(p, walk, s, 32 * part + lane), SlotAhead(p, walk2, s2, kHalf + 32 * part + lane)};
         const int tiles = ahead[0].tiles;
         pair_ready();
-        bool on = true;
-        for (int n = 0; n < tiles && on; ++n) {
+        for (int n = 0; n < tiles && !wait.over(); ++n) {
             const int slots[kValueGroups] = {ahead[0].next(), ahead[1].next()};
             // One bit a slot that is seen.  Place n % 4 was last read for tile
             // n - 4; the copies of tile n - 1 waited for the second product of
@@ -422,8 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 512 * rank + (lane & 7) * 16;
 #pragma unroll
             for (int g = 0; g < kValueGroups; ++g) {
-                on = n == 0 || wait.all(&sh.value_empty[g], (n - 1) & 1);
-                if (!on) break;
+                if (n > 0) wait.warp(&sh.value_empty[g], (n - 1) & 1);
                 const uint32_t to = values + g * (kHalf * 128) + part * 4096 + r * 128;
                 const uint32_t even = to + (((lane & 7) ^ r) << 4), odd = to + (((lane & 7) ^ r ^ 4) << 4);
 #pragma unroll
@@ -672,15 +668,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int n = 0, segment = 0;
             bool add = false;  // whether the sums of tile n - 1 are added to
             int left = 0;      // its slots, up to the row's end
-            // Given up: nothing is issued or announced any more, so that the
-            // other block, which has a flag of its own, is told the truth.
+            // Pages: given up, nothing is issued or announced any more, so that
+            // the other block, which has a flag of its own, is told the truth.
+            // (Copies of selected slots are waited for by those who made them,
+            // whatever they were let loose by.)
             bool on = true;
             const auto sums = [&](int m) {
                 on &= wait.warp(&sh.weight, static_cast<uint32_t>(m) & 1);
                 tc::fence_after();
                 for (int g = 0; g < kValueGroups; ++g) {
                     on &= wait.warp(&sh.value_full[g], static_cast<uint32_t>(m) & 1);
-                    if (tc::elect() && on) {
+                    if (tc::elect() && (on || !kPaged)) {
                         // Weights past the row's end are zero: nothing to
                         // add (1662 rows of up to 41 slots: 76.6 -> 72.6 us;
                         // not copying those slots either: 73.7, and rows of
@@ -717,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     for (int g = 0; g < kKeyGroups; ++g) {
                         on &= wait.warp(&sh.key_full[g], static_cast<uint32_t>(n) & 1);
-                        if (tc::elect() && on) {
+                        if (tc::elect() && (on || !kPaged)) {
 #pragma unroll
                             for (int k = 0; k < 4 * kGroupPieces; ++k) {
                                 const int c = kGroupPieces * g + (k >> 2);

@@ -268,11 +268,11 @@ constexpr float kHead = kBf16 ? 0.f : 7.f;
 // A wait gives up after a limit (2 s unless the tuning says otherwise), sets
 // the block's flag and says so; from then on every wait of the block whose
 // phase is not complete does the same at once, and the block goes on to its
-// end on whatever its buffers hold.  What a copy is let loose by stays true
-// meanwhile: a warp that copies stops where its wait gave up, and never sees
-// room that was announced after a wait that did (each kernel says how).  So no
-// barrier is armed twice, and each has at most one phase in flight to drain
-// before the block ends.
+// end on whatever its buffers hold.  No barrier that counts the bytes of tiled
+// copies is armed twice meanwhile: a warp that copies stops where its wait gave
+// up and sees no room that was announced after one that did (each kernel says
+// how), or waits for each of its copies before the next.  So every barrier has
+// at most one phase in flight to drain before the block ends.
 constexpr uint64_t kDrainNs = 2000000000ull;  // whatever the limit of a wait is
 
 struct Waits {
