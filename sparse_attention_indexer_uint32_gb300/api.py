@@ -55,7 +55,8 @@ _c = _lib.library()
 
 # The calls below look their arguments over twice at most: one condition that
 # is true of every right call (a few microseconds), and, where it is not, the
-# checks that say which argument is wrong.
+# checks that say which argument is wrong.  None of them has a backward pass:
+# where gradients are being recorded, tensors that require one are refused.
 
 
 def _same(dtype: torch.dtype, device: torch.device, **tensors) -> None:
@@ -74,6 +75,15 @@ def _whole(shape: tuple, **tensors) -> None:
     for name, t in tensors.items():
         if t is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}: got {tuple(t.shape)}")
+
+
+def _no_grad(**tensors) -> None:
+    """Raises where a gradient would be lost: the calls have no backward pass, and their results are detached."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} requires a gradient and the call has no backward pass: detach it, or call under "
+                                 "torch.no_grad()")
 
 
 def _on_gpu(t: torch.Tensor) -> None:
@@ -101,6 +111,14 @@ def _empty(shape: tuple, dtype: torch.dtype, device: torch.device, stream) -> to
 
 def _is(t: torch.Tensor, dtype: torch.dtype, gpu: int, shape: tuple) -> bool:
     return t.dtype is dtype and t.get_device() == gpu and t.shape == shape and t.is_contiguous()
+
+
+_grad_enabled = torch.is_grad_enabled
+
+
+def _any_grad(a: torch.Tensor, b: torch.Tensor, c: torch.Tensor | None, d: torch.Tensor | None) -> bool:
+    return (a.requires_grad or b.requires_grad or (c is not None and c.requires_grad)
+            or (d is not None and d.requires_grad))
 
 
 def _line(t: torch.Tensor, n: int, gpu: int) -> bool:
@@ -201,6 +219,7 @@ def _check_append(rows, slots, cache, norm_weight, cos_sin, positions):
     _whole((_LATENT,), norm_weight=norm_weight)
     if cos_sin is not None:
         _whole((cos_sin.shape[0], _ROPE), cos_sin=cos_sin)
+    _no_grad(rows=rows, cache=cache, norm_weight=norm_weight, cos_sin=cos_sin)
     _on_gpu(cache)
 
 
@@ -216,7 +235,8 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
             and len(places) == 2 and shape[1] == _WIDTH == places[1] and rows.stride(1) == 1 == cache.stride(1)
             and _line(slots, tokens, gpu) and (positions is None or _line(positions, tokens, gpu))
             and (norm_weight is None or _is(norm_weight, dtype, gpu, (_LATENT,)))
-            and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))):
+            and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))
+            and not (_grad_enabled() and _any_grad(rows, cache, norm_weight, cos_sin))):
         _check_append(rows, slots, cache, norm_weight, cos_sin, positions)
     status = _c.topk_cache_append(
         rows.data_ptr(), rows.stride(0) if tokens > 1 else _WIDTH, tokens,
@@ -237,12 +257,13 @@ def _check_attend(q, cache, out, lse):
     _whole((*q.shape[:-1], _LATENT), out=out)
     _same(_F32, q.device, lse=lse)
     _whole(q.shape[:-1], lse=lse)
+    _no_grad(q=q, cache=cache, out=out, lse=lse)
     _on_gpu(q)
 
 
-def _fits(cache, places, out, lse, gpu, dtype, lead) -> bool:
+def _fits(q, cache, places, out, lse, gpu, dtype, lead) -> bool:
     """Whether they are what both cache attentions take; ``lead``: q's dimensions but the last."""
-    return (gpu >= 0 and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
+    return (gpu >= 0 and not (_grad_enabled() and _any_grad(q, cache, out, lse)) and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
             and places[1] == _WIDTH and cache.stride(1) == 1
             and (out is None or _is(out, dtype, gpu, lead + (_LATENT,)))
             and (lse is None or _is(lse, _F32, gpu, lead)))
@@ -277,7 +298,7 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
             and shape[2] == _WIDTH and steps[2] == 1 and indices.dtype is _I32 and indices.get_device() == gpu
             and (listed[1] <= 1 or indices.stride(1) == 1)
             and (seq_lens is None or _line(seq_lens, shape[0], gpu))
-            and _fits(cache, places, out, lse, gpu, dtype, (shape[0], shape[1]))):
+            and _fits(q, cache, places, out, lse, gpu, dtype, (shape[0], shape[1]))):
         if q.dim() != 3 or indices.dim() != 2 or indices.shape[0] != q.shape[0]:
             raise ValueError(f"q and indices must be [rows, heads, ..] and [rows, k]: got {tuple(q.shape)} and "
                              f"{tuple(indices.shape)}")
@@ -314,7 +335,7 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
     if not (code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
             and shape[3] == _WIDTH and steps[3] == 1 and page_table.dtype is _I32 and page_table.get_device() == gpu
             and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, shape[0], gpu)
-            and _fits(cache, places, out, lse, gpu, dtype, (shape[0], shape[1], shape[2]))):
+            and _fits(q, cache, places, out, lse, gpu, dtype, (shape[0], shape[1], shape[2]))):
         if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
             raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
                              f"{tuple(q.shape)} and {tuple(page_table.shape)}")
@@ -362,6 +383,7 @@ def _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse):
     _same(q.dtype, dev, q=q, k_nope=k_nope, k_rope=k_rope, v=v, out=out)
     _same(_I32, dev, cu_q=cu_q, cu_k=cu_k)
     _same(_F32, dev, lse=lse)
+    _no_grad(q=q, k_nope=k_nope, k_rope=k_rope, v=v, out=out, lse=lse)
     _on_gpu(q)
 
 
@@ -381,7 +403,8 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
             and q_step[2] == k_step[2] == r_step[1] == v_step[2] == 1
             and len(marks) == 1 and _line(cu_q, marks[0], gpu) and _line(cu_k, marks[0], gpu)
             and (out is None or _is(out, dtype, gpu, (shape[0], shape[1], _VALUE)))
-            and (lse is None or _is(lse, _F32, gpu, (shape[0], shape[1])))):
+            and (lse is None or _is(lse, _F32, gpu, (shape[0], shape[1])))
+            and not (_grad_enabled() and (_any_grad(q, k_nope, out, lse) or k_rope.requires_grad or v.requires_grad))):
         _check_prompt(q, k_nope, k_rope, v, cu_q, cu_k, out, lse)
     total_q, heads, _ = shape
     if out is None:
