@@ -8,6 +8,17 @@ import torch
 
 from . import _lib
 
+_current_device = torch.cuda.current_device
+
+
+def _there(fn, gpu: int):
+    """The function with the tensors' GPU as the current one, on which the library launches."""
+    def call(*args):
+        with torch.cuda.device(gpu):
+            return fn(*args)
+
+    return call
+
 
 def plan(seq_lens: torch.Tensor, max_seq_len: int, workspace: torch.Tensor | None = None,
          stream=None) -> torch.Tensor:
@@ -16,7 +27,9 @@ def plan(seq_lens: torch.Tensor, max_seq_len: int, workspace: torch.Tensor | Non
     need = _lib.topk_plan_workspace_bytes(batch)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=seq_lens.device)
-    _lib.topk_plan(seq_lens, batch, max_seq_len, workspace, stream)
+    gpu = seq_lens.get_device()
+    run = _lib.topk_plan if gpu < 0 or _current_device() == gpu else _there(_lib.topk_plan, gpu)
+    run(seq_lens, batch, max_seq_len, workspace, stream)
     return workspace
 
 
@@ -41,8 +54,10 @@ def topk_transform(scores: torch.Tensor, seq_lens: torch.Tensor, page_table: tor
         out = torch.empty((batch, k), dtype=torch.int32, device=scores.device)
     if want_raw and raw_out is None:
         raw_out = torch.empty((batch, k), dtype=torch.int32, device=scores.device)
-    _lib.topk_transform(scores, scores.stride(0), seq_lens, batch, max_seq_len, page_table, page_table.stride(0),
-                        page_size, k, out, raw_out if want_raw else None, workspace, stream)
+    gpu = scores.get_device()
+    run = _lib.topk_transform if gpu < 0 or _current_device() == gpu else _there(_lib.topk_transform, gpu)
+    run(scores, scores.stride(0), seq_lens, batch, max_seq_len, page_table, page_table.stride(0), page_size, k, out,
+        raw_out if want_raw else None, workspace, stream)
     return out, (raw_out if want_raw else None), workspace
 
 
@@ -195,7 +210,7 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         at = 3 * room
         out = BlockTables(buf[at:at + batch], buf[at + batch:at + 2 * batch + 1], buf[:max_tokens],
                           buf[room:room + max_tokens], buf[2 * room:2 * room + max_tokens], buf[at + 2 * batch + 1:])
-    status = _c.topk_block_tables(
+    status = (_c.topk_block_tables if _current_device() == gpu else _there(_c.topk_block_tables, gpu))(
         context_lens.data_ptr(), new_lens.data_ptr(), batch, page_size, free_pages.data_ptr(), num_free,
         page_table.data_ptr(), page_table.stride(0) if batch > 1 else pages, pages, max_tokens, out[0].data_ptr(),
         out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), out[5].data_ptr(),
@@ -238,7 +253,7 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
             and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))
             and not (_grad_enabled() and _any_grad(rows, cache, norm_weight, cos_sin))):
         _check_append(rows, slots, cache, norm_weight, cos_sin, positions)
-    status = _c.topk_cache_append(
+    status = (_c.topk_cache_append if _current_device() == gpu else _there(_c.topk_cache_append, gpu))(
         rows.data_ptr(), rows.stride(0) if tokens > 1 else _WIDTH, tokens,
         None if norm_weight is None else norm_weight.data_ptr(), eps, None if cos_sin is None else cos_sin.data_ptr(),
         positions_n, None if positions is None else positions.data_ptr(), interleaved,
@@ -313,7 +328,7 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
         lse = _empty((rows, heads), _F32, q.device, stream)
     workspace, room = _attend_workspace(workspace, rows, 1, heads, q.device, stream)
     slots = places[0]
-    status = _c.topk_attend_selected(
+    status = (_c.topk_attend_selected if _current_device() == gpu else _there(_c.topk_attend_selected, gpu))(
         q.data_ptr(), steps[0] if rows > 1 else _WIDTH, steps[1] if heads > 1 else _WIDTH, cache.data_ptr(),
         cache.stride(0) if slots > 1 else _WIDTH, slots, indices.data_ptr(),
         indices.stride(0) if rows > 1 else listed[1], None if seq_lens is None else seq_lens.data_ptr(), rows, heads,
@@ -356,7 +371,7 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
         lse = _empty((batch, queries, heads), _F32, q.device, stream)
     workspace, room = _attend_workspace(workspace, batch, queries, heads, q.device, stream)
     slots = places[0]
-    status = _c.topk_attend_paged(
+    status = (_c.topk_attend_paged if _current_device() == gpu else _there(_c.topk_attend_paged, gpu))(
         q.data_ptr(), steps[0] if batch > 1 else _WIDTH, steps[1] if queries > 1 else _WIDTH,
         steps[2] if heads > 1 else _WIDTH, cache.data_ptr(), cache.stride(0) if slots > 1 else _WIDTH, slots,
         seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else listed[1], page_size,
@@ -413,7 +428,7 @@ def attend_prompt(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v
         lse = _empty((total_q, heads), _F32, q.device, stream)
     # The stride of a dimension of one entry means nothing.
     many_q, many_k, many_heads = total_q > 1, tokens > 1, heads > 1
-    status = _c.topk_attend_prompt(
+    status = (_c.topk_attend_prompt if _current_device() == gpu else _there(_c.topk_attend_prompt, gpu))(
         q.data_ptr(), q_step[0] if many_q else _NOPE + _ROPE, q_step[1] if many_heads else _NOPE + _ROPE,
         k_nope.data_ptr(), k_step[0] if many_k else _NOPE, k_step[1] if many_heads else _NOPE, k_rope.data_ptr(),
         r_step[0] if many_k else _ROPE, v.data_ptr(), v_step[0] if many_k else _VALUE,
