@@ -8,7 +8,9 @@ import torch
 
 from . import _lib
 
-_current_device = torch.cuda.current_device
+# The current device's index, without the look at CUDA's state around it, which
+# a tensor on a GPU has set up, where this torch has that call.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _there(fn, gpu: int):
