@@ -290,10 +290,12 @@ topk_status_t topk_block_tables(const int32_t* context_lens, const int32_t* new_
  *   positions         device int32[tokens]; needed with cos_sin.
  *   slots             device int32[tokens]; a row whose slot is outside
  *                     [0, num_slots), or whose position is outside
- *                     [0, num_positions), is not written.  Which of two rows
- *                     with one slot stays is not specified.
+ *                     [0, num_positions), is not written.  What a slot holds
+ *                     that two rows are sent to (one of them, or parts of
+ *                     both) is not specified.
  *   cache             device [num_slots][slot_stride].
  *   tokens            >= 0 (0: nothing is enqueued).
+ * No input may lie in a slot that is written.
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
  */
 topk_status_t topk_cache_append(const void* rows, int64_t row_stride, int32_t tokens, const void* norm_weight_or_null,
@@ -306,7 +308,8 @@ topk_status_t topk_cache_append(const void* rows, int64_t row_stride, int32_t to
  * Bytes of device workspace (16-byte aligned, contents free) that
  * topk_attend_selected and topk_attend_paged need for batch rows of `queries`
  * queries (selected: 1) and `heads` heads: the partial sums of rows that
- * several blocks share.  0 for arguments out of range.
+ * several blocks share.  Calls that may run at the same time (on two streams)
+ * need a workspace each.  0 for arguments out of range.
  */
 size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
 
@@ -329,7 +332,7 @@ size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads
  *   cache             device [num_slots][slot_stride], 576 values used.
  *   indices           device int32[rows][indices_stride], k used per row.
  *   rows, heads, k    >= 1; rows * heads <= 2^30, and less than 2^31 tiles of
- *                     64 slots by 128 heads in all.
+ *                     128 slots by 128 heads in all.
  *   out               device [rows][heads][512], contiguous, 32-byte aligned.
  *   lse_or_null       device float[rows][heads].
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_ENOSPACE, TOPK_EDEVICE, TOPK_ECUDA.
@@ -373,7 +376,8 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
  * Request b has the queries cu_q[b]..cu_q[b+1]-1 and the keys
  * cu_k[b]..cu_k[b+1]-1.  A query sees its request's keys; with causal != 0
  * the request's last query sees all of them and each one before it one key
- * less.  A query that sees nothing gets zeros and an lse of -inf; tokens that
+ * less.  Products, sums and weights are rounded as in topk_attend_selected.  A
+ * query that sees nothing gets zeros and an lse of -inf; tokens that
  * are in no request are not written.  Keys and values of other requests, or
  * of none, are never used, whatever they hold; values of one request that a
  * query does not see (causal) must be finite.

@@ -73,7 +73,10 @@ _c = _lib.library()
 # The calls below look their arguments over twice at most: one condition that
 # is true of every right call (a few microseconds), and, where it is not, the
 # checks that say which argument is wrong.  None of them has a backward pass:
-# where gradients are being recorded, tensors that require one are refused.
+# where gradients are being recorded, tensors that require one are refused.  The
+# attention calls do not wait for their kernels: topk_read_attend_flags of the
+# binding says afterwards whether a bounded wait of one gave up, which makes
+# that call's output void.
 
 
 def _same(dtype: torch.dtype, device: torch.device, **tensors) -> None:
@@ -308,7 +311,8 @@ def attend_selected(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Runs ``topk_attend_selected``: ``q`` [rows, heads, 576] over the slots ``indices`` [rows, k] (int32, as
     :func:`topk_transform` writes them) of ``cache`` [num_slots, 576].  ``seq_lens`` [rows], where given, bounds
-    the slots looked at.  Returns ``(out [rows, heads, 512], lse [rows, heads], workspace)``."""
+    the slots looked at.  Returns ``(out [rows, heads, 512], lse [rows, heads], workspace)``; the workspace serves
+    later calls on the same stream."""
     gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, indices.shape, cache.shape, q.stride()
     code = _DTYPES.get(dtype)
     if not (code is not None and len(shape) == 3 and len(listed) == 2 and listed[0] == shape[0]

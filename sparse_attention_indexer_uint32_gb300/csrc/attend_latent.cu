@@ -34,11 +34,12 @@
 // bits).
 //
 // Measured (with the join): 16 rows of 32768 to 131072 tokens, pages of 64, 128
-// heads 301 us, 5.0 TB/s (74 % of the measured copy rate) and 1.21 PFLOP/s, bound
-// by the copies' way into shared memory and, for long calls, the power limit;
-// 2048 rows of up to 512 slots, 16 heads 245 us, 4.9 TB/s; 128 rows of 2048 slots,
-// 128 heads 84 us, of which about 8 us pass before the first product and 11 in the
-// join; one such row 14.5 us, four fifths of it waiting for memory in turn.
+// heads 292 to 308 us, 4.9 to 5.2 TB/s (73 to 76 % of the measured copy rate) and
+// 1.18 to 1.25 PFLOP/s, by memory and products together at the power limit; 2048
+// rows of up to 512 slots, 16 heads 238 to 250 us, 4.8 to 5.1 TB/s; 128 rows of
+// 2048 slots, 128 heads 83 to 85 us, of which about 8 us pass before the first
+// product and 11 in the join; one such row 14.2 to 15.3 us, four fifths of it
+// waiting for memory in turn.
 //
 // Warps of each block: 0-3 softmax and results (thread t: row t & 63, half t >> 6
 // of the tile's slots, values 256 (t >> 6).. of the sums), 4 products (first

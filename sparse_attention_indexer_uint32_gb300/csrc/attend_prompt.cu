@@ -19,11 +19,13 @@
 //
 // One block per SM takes pieces of work in turn, so that the next piece's
 // queries, keys and first scores are under way while this one's results are
-// written (a block a piece: 469 and 103 us for the two cases below).
+// written (a block a piece: 469 us where this took 455, and 103 where it took 99,
+// on the two cases below).
 //
-// Measured: a prompt of 8192 tokens, 32 heads, causal 455 us, 1.51 PFLOP/s (78 %
-// of the measured burst rate, 88 % of the sustained one, at the power limit); 8
-// pieces of up to 1024 tokens after up to 4096 cached ones, 16 heads 99 us.  A
+// Measured: a prompt of 8192 tokens, 32 heads, causal 459 to 474 us, 1.45 to 1.50
+// PFLOP/s (75 to 78 % of the measured burst rate, 84 to 87 % of the sustained
+// one, at the power limit); 8 pieces of up to 1024 tokens after up to 4096
+// cached ones, 16 heads 95 to 106 us.  A
 // step takes 3150 cycles for 2560 of products: the first product reads 128 bytes a
 // cycle from shared memory, all there is, beside the copies' writes (92 cycles in
 // place of 64).  Pairs of blocks with products of M = 256, which read less, were 3 %

@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import torch
 
-from . import api
+from . import _lib, api
 
 HEADS, LATENT, ROPE, NOPE, VALUE = 16, 512, 64, 128, 128
 SCALE = (NOPE + ROPE) ** -0.5
@@ -96,6 +96,10 @@ def main() -> None:
         gap = (selected[short].float() - whole[short].float()).abs().max().item()
         print("decode: lengths", layer.lens.tolist(), "pages", int(step.status[0]), "selected", tuple(selected.shape),
               f"rows that were selected whole differ by {gap:.1e}")
+    # Where the host waits anyway: a wait of a kernel that gave up makes the
+    # outputs of its call void.
+    if _lib.topk_read_attend_flags(clear=True):
+        raise RuntimeError("a wait of an attention kernel gave up")
 
 
 if __name__ == "__main__":
