@@ -408,7 +408,9 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
  * GPU, shared by all calls) to *flags_host after all work enqueued on
  * `stream` so far (this call synchronises the stream).  TOPK_FLAG_TIMEOUT: a
  * bounded device wait of some call since the last clearing gave up and that
- * call's output is void.  clear != 0 resets the word afterwards.  The first
+ * call's output is void (a wait may span the work on one row or piece: calls
+ * that take seconds need a higher wait_limit_us).  clear != 0 resets the word
+ * afterwards.  The first
  * call of an attention entry point on a device looks up the word's address;
  * make it before any stream capture.
  */
