@@ -223,6 +223,8 @@ topk_status_t topk_transform_noalloc(const float* scores, int64_t row_stride, co
 #define TOPK_ROPE_DIM 64
 #define TOPK_NOPE_DIM 128 /* unrotated values per head of the expanded form */
 #define TOPK_VALUE_DIM 128 /* values per value head of the expanded form    */
+#define TOPK_INDEX_DIM 128 /* values of an index key and of an index query head */
+#define TOPK_INDEX_MAX_HEADS 256
 
 typedef enum {
     TOPK_BF16 = 0,
@@ -305,6 +307,70 @@ topk_status_t topk_cache_append(const void* rows, int64_t row_stride, int32_t to
                                 topk_stream_t stream);
 
 /*
+ * Writes the indexer's keys to their slots of a paged cache of their own: the
+ * layer norm of the 128 values, the rotation of 64 of them, and the store in
+ * one pass.
+ *   y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * norm_weight + norm_bias
+ *                                             (norm_weight NULL: y = x)
+ *   (a, b)' = (a cos - b sin, a sin + b cos)  (cos_sin NULL: unchanged)
+ * for pair i = 0..31 of the rotary values, which are the first 64, or, with
+ * rope_last != 0, the last: (2i, 2i + 1) of them if interleaved, else
+ * (i, i + 32).  Norm and rotation are computed in fp32 and rounded once.
+ *   rows              device [tokens][row_stride], 128 values used per row.
+ *   norm_weight_or_null, norm_bias_or_null  device [128], the rows' type; a
+ *                     bias only with a weight.
+ *   cos_sin_or_null, positions, slots, tokens  as in topk_cache_append.
+ *   cache             device [num_slots][slot_stride], 128 values used.
+ * No input may lie in a slot that is written.
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+topk_status_t topk_index_append(const void* rows, int64_t row_stride, int32_t tokens, const void* norm_weight_or_null,
+                                const void* norm_bias_or_null, float eps, const float* cos_sin_or_null,
+                                int32_t num_positions, const int32_t* positions_or_null, int32_t interleaved,
+                                int32_t rope_last, const int32_t* slots, void* cache, int64_t slot_stride,
+                                int32_t num_slots, topk_dtype_t dtype, topk_stream_t stream);
+
+/*
+ * The indexer's scores, which topk_transform selects from:
+ *   scores[i][t] = sum_h weights[i][h] * max(q[i][h][:] . cache[slot][:], 0)
+ * over 128 values a head, for the queries i of ragged requests and the
+ * positions t that each sees, whose slot is
+ * page_table[b][t / page_size] * page_size + t % page_size.  Request b has the
+ * queries cu_q[b]..cu_q[b+1]-1 (cu_q NULL: total_q / batch each), its newest
+ * tokens: the last sees t < seq_lens[b] (values above max_seq_len count as
+ * max_seq_len, negative ones as 0), each one before it one position less.
+ * Positions that a query does not see, and queries of no request, are left as
+ * they were (the selection reads a row up to its length only); a position
+ * whose slot is outside [0, num_slots) scores -inf.  A NaN among a key's
+ * products goes to that position's score; what other slots hold is not used.
+ * Products of two-byte values are exact and summed in fp32.
+ *   q                 device [total_q][q_token_stride], head h at h * q_head_stride
+ *                     (strides of at least 128 where there is more than one).
+ *   weights           device float[total_q][weights_stride], heads used per row.
+ *   cache             device [num_slots][slot_stride], 128 values used.
+ *   seq_lens          device int32[batch].
+ *   page_table        as in topk_transform; page_table_stride >=
+ *                     ceil(max_seq_len / page_size).
+ *   cu_q_or_null      device int32[batch + 1]; values outside [0, total_q] are
+ *                     clamped to it, and a request that ends before it begins
+ *                     has no queries.  No query may be in two requests.  NULL:
+ *                     total_q is a multiple of batch.
+ *   heads             1..TOPK_INDEX_MAX_HEADS.
+ *   total_q           >= 0 (0: nothing is enqueued); with batch and max_seq_len
+ *                     such that (total_q + batch) * ceil(max_seq_len / 128) < 2^31.
+ *   scores            device float[total_q][scores_stride], scores_stride >=
+ *                     max_seq_len; no input may lie in it.
+ * Waits are bounded as those of the attention calls (topk_read_attend_flags).
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+topk_status_t topk_index_scores(const void* q, int64_t q_token_stride, int64_t q_head_stride, const float* weights,
+                                int64_t weights_stride, const void* cache, int64_t slot_stride, int32_t num_slots,
+                                const int32_t* seq_lens, const int32_t* page_table, int64_t page_table_stride,
+                                int32_t page_size, int32_t max_seq_len, const int32_t* cu_q_or_null, int32_t batch,
+                                int32_t total_q, int32_t heads, topk_dtype_t dtype, float* scores, int64_t scores_stride,
+                                topk_stream_t stream);
+
+/*
  * Bytes of device workspace (16-byte aligned, contents free) that
  * topk_attend_selected and topk_attend_paged need for batch rows of `queries`
  * queries (selected: 1) and `heads` heads: the partial sums of rows that
@@ -367,6 +433,36 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
                                 int32_t max_seq_len, int32_t batch, int32_t queries, int32_t heads, float scale,
                                 topk_dtype_t dtype, void* out, float* lse_or_null, void* workspace,
                                 size_t workspace_bytes, topk_stream_t stream);
+
+/*
+ * topk_attend_paged for requests whose first positions are the same (a common
+ * prompt), which are read once for all of them: position t of request b is
+ * found through shared_pages[t / page_size] where t < shared_len, and through
+ * page_table[b][t / page_size] from there on.  Lengths, what each query sees,
+ * and the rest are as in topk_attend_paged: seq_lens counts the shared
+ * positions, and a request shorter than shared_len sees as many as it has.
+ *   shared_pages      device int32[num_shared_pages] (may be a row of the
+ *                     page table); the entries of the rows below shared_len /
+ *                     page_size are not read.
+ *   shared_len        device int32[1]; values outside [0,
+ *                     min(num_shared_pages * page_size, max_seq_len)] are
+ *                     clamped to it.  It may end inside a page.
+ * What slots past a request's length hold is not used, nor what the page at
+ * which its own positions begin holds before them; the shared positions and
+ * the rows of its own newest tokens must be finite.
+ *   workspace         of topk_attend_shared_workspace_bytes(batch, queries,
+ *                     heads) bytes, 16-byte aligned, contents free; calls that
+ *                     may run at the same time need one each.
+ * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_ENOSPACE, TOPK_EDEVICE, TOPK_ECUDA.
+ */
+size_t topk_attend_shared_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
+topk_status_t topk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_query_stride, int64_t q_head_stride,
+                                 const void* cache, int64_t slot_stride, int32_t num_slots, const int32_t* seq_lens,
+                                 const int32_t* page_table, int64_t page_table_stride, const int32_t* shared_pages,
+                                 int32_t num_shared_pages, const int32_t* shared_len, int32_t page_size,
+                                 int32_t max_seq_len, int32_t batch, int32_t queries, int32_t heads, float scale,
+                                 topk_dtype_t dtype, void* out, float* lse_or_null, void* workspace,
+                                 size_t workspace_bytes, topk_stream_t stream);
 
 /*
  * Latent attention in its expanded form, for prompts (ragged, one launch):

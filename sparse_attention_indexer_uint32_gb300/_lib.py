@@ -34,6 +34,8 @@ TOPK_LATENT_DIM = 512
 TOPK_ROPE_DIM = 64
 TOPK_NOPE_DIM = 128
 TOPK_VALUE_DIM = 128
+TOPK_INDEX_DIM = 128
+TOPK_INDEX_MAX_HEADS = 256
 
 TOPK_BF16 = 0
 TOPK_FP16 = 1
@@ -53,9 +55,13 @@ EXPORTED = (
     "topk_key_map",
     "topk_block_tables",
     "topk_cache_append",
+    "topk_index_append",
+    "topk_index_scores",
     "topk_attend_workspace_bytes",
     "topk_attend_selected",
     "topk_attend_paged",
+    "topk_attend_shared_workspace_bytes",
+    "topk_attend_shared",
     "topk_attend_prompt",
     "topk_read_attend_flags",
     "topk_read_flags",
@@ -130,6 +136,16 @@ def _load() -> ctypes.CDLL:
     lib.topk_block_tables.restype = ctypes.c_int
     lib.topk_cache_append.argtypes = [p, i64, i32, p, f32, p, i32, p, i32, p, p, i64, i32, ctypes.c_int, p]
     lib.topk_cache_append.restype = ctypes.c_int
+    lib.topk_index_append.argtypes = [p, i64, i32, p, p, f32, p, i32, p, i32, i32, p, p, i64, i32, ctypes.c_int, p]
+    lib.topk_index_append.restype = ctypes.c_int
+    lib.topk_index_scores.argtypes = [p, i64, i64, p, i64, p, i64, i32, p, p, i64, i32, i32, p, i32, i32, i32,
+                                      ctypes.c_int, p, i64, p]
+    lib.topk_index_scores.restype = ctypes.c_int
+    lib.topk_attend_shared_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.topk_attend_shared_workspace_bytes.restype = sz
+    lib.topk_attend_shared.argtypes = [p, i64, i64, i64, p, i64, i32, p, p, i64, p, i32, p, i32, i32, i32, i32, i32, f32,
+                                       ctypes.c_int, p, p, p, sz, p]
+    lib.topk_attend_shared.restype = ctypes.c_int
     lib.topk_attend_workspace_bytes.argtypes = [i32, i32, i32]
     lib.topk_attend_workspace_bytes.restype = sz
     lib.topk_attend_selected.argtypes = [p, i64, i64, p, i64, i32, p, i64, p, i32, i32, i32, f32, ctypes.c_int, p, p,
@@ -283,6 +299,48 @@ def topk_cache_append(rows: torch.Tensor, row_stride: int, tokens: int, norm_wei
         _ptr(rows), row_stride, tokens, _ptr(norm_weight_or_null), eps, _ptr(cos_sin_or_null), num_positions,
         _ptr(positions_or_null), int(interleaved), _ptr(slots), _ptr(cache), slot_stride, num_slots, dtype,
         _stream(stream, cache.device)))
+
+
+def topk_index_append(rows: torch.Tensor, row_stride: int, tokens: int, norm_weight_or_null: torch.Tensor | None,
+                      norm_bias_or_null: torch.Tensor | None, eps: float, cos_sin_or_null: torch.Tensor | None,
+                      num_positions: int, positions_or_null: torch.Tensor | None, interleaved: bool, rope_last: bool,
+                      slots: torch.Tensor, cache: torch.Tensor, slot_stride: int, num_slots: int, dtype: int,
+                      stream=None) -> None:
+    """Layer norm, rotation and paged store of index keys."""
+    _check("topk_index_append", _lib.topk_index_append(
+        _ptr(rows), row_stride, tokens, _ptr(norm_weight_or_null), _ptr(norm_bias_or_null), eps, _ptr(cos_sin_or_null),
+        num_positions, _ptr(positions_or_null), int(interleaved), int(rope_last), _ptr(slots), _ptr(cache), slot_stride,
+        num_slots, dtype, _stream(stream, cache.device)))
+
+
+def topk_index_scores(q: torch.Tensor, q_token_stride: int, q_head_stride: int, weights: torch.Tensor,
+                      weights_stride: int, cache: torch.Tensor, slot_stride: int, num_slots: int,
+                      seq_lens: torch.Tensor, page_table: torch.Tensor, page_table_stride: int, page_size: int,
+                      max_seq_len: int, cu_q_or_null: torch.Tensor | None, batch: int, total_q: int, heads: int,
+                      dtype: int, scores: torch.Tensor, scores_stride: int, stream=None) -> None:
+    """The indexer's scores over its paged keys."""
+    _check("topk_index_scores", _lib.topk_index_scores(
+        _ptr(q), q_token_stride, q_head_stride, _ptr(weights), weights_stride, _ptr(cache), slot_stride, num_slots,
+        _ptr(seq_lens), _ptr(page_table), page_table_stride, page_size, max_seq_len, _ptr(cu_q_or_null), batch, total_q,
+        heads, dtype, _ptr(scores), scores_stride, _stream(stream, q.device)))
+
+
+def topk_attend_shared_workspace_bytes(batch: int, queries: int, heads: int) -> int:
+    return int(_lib.topk_attend_shared_workspace_bytes(batch, queries, heads))
+
+
+def topk_attend_shared(q: torch.Tensor, q_row_stride: int, q_query_stride: int, q_head_stride: int,
+                       cache: torch.Tensor, slot_stride: int, num_slots: int, seq_lens: torch.Tensor,
+                       page_table: torch.Tensor, page_table_stride: int, shared_pages: torch.Tensor | None,
+                       num_shared_pages: int, shared_len: torch.Tensor, page_size: int, max_seq_len: int, batch: int,
+                       queries: int, heads: int, scale: float, dtype: int, out: torch.Tensor,
+                       lse_or_null: torch.Tensor | None, workspace: torch.Tensor, stream=None) -> None:
+    """Latent attention for requests whose first positions are the same."""
+    _check("topk_attend_shared", _lib.topk_attend_shared(
+        _ptr(q), q_row_stride, q_query_stride, q_head_stride, _ptr(cache), slot_stride, num_slots, _ptr(seq_lens),
+        _ptr(page_table), page_table_stride, _ptr(shared_pages), num_shared_pages, _ptr(shared_len), page_size,
+        max_seq_len, batch, queries, heads, scale, dtype, _ptr(out), _ptr(lse_or_null), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream, q.device)))
 
 
 def topk_attend_workspace_bytes(batch: int, queries: int, heads: int) -> int:

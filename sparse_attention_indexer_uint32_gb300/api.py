@@ -66,6 +66,7 @@ def topk_transform(scores: torch.Tensor, seq_lens: torch.Tensor, page_table: tor
 _DTYPES = {torch.bfloat16: _lib.TOPK_BF16, torch.float16: _lib.TOPK_FP16}
 _LATENT, _ROPE, _NOPE, _VALUE = _lib.TOPK_LATENT_DIM, _lib.TOPK_ROPE_DIM, _lib.TOPK_NOPE_DIM, _lib.TOPK_VALUE_DIM
 _WIDTH = _LATENT + _ROPE
+_INDEX = _lib.TOPK_INDEX_DIM
 _I32, _F32 = torch.int32, torch.float32
 _c = _lib.library()
 
@@ -268,8 +269,121 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
         _lib.check("topk_cache_append", status)
 
 
+def _check_index_append(rows, slots, cache, norm_weight, norm_bias, cos_sin, positions):
+    dev = cache.device
+    _dtype(cache, "cache")
+    _same(cache.dtype, dev, rows=rows, cache=cache, norm_weight=norm_weight, norm_bias=norm_bias)
+    _same(_I32, dev, slots=slots, positions=positions)
+    _same(_F32, dev, cos_sin=cos_sin)
+    if rows.dim() != 2 or cache.dim() != 2 or rows.shape[1] != _INDEX or cache.shape[1] != _INDEX:
+        raise ValueError(f"rows and cache must be [.., {_INDEX}]: got {tuple(rows.shape)} and {tuple(cache.shape)}")
+    _whole((rows.shape[0],), slots=slots, positions=positions)
+    _whole((_INDEX,), norm_weight=norm_weight, norm_bias=norm_bias)
+    if cos_sin is not None:
+        _whole((cos_sin.shape[0], _ROPE), cos_sin=cos_sin)
+    _no_grad(rows=rows, cache=cache, norm_weight=norm_weight, norm_bias=norm_bias, cos_sin=cos_sin)
+    _on_gpu(cache)
+
+
+def index_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
+                 norm_weight: torch.Tensor | None = None, norm_bias: torch.Tensor | None = None, eps: float = 1e-6,
+                 cos_sin: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
+                 rope_last: bool = False, stream=None) -> None:
+    """Runs ``topk_index_append``: the indexer's keys ``rows`` [tokens, 128] to ``slots`` of their ``cache``
+    [num_slots, 128], layer-normed by ``norm_weight`` and ``norm_bias`` [128] and, in their first 64 values (the last
+    with ``rope_last``), rotated by ``cos_sin`` (as in :func:`cache_append`) at ``positions``, where these are given."""
+    gpu, dtype, shape, places = cache.get_device(), cache.dtype, rows.shape, cache.shape
+    code, tokens, positions_n = _DTYPES.get(dtype), shape[0] if shape else 0, 0 if cos_sin is None else cos_sin.shape[0]
+    if not (gpu >= 0 and code is not None and rows.dtype is dtype and rows.get_device() == gpu and len(shape) == 2
+            and len(places) == 2 and shape[1] == _INDEX == places[1] and rows.stride(1) == 1 == cache.stride(1)
+            and _line(slots, tokens, gpu) and (positions is None or _line(positions, tokens, gpu))
+            and (norm_weight is None or _is(norm_weight, dtype, gpu, (_INDEX,)))
+            and (norm_bias is None or _is(norm_bias, dtype, gpu, (_INDEX,)))
+            and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))
+            and not (_grad_enabled() and (_any_grad(rows, cache, norm_weight, norm_bias)
+                                          or (cos_sin is not None and cos_sin.requires_grad)))):
+        _check_index_append(rows, slots, cache, norm_weight, norm_bias, cos_sin, positions)
+    status = (_c.topk_index_append if _current_device() == gpu else _there(_c.topk_index_append, gpu))(
+        rows.data_ptr(), rows.stride(0) if tokens > 1 else _INDEX, tokens,
+        None if norm_weight is None else norm_weight.data_ptr(), None if norm_bias is None else norm_bias.data_ptr(), eps,
+        None if cos_sin is None else cos_sin.data_ptr(), positions_n, None if positions is None else positions.data_ptr(),
+        interleaved, rope_last, slots.data_ptr(), cache.data_ptr(), cache.stride(0) if places[0] > 1 else _INDEX, places[0],
+        code, _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_index_append", status)
+
+
+def _check_index_scores(q, weights, cache, seq_lens, page_table, page_size, cu_q, max_seq_len, out):
+    dev = q.device
+    _dtype(q, "q")
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError(f"q and page_table must be [tokens, heads, ..] and [batch, pages]: got {tuple(q.shape)} and "
+                         f"{tuple(page_table.shape)}")
+    (total, heads, width), batch = q.shape, page_table.shape[0]
+    _same(q.dtype, dev, q=q, cache=cache)
+    if width != _INDEX or cache.dim() != 2 or cache.shape[1] != _INDEX:
+        raise ValueError(f"q and cache must be [.., {_INDEX}]: got {tuple(q.shape)} and {tuple(cache.shape)}")
+    _same(_F32, dev, weights=weights, out=out)
+    if tuple(weights.shape) != (total, heads):
+        raise ValueError(f"weights must be {(total, heads)}: got {tuple(weights.shape)}")
+    _same(_I32, dev, seq_lens=seq_lens, page_table=page_table, cu_q=cu_q)
+    _whole((batch,), seq_lens=seq_lens)
+    _whole((batch + 1,), cu_q=cu_q)
+    if cu_q is None and (batch == 0 or total % batch):
+        raise ValueError(f"without cu_q the {total} queries must be as many for each of the {batch} requests")
+    if max_seq_len is not None and max_seq_len > page_table.shape[1] * page_size:
+        raise ValueError(f"max_seq_len {max_seq_len} is over {page_table.shape[1]} pages of {page_size}")
+    if out is not None:
+        most = page_table.shape[1] * page_size if max_seq_len is None else max_seq_len
+        if out.dim() != 2 or out.shape[0] != total or out.shape[1] < most:
+            raise ValueError(f"out must be [{total}, {most} or more]: got {tuple(out.shape)}")
+    _no_grad(q=q, weights=weights, cache=cache, out=out)
+    _on_gpu(q)
+
+
+def index_scores(q: torch.Tensor, weights: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor,
+                 page_table: torch.Tensor, page_size: int, cu_q: torch.Tensor | None = None,
+                 max_seq_len: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Runs ``topk_index_scores``: the scores that :func:`topk_transform` selects from, of the index queries ``q``
+    [tokens, heads, 128] with ``weights`` [tokens, heads] (float32) over the keys ``cache`` [num_slots, 128] of their
+    requests, through ``page_table`` [batch, pages].  ``cu_q`` [batch + 1]: the requests' queries, their newest
+    tokens (None: as many for each).  Returns ``out`` [tokens, max_seq_len or more] (float32; new memory has
+    max_seq_len rounded up to a multiple of 4), of which each query's row is written up to what it sees: the last
+    query of a request ``seq_lens`` positions, each one before it one less."""
+    gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
+    code = _DTYPES.get(dtype)
+    most = min(listed[1] * page_size, 2 ** 31 - 1) if max_seq_len is None and len(listed) == 2 else max_seq_len
+    if not (gpu >= 0 and code is not None and len(shape) == 3 and len(listed) == 2 and shape[2] == _INDEX
+            and steps[2] == 1 and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
+            and places[1] == _INDEX and cache.stride(1) == 1 and weights.dtype is _F32 and weights.get_device() == gpu
+            and weights.shape == shape[:2] and (shape[1] <= 1 or weights.stride(1) == 1)
+            and page_table.dtype is _I32 and page_table.get_device() == gpu
+            and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, listed[0], gpu)
+            and (_line(cu_q, listed[0] + 1, gpu) if cu_q is not None else listed[0] > 0 and shape[0] % listed[0] == 0)
+            and most <= listed[1] * page_size
+            and (out is None or (out.dtype is _F32 and out.get_device() == gpu and out.dim() == 2
+                                 and out.shape[0] == shape[0] and out.shape[1] >= most
+                                 and (out.shape[1] <= 1 or out.stride(1) == 1)))
+            and not (_grad_enabled() and _any_grad(q, weights, cache, out))):
+        _check_index_scores(q, weights, cache, seq_lens, page_table, page_size, cu_q, max_seq_len, out)
+    total, heads, _ = shape
+    batch, slots = listed[0], places[0]
+    if out is None:
+        out = _empty((total, (most + 3) // 4 * 4), _F32, q.device, stream)
+    many = total > 1
+    status = (_c.topk_index_scores if _current_device() == gpu else _there(_c.topk_index_scores, gpu))(
+        q.data_ptr(), steps[0] if many else _INDEX, steps[1] if heads > 1 else _INDEX, weights.data_ptr(),
+        weights.stride(0) if many else heads, cache.data_ptr(), cache.stride(0) if slots > 1 else _INDEX, slots,
+        seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else listed[1], page_size, most,
+        None if cu_q is None else cu_q.data_ptr(), batch, total, heads, code, out.data_ptr(),
+        out.stride(0) if many else out.shape[1], _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_index_scores", status)
+    return out
+
+
 def _check_attend(q, cache, out, lse):
-    """What both cache attentions share."""
+    """What the cache attentions share."""
     _dtype(q, "q")
     _same(q.dtype, q.device, q=q, cache=cache, out=out)
     if q.shape[-1] != _WIDTH or cache.dim() != 2 or cache.shape[1] != _WIDTH:
@@ -282,7 +396,7 @@ def _check_attend(q, cache, out, lse):
 
 
 def _fits(q, cache, places, out, lse, gpu, dtype, lead) -> bool:
-    """Whether they are what both cache attentions take; ``lead``: q's dimensions but the last."""
+    """Whether they are what the cache attentions take; ``lead``: q's dimensions but the last."""
     return (gpu >= 0 and not (_grad_enabled() and _any_grad(q, cache, out, lse)) and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
             and places[1] == _WIDTH and cache.stride(1) == 1
             and (out is None or _is(out, dtype, gpu, lead + (_LATENT,)))
@@ -296,7 +410,11 @@ def _workspace_bytes(batch: int, queries: int, heads: int) -> int:
 
 def _attend_workspace(workspace, batch, queries, heads, device, stream):
     """The workspace and its bytes."""
-    need = _workspace_bytes(batch, queries, heads)
+    return _room(workspace, _workspace_bytes(batch, queries, heads), device, stream)
+
+
+def _room(workspace, need, device, stream):
+    """The workspace, a new one where it is too small, and its bytes."""
     if workspace is not None:
         if workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous on {device}: got {workspace.device}")
@@ -385,6 +503,59 @@ def attend_paged(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, p
         _lib.stream_handle(stream, gpu))
     if status:
         _lib.check("topk_attend_paged", status)
+    return out, lse, workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _shared_workspace_bytes(batch: int, queries: int, heads: int) -> int:
+    return _lib.topk_attend_shared_workspace_bytes(batch, queries, heads)
+
+
+def attend_shared(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, page_table: torch.Tensor,
+                  shared_pages: torch.Tensor, shared_len: torch.Tensor, page_size: int, scale: float,
+                  max_seq_len: int | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Runs ``topk_attend_shared``: :func:`attend_paged` for requests whose first ``shared_len`` [1] positions are the
+    same, which are read once for all through ``shared_pages`` [pages]; those after them through each request's row of
+    ``page_table``.  ``seq_lens`` counts both.  Returns ``(out [batch, queries, heads, 512], lse [batch, queries,
+    heads], workspace)``."""
+    gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
+    code, common = _DTYPES.get(dtype), shared_pages.numel()
+    if not (code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
+            and shape[3] == _WIDTH and steps[3] == 1 and page_table.dtype is _I32 and page_table.get_device() == gpu
+            and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, shape[0], gpu)
+            and _line(shared_pages, common, gpu) and _line(shared_len, 1, gpu)
+            and _fits(q, cache, places, out, lse, gpu, dtype, (shape[0], shape[1], shape[2]))):
+        if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
+            raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
+                             f"{tuple(q.shape)} and {tuple(page_table.shape)}")
+        _dtype(q, "q")
+        _same(_I32, q.device, seq_lens=seq_lens, page_table=page_table, shared_pages=shared_pages, shared_len=shared_len)
+        _whole(shape[:1], seq_lens=seq_lens)
+        _whole((common,), shared_pages=shared_pages)
+        _whole((1,), shared_len=shared_len.reshape(-1))
+        if max_seq_len is not None and max_seq_len > listed[1] * page_size:
+            raise ValueError(f"max_seq_len {max_seq_len} is over {listed[1]} pages of {page_size}")
+        _check_attend(q, cache, out, lse)
+    batch, queries, heads, _ = shape
+    if max_seq_len is None:
+        max_seq_len = min(listed[1] * page_size, 2 ** 31 - 1)
+    elif max_seq_len > listed[1] * page_size:
+        raise ValueError(f"max_seq_len {max_seq_len} is over {listed[1]} pages of {page_size}")
+    if out is None:
+        out = _empty((batch, queries, heads, _LATENT), dtype, q.device, stream)
+    if lse is None:
+        lse = _empty((batch, queries, heads), _F32, q.device, stream)
+    workspace, room = _room(workspace, _shared_workspace_bytes(batch, queries, heads), q.device, stream)
+    slots = places[0]
+    status = (_c.topk_attend_shared if _current_device() == gpu else _there(_c.topk_attend_shared, gpu))(
+        q.data_ptr(), steps[0] if batch > 1 else _WIDTH, steps[1] if queries > 1 else _WIDTH,
+        steps[2] if heads > 1 else _WIDTH, cache.data_ptr(), cache.stride(0) if slots > 1 else _WIDTH, slots,
+        seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else listed[1],
+        shared_pages.data_ptr(), common, shared_len.data_ptr(), page_size, max_seq_len, batch, queries, heads, scale, code,
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room, _lib.stream_handle(stream, gpu))
+    if status:
+        _lib.check("topk_attend_shared", status)
     return out, lse, workspace
 
 

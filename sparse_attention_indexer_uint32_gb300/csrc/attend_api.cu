@@ -1,5 +1,5 @@
-// attend_api.cu -- host side of the block-table, cache-append and attention
-// entry points of include/topkidx.h: argument checks before any launch.
+// attend_api.cu -- host side of the block-table, append, index-score and
+// attention entry points of include/topkidx.h: argument checks before any launch.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -155,6 +155,60 @@ topk_status_t topk_cache_append(const void* rows, int64_t row_stride, int32_t to
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "cache append launch");
 }
 
+topk_status_t topk_index_append(const void* rows, int64_t row_stride, int32_t tokens, const void* norm_weight_or_null,
+                                const void* norm_bias_or_null, float eps, const float* cos_sin_or_null,
+                                int32_t num_positions, const int32_t* positions_or_null, int32_t interleaved,
+                                int32_t rope_last, const int32_t* slots, void* cache, int64_t slot_stride,
+                                int32_t num_slots, topk_dtype_t dtype, topk_stream_t stream) {
+    if (tokens < 0 || num_slots < 1 || !cache || !dtype_ok(dtype)) return TOPK_EINVAL;
+    if (tokens > 0 && (!rows || !slots)) return TOPK_EINVAL;
+    if (!row_stride_ok(row_stride, kIndex) || !row_stride_ok(slot_stride, kIndex)) return TOPK_EINVAL;
+    if (norm_weight_or_null ? !(eps >= 0.f && std::isfinite(eps)) : norm_bias_or_null != nullptr) return TOPK_EINVAL;
+    if (cos_sin_or_null && (num_positions < 1 || (tokens > 0 && !positions_or_null))) return TOPK_EINVAL;
+    if (misaligned(rows, 16) || misaligned(cache, 16) || row_stride % 8 || slot_stride % 8 ||
+        misaligned(norm_weight_or_null, 16) || misaligned(norm_bias_or_null, 16) || misaligned(cos_sin_or_null, 16) ||
+        misaligned(positions_or_null, 4) || misaligned(slots, 4))
+        return TOPK_EALIGN;
+    AttendDevice device;
+    const topk_status_t st = attend_device(&device);
+    if (st != TOPK_OK || tokens == 0) return st;
+    IndexAppendParams p = {rows,          row_stride,        tokens, norm_weight_or_null, norm_bias_or_null, eps, cos_sin_or_null,
+                           num_positions, positions_or_null, interleaved != 0, rope_last != 0, slots, cache, slot_stride, num_slots};
+    const cudaError_t e = launch_index_append(p, dtype, device, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "index append launch");
+}
+
+topk_status_t topk_index_scores(const void* q, int64_t q_token_stride, int64_t q_head_stride, const float* weights,
+                                int64_t weights_stride, const void* cache, int64_t slot_stride, int32_t num_slots,
+                                const int32_t* seq_lens, const int32_t* page_table, int64_t page_table_stride,
+                                int32_t page_size, int32_t max_seq_len, const int32_t* cu_q_or_null, int32_t batch,
+                                int32_t total_q, int32_t heads, topk_dtype_t dtype, float* scores, int64_t scores_stride,
+                                topk_stream_t stream) {
+    if (batch < 1 || total_q < 0 || heads < 1 || heads > TOPK_INDEX_MAX_HEADS || !dtype_ok(dtype) || num_slots < 1) return TOPK_EINVAL;
+    if (!cache || !seq_lens || !page_table || !page_ok(page_size) || max_seq_len < 0) return TOPK_EINVAL;
+    if (total_q > 0 && (!q || !weights || !scores)) return TOPK_EINVAL;
+    if (!cu_q_or_null && total_q % batch != 0) return TOPK_EINVAL;
+    if ((static_cast<int64_t>(total_q) + batch) * ((static_cast<int64_t>(max_seq_len) + 127) / 128) > INT32_MAX) return TOPK_EINVAL;
+    if (page_table_stride < (static_cast<int64_t>(max_seq_len) + page_size - 1) / page_size || page_table_stride < 1)
+        return TOPK_EINVAL;
+    if (!token_stride_ok(q_token_stride, kIndex, total_q) || !token_stride_ok(q_head_stride, kIndex, heads) ||
+        !row_stride_ok(slot_stride, kIndex) || !row_stride_ok(weights_stride, total_q > 1 ? heads : 0) ||
+        !row_stride_ok(scores_stride, total_q > 1 ? max_seq_len : 0))
+        return TOPK_EINVAL;
+    if (misaligned(q, 16) || misaligned(cache, 16) || misaligned(weights, 4) || misaligned(seq_lens, 4) ||
+        misaligned(page_table, 4) || misaligned(cu_q_or_null, 4) || misaligned(scores, 4) || q_token_stride % 8 ||
+        q_head_stride % 8 || slot_stride % 8)
+        return TOPK_EALIGN;
+    AttendDevice device;
+    const topk_status_t st = attend_device(&device);
+    if (st != TOPK_OK || total_q == 0 || max_seq_len == 0) return st;
+    IndexScoresParams p = {q,           q_token_stride, q_head_stride, weights,       weights_stride,
+                           cache,       slot_stride,    num_slots,     seq_lens,      page_table,
+                           page_table_stride, log2_of(page_size), max_seq_len, cu_q_or_null, batch,
+                           total_q,     heads,          scores,        scores_stride, wait_limit()};
+    return launch_index_scores(p, dtype, device, reinterpret_cast<cudaStream_t>(stream));
+}
+
 size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads) {
     if (batch < 1 || queries < 1 || heads < 1) return 0;
     if (static_cast<int64_t>(queries) * heads > kMaxQueryHeads / batch) return 0;
@@ -163,10 +217,9 @@ size_t topk_attend_workspace_bytes(int32_t batch, int32_t queries, int32_t heads
 
 namespace {
 
-// What both cache attentions check: the query rows, the cache, the outputs.
-topk_status_t check_latent(const LatentParams& p, topk_dtype_t dtype, size_t workspace_bytes) {
+// What the cache attentions check: the query rows, the cache, the outputs.
+topk_status_t check_latent(const LatentParams& p, topk_dtype_t dtype, size_t need, size_t workspace_bytes) {
     if (!p.q || !p.cache || !p.out || !p.workspace || !dtype_ok(dtype)) return TOPK_EINVAL;
-    const size_t need = topk_attend_workspace_bytes(p.batch, p.queries, p.heads);
     if (need == 0 || p.num_slots < 1 || std::isnan(p.scale)) return TOPK_EINVAL;
     if (!row_stride_ok(p.slot_stride, kWidth)) return TOPK_EINVAL;
     if (!token_stride_ok(p.q_row_stride, kWidth, p.batch) || !token_stride_ok(p.q_query_stride, kWidth, p.queries) ||
@@ -214,7 +267,7 @@ topk_status_t topk_attend_selected(const void* q, int64_t q_row_stride, int64_t 
     p.out = out;
     p.lse = lse_or_null;
     p.workspace = workspace;
-    const topk_status_t st = check_latent(p, dtype, workspace_bytes);
+    const topk_status_t st = check_latent(p, dtype, topk_attend_workspace_bytes(p.batch, p.queries, p.heads), workspace_bytes);
     return st == TOPK_OK ? run_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
 }
 
@@ -247,8 +300,57 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
     p.out = out;
     p.lse = lse_or_null;
     p.workspace = workspace;
-    const topk_status_t st = check_latent(p, dtype, workspace_bytes);
+    const topk_status_t st = check_latent(p, dtype, topk_attend_workspace_bytes(p.batch, p.queries, p.heads), workspace_bytes);
     return st == TOPK_OK ? run_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
+}
+
+size_t topk_attend_shared_workspace_bytes(int32_t batch, int32_t queries, int32_t heads) {
+    if (topk_attend_workspace_bytes(batch, queries, heads) == 0) return 0;
+    return shared_workspace_bytes(batch, queries, heads);
+}
+
+topk_status_t topk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_query_stride, int64_t q_head_stride,
+                                 const void* cache, int64_t slot_stride, int32_t num_slots, const int32_t* seq_lens,
+                                 const int32_t* page_table, int64_t page_table_stride, const int32_t* shared_pages,
+                                 int32_t num_shared_pages, const int32_t* shared_len, int32_t page_size,
+                                 int32_t max_seq_len, int32_t batch, int32_t queries, int32_t heads, float scale,
+                                 topk_dtype_t dtype, void* out, float* lse_or_null, void* workspace,
+                                 size_t workspace_bytes, topk_stream_t stream) {
+    if (!seq_lens || !page_table || !shared_len || !page_ok(page_size) || max_seq_len < 0) return TOPK_EINVAL;
+    if (num_shared_pages < 0 || (num_shared_pages > 0 && !shared_pages)) return TOPK_EINVAL;
+    if (page_table_stride < (static_cast<int64_t>(max_seq_len) + page_size - 1) / page_size || page_table_stride < 1)
+        return TOPK_EINVAL;
+    if (misaligned(shared_pages, 4) || misaligned(shared_len, 4)) return TOPK_EALIGN;
+    const int64_t room = static_cast<int64_t>(num_shared_pages) * page_size;
+    LatentParams p = {};
+    p.q = q;
+    p.q_row_stride = q_row_stride;
+    p.q_query_stride = q_query_stride;
+    p.q_head_stride = q_head_stride;
+    p.cache = cache;
+    p.slot_stride = slot_stride;
+    p.num_slots = num_slots;
+    p.seq_lens = seq_lens;
+    p.table = page_table;
+    p.table_stride = page_table_stride;
+    p.log2_page = log2_of(page_size);
+    p.max_len = max_seq_len;
+    p.batch = batch;
+    p.queries = queries;
+    p.heads = heads;
+    p.scale = scale;
+    p.out = out;
+    p.lse = lse_or_null;
+    p.workspace = workspace;
+    p.shared_pages = shared_pages;
+    p.shared_len = shared_len;
+    p.max_shared = static_cast<int32_t>(room < max_seq_len ? room : max_seq_len);
+    topk_status_t st = check_latent(p, dtype, topk_attend_shared_workspace_bytes(batch, queries, heads), workspace_bytes);
+    if (st != TOPK_OK) return st;
+    AttendDevice device;
+    st = attend_device(&device);
+    p.wait = wait_limit();
+    return st == TOPK_OK ? launch_shared(p, dtype, device, reinterpret_cast<cudaStream_t>(stream)) : st;
 }
 
 topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,

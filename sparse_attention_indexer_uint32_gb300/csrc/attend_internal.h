@@ -1,5 +1,5 @@
-// attend_internal.h -- launch parameters of the block-table, cache-append and
-// attention kernels, shared by the host side of the ABI (attend_api.cu).
+// attend_internal.h -- launch parameters of the block-table, append, index-score
+// and attention kernels, shared by the host side of the ABI (attend_api.cu).
 #pragma once
 
 #include <atomic>
@@ -17,6 +17,7 @@ constexpr int kRope = TOPK_ROPE_DIM;
 constexpr int kWidth = kLatent + kRope;
 constexpr int kNope = TOPK_NOPE_DIM;
 constexpr int kValue = TOPK_VALUE_DIM;
+constexpr int kIndex = TOPK_INDEX_DIM;
 
 // The ABI's device check and CUDA-error record (topkidx_api.cu).
 topk_status_t api_check_device();
@@ -128,6 +129,45 @@ struct AppendParams {
 };
 cudaError_t launch_cache_append(const AppendParams& p, bool interleaved, topk_dtype_t dtype, cudaStream_t stream);
 
+struct IndexAppendParams {
+    const void* rows;
+    int64_t row_stride;
+    int32_t tokens;
+    const void* weight;  // or null
+    const void* bias;    // or null
+    float eps;
+    const float* cos_sin;  // or null
+    int32_t num_positions;
+    const int32_t* positions;
+    bool interleaved, rope_last;
+    const int32_t* slots;
+    void* cache;
+    int64_t slot_stride;
+    int32_t num_slots;
+};
+cudaError_t launch_index_append(const IndexAppendParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
+
+struct IndexScoresParams {
+    const void* q;
+    int64_t q_token_stride, q_head_stride;
+    const float* weights;
+    int64_t weights_stride;
+    const void* cache;
+    int64_t slot_stride;
+    int32_t num_slots;
+    const int32_t* seq_lens;
+    const int32_t* table;
+    int64_t table_stride;
+    int32_t log2_page;
+    int32_t max_len;
+    const int32_t* cu_q;  // null: total_q / batch queries each
+    int32_t batch, total_q, heads;
+    float* scores;
+    int64_t scores_stride;
+    WaitLimit wait;
+};
+topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
+
 // Absorbed latent attention: `batch` rows of queries x heads query heads over
 // up to max_len slots each, listed in `indices` or reached through `table`.
 struct LatentParams {
@@ -149,9 +189,15 @@ struct LatentParams {
     float* lse;  // or null
     void* workspace;
     WaitLimit wait;
+    // Positions that all rows share come through a page list of their own.
+    const int32_t* shared_pages;
+    const int32_t* shared_len;  // null: nothing is shared
+    int32_t max_shared;
 };
 size_t latent_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
 topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
+size_t shared_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
+topk_status_t launch_shared(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
 
 struct PromptParams {
     const void* q;

@@ -10,58 +10,19 @@
 // cosines under way: 65536 rows take 31.6 us, 5.3 TB/s or 79 % of the measured
 // copy rate (a warp for one row or two took 43 us, the weight's second reading
 // filled the L1 path); 64 rows 7.9 us a call, most of it the host's.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "attend_internal.h"
 #include "ptx.cuh"
+#include "two_byte.cuh"
 
 namespace topkidx {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kResident = 152 * 3;  // blocks that the GPU holds at once
-
-template <typename T>
-struct Pair;
-template <>
-struct Pair<__nv_bfloat16> {
-    using two = __nv_bfloat162;
-    static __device__ __forceinline__ float2 wide(two x) { return __bfloat1622float2(x); }
-    static __device__ __forceinline__ two narrow(float2 x) { return __float22bfloat162_rn(x); }
-};
-template <>
-struct Pair<__half> {
-    using two = __half2;
-    static __device__ __forceinline__ float2 wide(two x) { return __half22float2(x); }
-    static __device__ __forceinline__ two narrow(float2 x) { return __float22half2_rn(x); }
-};
-
-template <typename T>
-struct alignas(16) Eight {
-    typename Pair<T>::two v[4];
-};
-
-template <typename T>
-__device__ __forceinline__ void widen(const Eight<T>& x, float* f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 y = Pair<T>::wide(x.v[i]);
-        f[2 * i] = y.x;
-        f[2 * i + 1] = y.y;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ Eight<T> narrow(const float* f) {
-    Eight<T> x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.v[i] = Pair<T>::narrow(make_float2(f[2 * i], f[2 * i + 1]));
-    return x;
-}
 
 // One row on its way; a slot below 0 is not written.
 template <typename T, bool kInterleaved>
