@@ -1,72 +1,505 @@
 // index_scores.cu -- topk_index_scores: weighted scores of the indexer's heads
-// over its paged keys.
+// over its paged keys, on the tensor cores.
 //
 // Mathematics: I[i][t] = sum_h w[i][h] max(q[i][h].k[t], 0) over 128 values a
-// head.  Products of two-byte values are exact in fp32; all sums are fp32.
+// head.  Products of two-byte values are exact; all sums are fp32.  With D =
+// K Q^T, 128 keys by up to 256 (query, head) columns, each key is a lane of
+// tensor memory: the sum over a query's heads stays in one thread, and a warp
+// writes 32 neighbouring scores.  A key's 256 bytes are read once for up to 512
+// columns.  One query of 64 heads takes 16 K operations on 260 bytes and is
+// bound by memory, 16 of them together by the products.
+//
+// Work is cut in equal runs of tiles (128 keys by one chunk of a request's
+// queries), one block an SM: the host does not know the lengths.  Tiles are
+// independent, so nothing is joined.  A chunk's queries stay in shared memory
+// while its keys pass through a ring of three places, by tiled copies of a page
+// (or 128 rows of it) each; tensor memory holds two tiles of scores, one of
+// them read while the other is computed.
+//
+// Heads are padded to a multiple of 16 columns by the copy engine, with zeros.
+// A chunk holds a power of two of queries (up to 256 columns in each of one or
+// two products), so that the sum of a request's tiles under the causal limit
+// has a closed form.
+//
+// Warps: 0-3 and 4-7 sums of even and odd score tiles, 8 products, 9 keys, 10
+// queries and weights.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "attend_internal.h"
-#include "ptx.cuh"
-#include "two_byte.cuh"
+#include "tc.cuh"
+#include "tensor_map.h"
 
 namespace topkidx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 352;
+constexpr int kProductWarp = 8, kKeyWarp = 9, kQueryWarp = 10;
+constexpr int kTile = 128;
+constexpr int kStages = 3;
+constexpr int kMasks = 8;  // tiles whose masks are kept: kStages copied ahead, two scored, and room
+constexpr int kColumns = 256, kAllColumns = 2 * kColumns;  // of one product; of the queries in shared memory
+constexpr int kHalfKeys = kTile * 128;                     // 64 values of a tile's keys
+constexpr int kKeyBytes = 2 * kHalfKeys, kQueryBytes = 2 * kAllColumns * 128, kWeightBytes = kAllColumns * 4;
 
-// One query a block, one key a half warp at a time.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) index_scores_kernel(const IndexScoresParams p) {
+struct Shared {
+    uint64_t query_full[2], query_empty[2], weight_full[2];
+    uint64_t key_full[kStages], key_empty[kStages], mask_full[kMasks];
+    uint64_t score_full[2], score_empty[2], end;
+    int64_t total, begin;  // tiles of the whole call; the first of this block's run
+    int64_t scan[kThreads / 32];
+    uint32_t mask[kMasks][4];
+    int32_t row, chunk, tile;  // where the run begins
+    uint32_t tmem, gave_up;
+};
+// The structure lies before or behind the tiles, in what their alignment leaves.
+constexpr int kSlack = 1024;
+static_assert(sizeof(Shared) <= kSlack / 2, "barriers fit on one side");
+constexpr int kSmem = kQueryBytes + kStages * kKeyBytes + kWeightBytes + kSlack;
+static_assert(kSmem <= 232448, "shared memory of a block");
+
+struct ScoreMaps {
+    CUtensorMap q, cache;
+};
+// How the columns are laid out: per query, product, chunk.
+struct Layout {
+    int32_t padded;      // heads, a multiple of 16
+    int32_t log2_queries;  // of a chunk
+    int32_t product_queries;
+    int32_t places;      // chunks in shared memory: 2 of one product or 1 of two
+    int32_t box_rows;    // keys per copy
+    uint32_t instruction;  // without N
+};
+
+// A request's queries and what its tiles are.
+struct Request {
+    int from, n, length;
+
+    __device__ __forceinline__ Request(const IndexScoresParams& p, int b) {
+        length = min(max(p.seq_lens[b], 0), p.max_len);
+        if (p.cu_q) {
+            from = min(max(p.cu_q[b], 0), p.total_q);
+            n = max(min(max(p.cu_q[b + 1], 0), p.total_q) - from, 0);
+        } else {
+            n = p.total_q / p.batch;
+            from = b * n;
+        }
+    }
+    __device__ __forceinline__ int chunks(int log2) const { return (n + (1 << log2) - 1) >> log2; }
+    // Positions that the last query of a chunk sees.
+    __device__ __forceinline__ int seen(int chunk, int log2) const {
+        return max(length - n + min(n, (chunk + 1) << log2), 0);
+    }
+    __device__ __forceinline__ int tiles(int chunk, int log2) const {
+        return static_cast<int>((static_cast<uint32_t>(seen(chunk, log2)) + kTile - 1) / kTile);
+    }
+    // Tiles of the chunks before `chunk`: whole ones, each sees 2^log2 more
+    // than the one before, and 2^log2 divides a tile.
+    __device__ __forceinline__ int64_t before(int chunk, int log2) const {
+        const int step = 1 << log2;
+        int64_t at = static_cast<int64_t>(length) - n + step + kTile - 1;
+        int first = 0;
+        if (at < 0) {
+            first = static_cast<int>((-at + step - 1) >> log2);
+            at += static_cast<int64_t>(first) << log2;
+        }
+        if (chunk <= first) return 0;
+        const int per_tile = kTile >> log2;
+        const auto sum = [&](int64_t x) {  // of i / per_tile over i < x
+            const int64_t q = x / per_tile;
+            return per_tile * (q * (q - 1) / 2) + (x % per_tile) * q;
+        };
+        const int64_t a = at >> log2;
+        return sum(a + chunk - first) - sum(a);
+    }
+    __device__ __forceinline__ int64_t all(int log2) const {
+        const int c = chunks(log2);
+        return c > 0 ? before(c - 1, log2) + tiles(c - 1, log2) : 0;
+    }
+};
+
+// The run of one of n blocks: as even as can be.
+__device__ __forceinline__ int64_t run_start(int64_t total, int n, int i) {
+    return total / n * i + min(static_cast<int64_t>(i), total % n);
+}
+
+// All threads: the tiles of the call, and where this block's run begins.
+__device__ void locate(const IndexScoresParams& p, const Layout& a, Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int from = min(tid * per, p.batch), to = min(from + per, p.batch);
+    int64_t mine = 0;
+    for (int b = from; b < to; ++b) mine += Request(p, b).all(a.log2_queries);
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 31) sh.scan[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int64_t x = sh.scan[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    before += upto - mine;
+    const int64_t begin = run_start(total, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
+    if (tid == 0) {
+        sh.total = total;
+        sh.begin = begin;
+    }
+    if (begin >= before && begin < before + mine) {
+        int64_t at = begin - before;
+        int b = from;
+        while (true) {
+            const int64_t n = Request(p, b).all(a.log2_queries);
+            if (at < n) break;
+            at -= n;
+            ++b;
+        }
+        const Request r(p, b);
+        int lo = 0, hi = r.chunks(a.log2_queries) - 1;  // the last chunk with before <= at
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (r.before(mid, a.log2_queries) <= at)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        sh.row = b;
+        sh.chunk = lo;
+        sh.tile = static_cast<int>(at - r.before(lo, a.log2_queries));
+    }
+    __syncthreads();
+}
+
+// A run's pieces: tiles [first, last) of one chunk.
+struct Segment {
+    int row, query, queries, first, last;
+    int seen;  // positions that the chunk's first query sees (may be below 1)
+    int length;
+};
+struct Walk {
+    const IndexScoresParams& p;
+    int log2;
+    int64_t left;
+    int row, chunk, first;
+
+    __device__ __forceinline__ Walk(const IndexScoresParams& p, const Layout& a, const Shared& sh)
+        : p(p), log2(a.log2_queries), row(sh.row), chunk(sh.chunk), first(sh.tile) {
+        left = run_start(sh.total, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x) + 1) - sh.begin;
+    }
+    __device__ __forceinline__ bool next(Segment& s) {
+        while (left > 0 && row < p.batch) {
+            const Request r(p, row);
+            const int chunks = r.chunks(log2);
+            // Chunks that see nothing come before those that see something.
+            while (chunk < chunks) {
+                const int tiles = r.tiles(chunk, log2), at = chunk << log2;
+                ++chunk;
+                if (first >= tiles) {
+                    first = 0;
+                    continue;
+                }
+                s.row = row;
+                s.query = r.from + at;
+                s.queries = min(r.n - at, 1 << log2);
+                s.first = first;
+                s.last = static_cast<int>(min(static_cast<int64_t>(tiles), first + left));
+                s.seen = r.length - (r.n - 1 - at);
+                s.length = r.length;
+                left -= s.last - s.first;
+                first = 0;
+                return true;
+            }
+            chunk = 0;
+            ++row;
+        }
+        return false;
+    }
+};
+
+// kStep: columns of scores that a thread takes at a time (it divides a query's).
+template <int kStep>
+__global__ void __launch_bounds__(kThreads, 1)
+    index_scores_kernel(const IndexScoresParams p, const __grid_constant__ ScoreMaps maps, const Layout a, uint32_t* flags) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t start = ptx::smem_addr(raw), base = (start + kSlack - 1u) & ~(kSlack - 1u);
+    const uint32_t queries = base, keys = queries + kQueryBytes, weights = keys + kStages * kKeyBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(raw + (base - start >= sizeof(Shared) ? 0 : weights + kWeightBytes - start));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int place_columns = kAllColumns / a.places, place_bytes = kQueryBytes / a.places;
+
+    if (threadIdx.x == 0) {
+        sh.gave_up = p.wait.none;
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.query_full[i], 1);
+            ptx::mbar_init(&sh.query_empty[i], 9);  // the products, and each warp that reads the weights
+            ptx::mbar_init(&sh.weight_full[i], 1);
+            ptx::mbar_init(&sh.score_full[i], 1);
+            ptx::mbar_init(&sh.score_empty[i], 4);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(&sh.key_full[i], 1);
+            ptx::mbar_init(&sh.key_empty[i], 1);
+        }
+        for (int i = 0; i < kMasks; ++i) ptx::mbar_init(&sh.mask_full[i], 1);
+        ptx::mbar_init(&sh.end, 1);
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == kProductWarp) tc::alloc<1>(ptx::smem_addr(&sh.tmem), 2 * kColumns);
     ptx::grid_dependency_wait();
+    tc::fence_before();
+    locate(p, a, sh);
+    tc::fence_after();
     ptx::launch_dependents();
-    const int i = blockIdx.x;
-    int b = -1, last = 0;
-    if (p.cu_q) {
-        for (int r = 0; r < p.batch; ++r)
-            if (p.cu_q[r] <= i && i < p.cu_q[r + 1]) {
-                b = r;
-                last = min(p.cu_q[r + 1], p.total_q) - 1;
+    const uint32_t tmem = sh.tmem;
+    const tc::Waits wait{&sh.gave_up, p.wait.ns};
+    Walk walk(p, a, sh);
+    Segment s = {};
+
+    if (warp == kKeyWarp) {
+        int n = 0;
+        bool more = walk.next(s);
+        int tile = s.first;
+        int32_t page[4];  // of positions lane, lane + 32, .. of the next tile; -1 past the row's end
+        const int in_page = (1 << p.log2_page) - 1;
+        const auto fetch = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = static_cast<int64_t>(tile) * kTile + 32 * i + lane;
+                page[i] = more && t < s.length ? p.table[static_cast<int64_t>(s.row) * p.table_stride + (t >> p.log2_page)] : -1;
+            }
+        };
+        fetch();
+        while (more) {
+            int slot[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int offset = (tile * kTile + 32 * i + lane) & in_page;
+                const int64_t x = (static_cast<int64_t>(page[i]) << p.log2_page) + offset;
+                slot[i] = x >= 0 && x < p.num_slots ? static_cast<int>(x) : -1;
+            }
+            if (++tile == s.last) {
+                more = walk.next(s);
+                tile = s.first;
+            }
+            fetch();
+            const int stage = n % kStages;
+            if (n >= kStages && !wait.all(&sh.key_empty[stage], (n / kStages - 1) & 1)) break;
+            // The mask's place was last read for tile n - 8; the copies of tile
+            // n waited for the products of tile n - 3, and those for the sums
+            // two score tiles before.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = __ballot_sync(~0u, slot[i] >= 0);
+                if (lane == 0) sh.mask[n % kMasks][i] = bits;
+            }
+            if (lane == 0) {
+                ptx::mbar_arrive(&sh.mask_full[n % kMasks]);
+                ptx::mbar_arrive_expect_tx(&sh.key_full[stage], kKeyBytes);
+            }
+            __syncwarp();
+            // A slot outside the cache is copied as zeros.
+            for (int first = 0; first < kTile; first += 32 * a.box_rows) {
+                const int at = first + lane * a.box_rows;
+                int box = -1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = __shfl_sync(~0u, slot[i], at & 31);
+                    if ((at >> 5) == i) box = x;
+                }
+                if (box < 0) box = p.num_slots;
+                if (at < kTile) {
+                    tc::load_2d(keys + stage * kKeyBytes + at * 128, &maps.cache, 0, box, &sh.key_full[stage]);
+                    tc::load_2d(keys + stage * kKeyBytes + kHalfKeys + at * 128, &maps.cache, 64, box, &sh.key_full[stage]);
+                }
+            }
+            ++n;
+        }
+        for (int i = 0; i < kStages; ++i) {
+            const int copied = (n + kStages - 1 - i) / kStages;  // to this place
+            if (copied > 0) tc::Waits::drain(&sh.key_full[i], (copied - 1) & 1);
+        }
+    } else if (warp == kQueryWarp) {
+        for (int n = 0; walk.next(s); ++n) {
+            const int place = n % a.places, round = n / a.places;
+            if (round > 0 && (!wait.all(&sh.query_empty[place], (round - 1) & 1) || wait.over())) break;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.query_full[place], s.queries * a.padded * 256);
+            __syncwarp();
+            for (int i = lane; i < 2 * s.queries; i += 32)
+                tc::load_3d(queries + place * place_bytes + (i & 1) * (place_columns * 128) + (i >> 1) * (a.padded * 128), &maps.q,
+                            64 * (i & 1), 0, s.query + (i >> 1), &sh.query_full[place]);
+            const uint32_t to = weights + place * (place_columns * 4);
+            for (int i = lane; i < s.queries * a.padded; i += 32) {
+                const int h = i % a.padded;
+                const float w = h < p.heads ? p.weights[(s.query + i / a.padded) * p.weights_stride + h] : 0.f;
+                ptx::sts_u32(to + 4 * i, __float_as_uint(w));
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.weight_full[place]);
+            if (!wait.all(&sh.query_full[place], round & 1)) {
+                tc::Waits::drain(&sh.query_full[place], round & 1);
                 break;
             }
+        }
+    } else if (warp == kProductWarp) {
+        const uint64_t key_at = tc::operand(keys), query_at = tc::operand(queries);
+        int n = 0, u = 0;
+        // Given up, nothing is issued or announced any more.
+        bool on = true;
+        for (int segment = 0; walk.next(s); ++segment) {
+            const int place = segment % a.places;
+            on = wait.all(&sh.query_full[place], (segment / a.places) & 1) && on;
+            for (int tile = s.first; tile < s.last; ++tile, ++n) {
+                const int stage = n % kStages;
+                on = wait.all(&sh.key_full[stage], (n / kStages) & 1) && on;
+                for (int first = 0; first < s.queries; first += a.product_queries, ++u) {
+                    if (u > 1) on = wait.all(&sh.score_empty[u & 1], ((u >> 1) - 1) & 1) && on;
+                    tc::fence_after();
+                    if (on && tc::elect()) {
+                        const int columns = min(s.queries - first, a.product_queries) * a.padded;
+                        const uint32_t instr = a.instruction | (static_cast<uint32_t>(columns >> 3) << 17);
+                        const uint64_t k_at = key_at + stage * (kKeyBytes >> 4);
+                        const uint64_t q_at = query_at + ((place * place_bytes + first * a.padded * 128) >> 4);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma<1>(tmem + kColumns * (u & 1), k_at + (k >> 2) * (kHalfKeys >> 4) + 2 * (k & 3),
+                                       q_at + (k >> 2) * (place_columns * 8) + 2 * (k & 3), instr, k > 0);
+                        tc::commit<1>(&sh.score_full[u & 1]);
+                        if (first + a.product_queries >= s.queries) {
+                            tc::commit<1>(&sh.key_empty[stage]);
+                            if (tile == s.last - 1) tc::commit<1>(&sh.query_empty[place]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (tc::elect()) {
+            tc::commit<1>(&sh.end);
+            tc::Waits::drain(&sh.end, 0);
+        }
     } else {
-        const int n = p.total_q / p.batch;
-        b = i / n;
-        last = b * n + n - 1;
-    }
-    if (b < 0) return;
-    const int limit = min(max(p.seq_lens[b], 0), p.max_len) - (last - i);
-    const int j = threadIdx.x & 15;
-    const T* q = static_cast<const T*>(p.q) + i * p.q_token_stride;
-    for (int t0 = static_cast<int>(blockIdx.y) * (kThreads / 16); t0 < limit; t0 += static_cast<int>(gridDim.y) * (kThreads / 16)) {
-        const int t = t0 + threadIdx.x / 16;
-        float k[8] = {}, total = 0.f;
-        bool seen = false;
-        if (t < limit) {
-            const int64_t slot = (static_cast<int64_t>(p.table[b * p.table_stride + (t >> p.log2_page)]) << p.log2_page) + (t & ((1 << p.log2_page) - 1));
-            seen = slot >= 0 && slot < p.num_slots;
-            if (seen) widen(reinterpret_cast<const Eight<T>*>(static_cast<const T*>(p.cache) + slot * p.slot_stride)[j], k);
-        }
-        for (int h = 0; h < p.heads; ++h) {
-            float x[8], dot = 0.f;
-            widen(reinterpret_cast<const Eight<T>*>(q + h * p.q_head_stride)[j], x);
+        const int group = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColumns * group;
+        const int steps = a.padded / kStep;  // of a query
+        const int rest = p.heads - (steps - 1) * kStep;  // heads of the last of them
+        int n = 0, u = 0;
+        // These warps go through all tiles, also after a wait has given up.
+        for (int segment = 0; walk.next(s); ++segment) {
+            const int place = segment % a.places;
+            const uint32_t weights_at = weights + place * (place_columns * 4);
+            wait.warp(&sh.weight_full[place], (segment / a.places) & 1);
+            for (int tile = s.first; tile < s.last; ++tile, ++n) {
+                for (int first = 0; first < s.queries; first += a.product_queries, ++u) {
+                    if ((u & 1) != group) continue;
+                    wait.warp(&sh.mask_full[n % kMasks], (n / kMasks) & 1);
+                    wait.warp(&sh.score_full[group], (u >> 1) & 1);
+                    tc::fence_after();
+                    const bool there = (sh.mask[n % kMasks][r >> 5] >> (r & 31)) & 1;
+                    const int t = tile * kTile + r, count = min(s.queries - first, a.product_queries);
+                    float* out = p.scores + (s.query + first) * p.scores_stride + t;
+                    int seen = s.seen + first;  // positions that the query sees
+                    uint32_t x[kStep];
+                    const auto load = [&](uint32_t column, uint32_t* to) {
+                        if constexpr (kStep == 32)
+                            tc::load32(lanes + column, to);
+                        else
+                            tc::load16(lanes + column, to);
+                    };
+                    load(0, x);
+                    uint32_t at = 0;  // column of what is loaded
+                    for (int q = 0; q < count; ++q, ++seen, out += p.scores_stride) {
+                        float2 sum[2] = {};
+                        for (int step = 0; step < steps; ++step) {
+                            float f[kStep];
+                            tc::wait_load();
+                            // (not read before, nor overwritten by the next)
 #pragma unroll
-            for (int v = 0; v < 8; ++v) dot += x[v] * k[v];
+                            for (int i = 0; i < kStep; ++i) {
+                                asm volatile("" : "+r"(x[i]));
+                                f[i] = __uint_as_float(x[i]);
+                            }
+                            const uint32_t w_at = weights_at + 4 * (first * a.padded + at);
+                            at += kStep;
+                            if (at < static_cast<uint32_t>(count * a.padded)) load(at, x);
+                            // Columns behind the last head are zeros, but a key may hold infinities.
+                            if (step == steps - 1 && rest < kStep) {
 #pragma unroll
-            for (int d = 8; d; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
-            total += p.weights[i * p.weights_stride + h] * ptx::fmax_nan(dot, 0.f);
+                                for (int i = 0; i < kStep; ++i)
+                                    if (i >= rest) f[i] = 0.f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < kStep; i += 4) {
+                                const float4 w = ptx::lds_f4(w_at + 4 * i);
+                                sum[0] = tc::fma2(make_float2(ptx::fmax_nan(f[i], 0.f), ptx::fmax_nan(f[i + 1], 0.f)),
+                                                  make_float2(w.x, w.y), sum[0]);
+                                sum[1] = tc::fma2(make_float2(ptx::fmax_nan(f[i + 2], 0.f), ptx::fmax_nan(f[i + 3], 0.f)),
+                                                  make_float2(w.z, w.w), sum[1]);
+                            }
+                        }
+                        if (t < seen) *out = there ? (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) : -INFINITY;
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sh.score_empty[group]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.query_empty[place]);
         }
-        if (t < limit && j == 0) p.scores[i * p.scores_stride + t] = seen ? total : -INFINITY;
     }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kProductWarp) {
+        tc::fence_after();
+        tc::dealloc<1>(tmem, 2 * kColumns);
+    }
+    if (threadIdx.x == 0 && sh.gave_up) atomicOr(flags, TOPK_FLAG_TIMEOUT);
 }
 
 }  // namespace
 
-topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype, const AttendDevice&, cudaStream_t stream) {
-    const auto kernel = dtype == TOPK_BF16 ? index_scores_kernel<__nv_bfloat16> : index_scores_kernel<__half>;
-    const cudaError_t e = launch_early(kernel, dim3(p.total_q, 32), kThreads, 0, stream, p);
+topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream) {
+    const bool bf16 = dtype == TOPK_BF16;
+    Layout a = {};
+    a.padded = (p.heads + 15) / 16 * 16;
+    int log2 = 0;  // queries of a product
+    while ((2 << log2) * a.padded <= kColumns) ++log2;
+    a.product_queries = 1 << log2;
+    // Requests of up to one product's queries: the next chunk's come while
+    // this one's are used; else each key is read for two products.
+    a.places = p.total_q <= static_cast<int64_t>(p.batch) * a.product_queries ? 2 : 1;
+    a.log2_queries = a.places == 2 ? log2 : log2 + 1;
+    a.box_rows = p.log2_page < 7 ? 1 << p.log2_page : kTile;
+    a.instruction = tc::instruction(bf16, kTile, 0, false, false);
+
+    ScoreMaps maps;
+    const int64_t any = 2 * kIndex;  // stride of a dimension of one entry
+    const int64_t q_dims[3] = {kIndex, p.heads, p.total_q};
+    const int64_t q_steps[2] = {p.heads > 1 ? 2 * p.q_head_stride : any, p.total_q > 1 ? 2 * p.q_token_stride : any};
+    CUresult r = encode_map(&maps.q, bf16, p.q, 3, q_dims, q_steps, 1, a.padded);
+    const int64_t c_dims[2] = {kIndex, p.num_slots}, c_steps[1] = {2 * p.slot_stride};
+    if (r == CUDA_SUCCESS) r = encode_map(&maps.cache, bf16, p.cache, 2, c_dims, c_steps, 1, a.box_rows);
+    if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "index scores tensor map");
+
+    const bool wide = a.padded % 32 == 0;
+    const auto kernel = wide ? index_scores_kernel<32> : index_scores_kernel<16>;
+    static std::atomic<bool> prepared[2][AttendDevice::kMax];
+    cudaError_t e = allow_shared(kernel, kSmem, prepared[wide][device.index]);
+    if (e != cudaSuccess) return api_cuda_fail(e, "index scores shared memory");
+    const int64_t chunks = ((static_cast<int64_t>(p.total_q) + (1 << a.log2_queries) - 1) >> a.log2_queries) + p.batch;
+    const int64_t tiles = chunks * ((p.max_len + int64_t{kTile} - 1) / kTile);
+    const unsigned blocks = static_cast<unsigned>(tiles < device.sms ? tiles : device.sms);
+    e = launch_early(kernel, dim3(blocks), kThreads, kSmem, stream, p, maps, a, device.flags);
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "index scores launch");
 }
 
