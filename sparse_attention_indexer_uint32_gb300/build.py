@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libtopkidx.so")
 SOURCES = ["topk_kernels.cu", "topk_stream.cu", "topk_warp.cu", "topk_split.cu", "topkidx_api.cu", "topk_noalloc.cu",
            "serve_tables.cu", "serve_append.cu", "index_append.cu", "index_scores.cu",
-           "attend_latent.cu", "attend_shared.cu", "attend_prompt.cu", "attend_api.cu"]
+           "attend_latent.cu", "attend_prompt.cu", "attend_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

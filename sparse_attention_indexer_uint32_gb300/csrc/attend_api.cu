@@ -345,12 +345,8 @@ topk_status_t topk_attend_shared(const void* q, int64_t q_row_stride, int64_t q_
     p.shared_pages = shared_pages;
     p.shared_len = shared_len;
     p.max_shared = static_cast<int32_t>(room < max_seq_len ? room : max_seq_len);
-    topk_status_t st = check_latent(p, dtype, topk_attend_shared_workspace_bytes(batch, queries, heads), workspace_bytes);
-    if (st != TOPK_OK) return st;
-    AttendDevice device;
-    st = attend_device(&device);
-    p.wait = wait_limit();
-    return st == TOPK_OK ? launch_shared(p, dtype, device, reinterpret_cast<cudaStream_t>(stream)) : st;
+    const topk_status_t st = check_latent(p, dtype, topk_attend_shared_workspace_bytes(batch, queries, heads), workspace_bytes);
+    return st == TOPK_OK ? run_latent(p, dtype, reinterpret_cast<cudaStream_t>(stream)) : st;
 }
 
 topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,

@@ -197,7 +197,6 @@ struct LatentParams {
 size_t latent_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
 topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
 size_t shared_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);
-topk_status_t launch_shared(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
 
 struct PromptParams {
     const void* q;

@@ -1,5 +1,6 @@
 // attend_latent.cu -- absorbed latent attention over the paged cache, over
-// selected slots or whole rows, on the tensor cores.
+// selected slots or whole rows, or behind a prompt that requests share, on the
+// tensor cores.
 //
 // Mathematics: as in attend_prompt.cu, with one latent row c_j for every head:
 // s_hj = q_h.c_j over 576 values, o_h = sum_j p_hj c_j over the first 512.  So a
@@ -95,6 +96,7 @@ struct Shared {
     int32_t total;            // tiles of the whole batch
     int32_t begin;            // first tile of this pair's run
     int32_t row, tile, length;  // where that lies: row of the batch, tile in the row, the row's length
+    int32_t common;           // positions that all rows share
     int32_t scan[kThreads / 32];
 };
 constexpr int kSmem = kQueryBytes + kKeyBytes + kValueBytes + kWeightBytes + 1024 + 2048;
@@ -103,6 +105,7 @@ static_assert(kSmem <= 232448, "shared memory of a block");
 
 struct LatentMaps {
     CUtensorMap q, cache;
+    CUtensorMap all_q;  // shared positions: the rows of all requests
 };
 
 __device__ __forceinline__ int length_of(const LatentParams& p, int b) {
@@ -114,13 +117,40 @@ __device__ __forceinline__ int tiles_of(int length) {
 }
 __device__ __forceinline__ int groups_of(const LatentParams& p) { return (p.queries * p.heads + kRows - 1) / kRows; }
 
+// Shared positions (kShared): row 0 of the walk is that prompt, with the
+// (request, query, head) rows of all requests; row 1 + b what request b has of
+// its own, from the tile in which the prompt ends on.  A row without positions
+// has no tiles.
+struct Row {
+    int all;     // (query, head) rows
+    int base;    // position of the first tile
+    int from;    // first position that is seen
+    int length;  // past the last one
+    __device__ __forceinline__ Row(const LatentParams& p, int row, int common) {
+        all = p.queries * p.heads;
+        if (row == 0) {
+            all *= p.batch;
+            base = from = 0;
+            length = common;
+        } else {
+            base = common & ~(kTile - 1);
+            from = common;
+            length = length_of(p, row - 1);
+        }
+    }
+    __device__ __forceinline__ int tiles() const {
+        return length <= from ? 0 : static_cast<int>((static_cast<uint32_t>(length - base) + kTile - 1) / kTile);
+    }
+    __device__ __forceinline__ int groups() const { return (all + kRows - 1) / kRows; }
+};
+
 // The runs of n pairs over all tiles (both below 2^31), as even as can be: the
 // first `more` pairs have one tile more than the others.  With fewer tiles than
 // pairs the last pairs, past `used`, have none.
 struct Runs {
     int each, more, used;
     __device__ __forceinline__ Runs(int total, int n) {
-        used = min(n, total);
+        used = max(min(n, total), 1);  // (with shared positions there may be no tiles at all)
         each = total / used;
         more = total % used;
     }
@@ -192,22 +222,105 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, Shared& sh) {
     __syncthreads();
 }
 
+// The same with shared positions.
+__device__ void locate_shared(const LatentParams& p, int pair, int pairs, Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int common = min(max(*p.shared_len, 0), p.max_shared);
+    const int per = (p.batch + kThreads) / kThreads;  // of the batch's rows and row 0
+    const int from = min(tid * per, p.batch + 1), to = min(from + per, p.batch + 1);
+    int mine = 0;
+#pragma unroll 4
+    for (int i = from; i < to; ++i) {
+        const Row row(p, i, common);
+        mine += row.tiles() * row.groups();
+    }
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 31) sh.scan[warp] = upto;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int x = sh.scan[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    before += upto - mine;
+    const int begin = Runs(total, pairs).start(pair);
+    if (tid == 0) {
+        sh.total = total;
+        sh.begin = begin;
+        sh.common = common;
+    }
+    if (begin >= before && begin < before + mine) {
+        int at = before, i = from;
+        while (true) {
+            const Row row(p, i, common);
+            const int n = row.tiles() * row.groups();
+            if (begin < at + n) break;
+            at += n;
+            ++i;
+        }
+        sh.row = i;
+        sh.tile = begin - at;
+    }
+    __syncthreads();
+}
+
 // A run's pieces: tiles [first, last) of one group of 128 rows.
 struct Segment {
     int row, group, first, last, tiles, length;
+    int all, base, from;  // of a Row
 };
+template <bool kShared>
 struct Walk {
     const LatentParams& p;
     int left, row, group, first, groups, length;
+    int common, at;  // shared positions; the next tile among all
 
     __device__ __forceinline__ Walk(const LatentParams& p, const Shared& sh, int pair, int pairs)
         : p(p), left(Runs(sh.total, pairs).count(pair)), row(sh.row), groups(groups_of(p)), length(sh.length) {
-        const int tiles = tiles_of(length);
-        group = sh.tile / tiles;
-        first = sh.tile - group * tiles;
+        if constexpr (kShared) {
+            common = sh.common;
+            at = sh.begin;
+            if (left <= 0) return;
+            const int tiles = Row(p, row, common).tiles();
+            group = sh.tile / tiles;
+            first = sh.tile - group * tiles;
+        } else {
+            const int tiles = tiles_of(length);
+            group = sh.tile / tiles;
+            first = sh.tile - group * tiles;
+        }
     }
     __device__ __forceinline__ bool next(Segment& s) {
         if (left <= 0) return false;
+        if constexpr (kShared) {
+            Row r(p, row, common);
+            while (r.tiles() == 0 && row < p.batch) r = Row(p, ++row, common);
+            if (r.tiles() == 0) return false;
+            s.row = row;
+            s.group = group;
+            s.length = r.length;
+            s.all = r.all;
+            s.base = r.base;
+            s.from = r.from;
+            s.tiles = r.tiles();
+            s.first = first;
+            s.last = min(s.tiles, first + left);
+            left -= s.last - s.first;
+            at += s.last - s.first;
+            first = 0;
+            if (++group == r.groups()) {
+                group = 0;
+                ++row;
+            }
+            return true;
+        }
         s.row = row;
         s.group = group;
         s.length = length;
@@ -232,15 +345,26 @@ template <bool kPaged>
 struct Slot {
     int32_t value, offset;
 
-    __device__ __forceinline__ void fetch(const LatentParams& p, int row, int length, int64_t at) {
+    // `more`: whether there is such a piece.  Of shared positions those from
+    // `until` on are looked up.
+    template <bool kShared>
+    __device__ __forceinline__ void fetch(const LatentParams& p, const Segment& s, bool more, int64_t at, int until) {
         value = -1;
         offset = 0;
-        if (at >= length) return;
+        if (at >= (more ? s.length : 0)) return;
+        if constexpr (kShared) {
+            if (at < until) return;
+            const int pos = static_cast<int>(at);
+            value = s.row == 0 ? p.shared_pages[pos >> p.log2_page]
+                               : p.table[static_cast<int64_t>(s.row - 1) * p.table_stride + (pos >> p.log2_page)];
+            offset = pos & ((1 << p.log2_page) - 1);
+            return;
+        }
         if (!kPaged && p.indices) {
-            value = p.indices[static_cast<int64_t>(row) * p.indices_stride + at];
+            value = p.indices[static_cast<int64_t>(s.row) * p.indices_stride + at];
         } else {
             const int pos = static_cast<int>(at);
-            value = p.table[static_cast<int64_t>(row) * p.table_stride + (pos >> p.log2_page)];
+            value = p.table[static_cast<int64_t>(s.row) * p.table_stride + (pos >> p.log2_page)];
             offset = pos & ((1 << p.log2_page) - 1);
         }
     }
@@ -252,24 +376,31 @@ struct Slot {
     }
 };
 
+// Position `at` of a tile.
+template <bool kShared>
+__device__ __forceinline__ int64_t position(const Segment& s, int tile, int at) {
+    return (kShared ? s.base : 0) + static_cast<int64_t>(tile) * kTile + at;
+}
+
 // One slot a tile of a run, fetched two tiles ahead of its use: loads wait
 // behind the copies that are under way.
+template <bool kShared>
 struct SlotAhead {
     const LatentParams& p;
-    Walk& walk;
+    Walk<kShared>& walk;
     Segment& s;
     int at, tiles, tile;
     Slot<false> slot[2];
     bool more;
 
-    __device__ __forceinline__ SlotAhead(const LatentParams& p, Walk& walk, Segment& s, int at)
+    __device__ __forceinline__ SlotAhead(const LatentParams& p, Walk<kShared>& walk, Segment& s, int at)
         : p(p), walk(walk), s(s), at(at), tiles(walk.left), more(walk.next(s)) {
         tile = s.first;
         fetch(slot[0]);
         fetch(slot[1]);
     }
     __device__ __forceinline__ void fetch(Slot<false>& x) {
-        x.fetch(p, s.row, more ? s.length : 0, static_cast<int64_t>(tile) * kTile + at);
+        x.template fetch<kShared>(p, s, more, position<kShared>(s, tile, at), s.from);
         if (more && ++tile == s.last) {
             more = walk.next(s);
             tile = s.first;
@@ -307,10 +438,41 @@ __device__ __forceinline__ float* part_of(const LatentParams& p, int rows, int p
            static_cast<int64_t>(place) * rows * (kLatent + 2);
 }
 
-template <bool kBf16, bool kPaged>
+// Workspace of a call with shared positions: for each group of rows (those of
+// the prompt first, then by request) the pair whose run begins it and how many
+// runs it is in; then a place for two partial sums of each run, as above, with
+// as many rows as any group has; then one for each group, for those that are
+// in one run only.
+__host__ __device__ __forceinline__ int64_t groups_in(int64_t rows) { return (rows + kRows - 1) / kRows; }
+__host__ __device__ __forceinline__ int64_t place_floats(int64_t rows) {
+    return static_cast<int64_t>(part_rows_of(rows)) * (kLatent + 2);
+}
+__host__ __device__ __forceinline__ int64_t all_groups(int64_t batch, int64_t each) {
+    return groups_in(batch * each) + batch * groups_in(each);
+}
+__device__ __forceinline__ int64_t group_at(const LatentParams& p, int row, int group) {
+    const int64_t each = p.queries * p.heads;
+    return row == 0 ? group : groups_in(p.batch * each) + (row - 1) * groups_in(each) + group;
+}
+__device__ __forceinline__ int2& parts_of(const LatentParams& p, int row, int group) {
+    return static_cast<int2*>(p.workspace)[group_at(p, row, group)];
+}
+__device__ __forceinline__ float* run_of(const LatentParams& p, int place) {
+    const int64_t each = p.queries * p.heads, parts = (all_groups(p.batch, each) + 1) / 2 * 2;
+    return reinterpret_cast<float*>(static_cast<int2*>(p.workspace) + parts) + place * place_floats(p.batch * each);
+}
+__device__ __forceinline__ float* whole_of(const LatentParams& p, int row, int group) {
+    const int64_t each = p.queries * p.heads;
+    float* at = run_of(p, 2 * kMaxPairs);
+    if (row == 0) return at + group * place_floats(p.batch * each);
+    at += groups_in(p.batch * each) * place_floats(p.batch * each);
+    return at + ((row - 1) * groups_in(each) + group) * place_floats(each);
+}
+
+template <bool kBf16, bool kPaged, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_kernel(const LatentParams p, const __grid_constant__ LatentMaps maps, uint32_t* flags, float scale_log2,
-                  bool negate, bool whole_rows, int box_rows) {
+                  bool negate, bool whole_rows, bool all_rows, int box_rows) {
     extern __shared__ uint8_t raw[];
     const uint32_t base = (ptx::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t queries = base, keys = queries + kQueryBytes, values = keys + kKeyBytes,
@@ -321,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
     // Up to 64 rows: 32 a block, two places for queries, and half of the
     // softmax warps.
-    const bool few = p.queries * p.heads <= kHalfRows;
+    const bool few = p.queries * p.heads * (kShared ? p.batch : 1) <= kHalfRows;
     const int block_rows = few ? kHalfRows / 2 : kHalfRows, query_piece = block_rows * 128;
 
     if (threadIdx.x == 0) {
@@ -349,7 +511,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 4) tc::alloc<2>(ptx::smem_addr(&sh.tmem), kColumns);
     ptx::grid_dependency_wait();
-    locate(p, pair, pairs, sh);
+    if constexpr (kShared)
+        locate_shared(p, pair, pairs, sh);
+    else
+        locate(p, pair, pairs, sh);
     // Both blocks' barriers and tensor memory are ready from the wait on; the
     // first slots are fetched before it.
     tc::fence_before();
@@ -362,14 +527,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     const uint32_t tmem = sh.tmem;
     const tc::Waits wait{&sh.gave_up, p.wait.ns};
-    Walk walk(p, sh, pair, pairs);
+    Walk<kShared> walk(p, sh, pair, pairs);
     Segment s = {};
 
     if (!kPaged && (warp == 5 || warp == 8)) {
         // Selected slots, first product: 32 of the block's 64 slots of each
         // tile, all values; 16 bytes a lane, four rows at a time.
         const int part = warp == 8 ? 1 : 0, r = lane >> 3;
-        SlotAhead ahead(p, walk, s, rank * kHalf + 32 * part + lane);
+        SlotAhead<kShared> ahead(p, walk, s, rank * kHalf + 32 * part + lane);
         const int tiles = ahead.tiles;
         pair_ready();
         for (int n = 0; n < tiles && !wait.over(); ++n) {
@@ -401,9 +566,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Selected slots, second product: 32 of each half of the tile's
         // slots, values 256 rank...
         const int part = warp == 9 ? 1 : 0, r = lane >> 3;
-        Walk walk2 = walk;
+        Walk<kShared> walk2 = walk;
         Segment s2 = {};
-        SlotAhead ahead[kValueGroups] = {SlotAhead(p, walk, s, 32 * part + lane), SlotAhead(p, walk2, s2, kHalf + 32 * part + lane)};
+        SlotAhead<kShared> ahead[kValueGroups] = {SlotAhead<kShared>(p, walk, s, 32 * part + lane),
+                                                  SlotAhead<kShared>(p, walk2, s2, kHalf + 32 * part + lane)};
         const int tiles = ahead[0].tiles;
         pair_ready();
         for (int n = 0; n < tiles && !wait.over(); ++n) {
@@ -443,7 +609,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool mine = lane * box_rows < kHalf;
         Slot<true> next;  // at which box `lane` of the next tile begins
         const auto fetch = [&]() {
-            next.fetch(p, s.row, more && mine ? s.length : 0, static_cast<int64_t>(tile) * kTile + rank * kHalf + lane * box_rows);
+            // A box that holds the first position that is seen may begin before it.
+            next.template fetch<kShared>(p, s, more && mine, position<kShared>(s, tile, rank * kHalf + lane * box_rows),
+                                         s.from - box_rows + 1);
         };
         const auto row_of = [&]() {  // outside the cache: copied as zeros
             const int x = next.get(p);
@@ -491,13 +659,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const auto fetch = [&]() {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                next[i].fetch(p, s.row, more ? s.length : 0, static_cast<int64_t>(tile) * kTile + 32 * i + lane);
+                next[i].template fetch<kShared>(p, s, more, position<kShared>(s, tile, 32 * i + lane),
+                                                s.from - box_rows + 1);
         };
         fetch();
         pair_ready();
         int stopped = kValueGroups;
         while (more && stopped == kValueGroups) {
             const int slots[4] = {next[0].get(p), next[1].get(p), next[2].get(p), next[3].get(p)};
+            const int hidden = kShared ? s.from - static_cast<int>(position<kShared>(s, tile, 0)) : 0;  // of the tile
             if (++tile == s.last) {
                 more = walk.next(s);
                 tile = s.first;
@@ -505,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fetch();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // as for selected slots
-                const uint32_t bits = __ballot_sync(~0u, slots[i] >= 0);
+                const uint32_t bits = __ballot_sync(~0u, slots[i] >= 0 && (!kShared || 32 * i + lane >= hidden));
                 if (lane == 0) sh.mask[n & 3][i] = bits;
             }
             if (lane == 0) ptx::mbar_arrive(&sh.mask_full[n & 3]);
@@ -538,7 +708,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (copied > 0) tc::Waits::drain(&sh.value_landed[g], (copied - 1) & 1);
         }
     } else if (warp == kQueryWarp) {
-        if (lane == 0 && rank == 0 && pair > 0) {
+        if (kShared && lane == 0 && rank == 0) {
+            // All of them at once: the join goes by them whatever becomes of the sums.
+            Walk<kShared> ahead = walk;
+            while (ahead.next(s))
+                if (s.first == 0)  // (`at` is past this piece)
+                    parts_of(p, s.row, s.group) =
+                        make_int2(pair, Runs(sh.total, pairs).of(ahead.at - s.last + s.tiles - 1) - pair + 1);
+        }
+        if (!kShared && lane == 0 && rank == 0 && pair > 0) {
             const Runs runs(sh.total, pairs);
             const int tiles = tiles_of(walk.length), all = p.queries * p.heads;
             const int start = sh.begin - walk.first;  // of the group's tiles
@@ -562,7 +740,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ptx::mbar_arrive_expect_tx(landed, kPieces * query_piece);
                 const int m = s.group * kRows + rank * block_rows;
                 for (int c = 0; c < kPieces; ++c) {
-                    if (whole_rows) {
+                    if (kShared && s.row == 0) {
+                        const int each = p.queries * p.heads;
+                        if (all_rows) {
+                            tc::load_4d(to + c * query_piece, &maps.all_q, 64 * c, m, 0, 0, landed);
+                        } else {
+                            for (int i = 0; i < block_rows; ++i)
+                                tc::load_4d(to + c * query_piece + i * 128, &maps.all_q, 64 * c, (m + i) % p.heads,
+                                            (m + i) % each / p.heads, (m + i) / each, landed);
+                        }
+                    } else if (kShared && whole_rows) {
+                        tc::load_4d(to + c * query_piece, &maps.q, 64 * c, m, 0, s.row - 1, landed);
+                    } else if (kShared) {
+                        for (int i = 0; i < block_rows; ++i)
+                            tc::load_4d(to + c * query_piece + i * 128, &maps.q, 64 * c, (m + i) % p.heads,
+                                        (m + i) / p.heads, s.row - 1, landed);
+                    } else if (whole_rows) {
                         tc::load_4d(to + c * query_piece, &maps.q, 64 * c, m, 0, s.row, landed);
                     } else {
                         for (int i = 0; i < block_rows; ++i)
@@ -591,7 +784,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 Slot<false> slots[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    slots[i].fetch(p, s.row, s.length, static_cast<int64_t>(tile) * kTile + at + 32 * i);
+                    slots[i].template fetch<kShared>(p, s, true, position<kShared>(s, tile, at + 32 * i), s.from);
                 // Once the copies of the tile before are under way; a tile
                 // whose own copies are needs no more help.
                 while (!over && __any_sync(~0u, sh.copied < n)) over = wait.idle(spins, since);
@@ -630,7 +823,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 spins = 0;
             } else if (values_done < tiles && ready(&sh.value_landed[vg], values_done)) {
-                const int left = s.length - tile * kTile - vg * kHalf;
+                const int left = s.length - static_cast<int>(position<kShared>(s, tile, vg * kHalf));
+                // Nor may those before the first that is seen.
+                const int hidden = kShared ? min(s.from - s.length + left, kHalf) : 0;
+                if (kPaged && kShared && hidden > 0) {
+                    for (int i = lane; i < hidden * 32; i += 32)
+                        ptx::sts_u4(values + ((i >> 3) & 3) * kValuePiece + (vg * kHalf + (i >> 5)) * 128 + (i & 7) * 16,
+                                    make_uint4(0, 0, 0, 0));
+                }
                 if (kPaged && left < kHalf) {
                     // Rows past the sequence's end may hold anything, and a
                     // weight of zero would not hide a NaN.
@@ -733,7 +933,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (!summed) sums(n - 1);
                     add = tile > s.first;
-                    left = s.length - tile * kTile;
+                    left = s.length - static_cast<int>(position<kShared>(s, tile, 0));
                 }
             }
             if (tiles > 0) sums(n - 1);
@@ -747,7 +947,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
         const uint32_t weight_full = ptx::map_rank(ptx::smem_addr(&sh.weight), 0);
         const uint32_t weight_row = weights + half * kWeightPiece + r * 128;
-        const int all = p.queries * p.heads, part_rows = part_rows_of(all);
+        const int each = p.queries * p.heads;
         const int threads = few ? 64 : 128;
         const auto softmax_sync = [&] { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); };
         int n = 0;
@@ -755,8 +955,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // tiles, also after one has given up.
         pair_ready();
         while (walk.next(s)) {
+            const int all = kShared ? s.all : each, part_rows = part_rows_of(all);
             const int m_row = s.group * kRows + rank * block_rows + r;
-            const int limit = s.length - (p.queries - 1 - min(m_row / p.heads, p.queries - 1));
+            int limit = s.length;
+            if (kShared && s.row == 0) {
+                const int m = min(m_row, all - 1), b = m / each;
+                limit = min(limit, length_of(p, b) - (p.queries - 1 - (m - b * each) / p.heads));
+            } else {
+                limit -= p.queries - 1 - min(m_row / p.heads, p.queries - 1);
+            }
             float m = -INFINITY, l = 0.f;
             for (int tile = s.first; tile < s.last; ++tile, ++n) {
                 wait.warp(&sh.mask_full[n & 3], (n >> 2) & 1);
@@ -768,7 +975,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc::load32(lanes + kScore + kHalf * (n & 1) + 32 * c, raw_s + 32 * c);
                 uint32_t seen[kHalf / 32];
                 bool all_seen = true;
-                const int left = limit - tile * kTile - half * kHalf;  // of this thread's slots
+                const int left = limit - static_cast<int>(position<kShared>(s, tile, half * kHalf));  // of this thread's slots
 #pragma unroll
                 for (int c = 0; c < kHalf / 32; ++c) {
                     seen[c] = sh.mask[n & 3][half * (kHalf / 32) + c];
@@ -843,10 +1050,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool whole = s.first == 0 && s.last == s.tiles;
             const int64_t at = static_cast<int64_t>(s.row) * all + m_row;
             const int r_part = m_row - s.group * kRows;
-            float* part = whole ? nullptr : part_of(p, part_rows, 2 * pair + (s.first == 0 ? 1 : 0));
-            if (!whole && half == 0 && m_row < all)
+            float* part = kShared ? (whole ? whole_of(p, s.row, s.group) : run_of(p, 2 * pair + (s.first == 0 ? 1 : 0)))
+                          : whole ? nullptr
+                                  : part_of(p, part_rows, 2 * pair + (s.first == 0 ? 1 : 0));
+            if ((kShared || !whole) && half == 0 && m_row < all)
                 reinterpret_cast<float2*>(part + static_cast<int64_t>(part_rows) * kLatent)[r_part] = make_float2(m, l);
-            if (whole && p.lse && half == 0 && m_row < all)
+            if (!kShared && whole && p.lse && half == 0 && m_row < all)
                 p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             const float by = l == 0.f ? 0.f : 1.f / l;
             uint16_t* out = static_cast<uint16_t*>(p.out) + at * kLatent + 256 * half;
@@ -858,7 +1067,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc::load32(lanes + 64 * c, o);
                 tc::load32(lanes + 64 * c + 32, o + 32);
                 tc::wait_load();
-                if (m_row < all && whole) {
+                if (!kShared && m_row < all && whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[8];
@@ -901,6 +1110,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // eight loads in flight.
 constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 4;
+// Units of 32 rows from which on a warp of the join behind shared positions
+// takes 16 values of each.
+constexpr int kFewUnits = 64;
 
 // Values 4 c.. 4 (c + kColumns) of one row; kParts parts at a time.
 template <bool kBf16, int kColumns, int kParts>
@@ -1011,7 +1223,92 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const LatentParam
     }
 }
 
+// Joins what the prompt and a request's own positions give: a (request, query,
+// head) row a lane, 32 of them in a row a unit, 4 kColumns values a warp.
+template <bool kBf16, int kColumns>
+__global__ void __launch_bounds__(kJoinThreads, 2) join_shared_kernel(const LatentParams p) {
+    constexpr int kParts = 8 / kColumns;  // looked at a time
+    constexpr int kPerUnit = kLatent / (4 * kColumns) / (kJoinThreads / 32);
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int each = p.queries * p.heads, common = min(max(*p.shared_len, 0), p.max_shared);
+    const int64_t rows = static_cast<int64_t>(p.batch) * each, units = (rows + 31) / 32 * kPerUnit;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t at = unit / kPerUnit * 32 + lane;
+        const int c = static_cast<int>(unit % kPerUnit * (kJoinThreads / 32) + warp) * kColumns;
+        if (at >= rows) continue;
+        const int b = static_cast<int>(at / each), m = static_cast<int>(at - static_cast<int64_t>(b) * each);
+        const int prompt_group = static_cast<int>(at / kRows), group = m / kRows;
+        const int2 prompt = common > 0 ? parts_of(p, 0, prompt_group) : make_int2(0, 0);
+        const int2 own = length_of(p, b) > common ? parts_of(p, b + 1, group) : make_int2(0, 0);
+        const int prompt_rows = part_rows_of(rows), own_rows = part_rows_of(each);
+        float top = -INFINITY, l = 0.f;
+        float4 o[kColumns] = {};
+        for (int i0 = 0; i0 < prompt.y + own.y; i0 += kParts) {
+            float2 stats[kParts];
+            float4 x[kParts][kColumns];
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                stats[k] = make_float2(-INFINITY, 0.f);
+                if (i0 + k < prompt.y + own.y) {
+                    const bool of_prompt = i0 + k < prompt.y;
+                    const int i = of_prompt ? i0 + k : i0 + k - prompt.y;
+                    const int2 parts = of_prompt ? prompt : own;
+                    const int n = of_prompt ? prompt_rows : own_rows;
+                    const int r = of_prompt ? static_cast<int>(at % kRows) : m % kRows;
+                    const float* part = parts.y > 1 ? run_of(p, 2 * (parts.x + i) + (i == 0 ? 1 : 0))
+                                        : of_prompt ? whole_of(p, 0, prompt_group)
+                                                    : whole_of(p, b + 1, group);
+                    stats[k] = reinterpret_cast<const float2*>(part + static_cast<int64_t>(n) * kLatent)[r];
+#pragma unroll
+                    for (int v = 0; v < kColumns; ++v)
+                        x[k][v] = reinterpret_cast<const float4*>(part)[static_cast<int64_t>(c + v) * n + r];
+                }
+            }
+            // The maximum may rise: what is summed so far is scaled back.
+            const float was = top;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) top = fmaxf(top, stats[k].x);
+            const float base = top == -INFINITY ? 0.f : top, back = exp2f(was - base);
+            l *= back;
+#pragma unroll
+            for (int v = 0; v < kColumns; ++v)
+                o[v] = make_float4(o[v].x * back, o[v].y * back, o[v].z * back, o[v].w * back);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                if (stats[k].y == 0.f) continue;  // a part that saw nothing
+                const float by = exp2f(stats[k].x - base);
+                l += stats[k].y * by;
+#pragma unroll
+                for (int v = 0; v < kColumns; ++v)
+                    o[v] = make_float4(o[v].x + x[k][v].x * by, o[v].y + x[k][v].y * by, o[v].z + x[k][v].z * by,
+                                       o[v].w + x[k][v].w * by);
+            }
+        }
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        uint32_t w[2 * kColumns];
+#pragma unroll
+        for (int v = 0; v < kColumns; ++v) {
+            w[2 * v] = tc::pack<kBf16>(o[v].x * by, o[v].y * by);
+            w[2 * v + 1] = tc::pack<kBf16>(o[v].z * by, o[v].w * by);
+        }
+        uint16_t* out = static_cast<uint16_t*>(p.out) + at * kLatent + 4 * c;
+        if constexpr (kColumns == 4)
+            tc::store_v8(out, w);
+        else
+            *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+        if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
 }  // namespace
+
+size_t shared_workspace_bytes(int32_t batch, int32_t queries, int32_t heads) {
+    const int64_t each = static_cast<int64_t>(queries) * heads, all = each * batch;
+    const int64_t floats = (2 * kMaxPairs + groups_in(all)) * place_floats(all) + batch * groups_in(each) * place_floats(each);
+    return static_cast<size_t>((all_groups(batch, each) + 1) / 2 * 2) * sizeof(int2) + static_cast<size_t>(floats) * sizeof(float);
+}
 
 size_t latent_workspace_bytes(int32_t, int32_t queries, int32_t heads) {
     const int64_t all = static_cast<int64_t>(queries) * heads;
@@ -1020,19 +1317,35 @@ size_t latent_workspace_bytes(int32_t, int32_t queries, int32_t heads) {
 }
 
 topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream) {
-    const bool bf16 = dtype == TOPK_BF16;
-    LatentMaps maps;
+    const bool bf16 = dtype == TOPK_BF16, shared = p.shared_len != nullptr;
+    LatentMaps maps = {};
     // Query rows: one dimension of (query, head) where those have one stride,
     // copied 64 rows at a time; else one row at a time.
     const bool whole_rows = p.queries == 1 || p.heads == 1 || p.q_query_stride == p.heads * p.q_head_stride;
     const int64_t any = 2 * kWidth;  // stride of a dimension of one entry
-    const int64_t all = static_cast<int64_t>(p.queries) * p.heads;
-    const int64_t rows = whole_rows ? all : p.heads;
+    const int64_t each = static_cast<int64_t>(p.queries) * p.heads, all = shared ? each * p.batch : each;
+    const int box = all <= kHalfRows ? kHalfRows / 2 : kHalfRows;
     const int64_t row_step = whole_rows && p.heads == 1 ? p.q_query_stride : p.q_head_stride;
-    const int64_t q_dims[4] = {kWidth, rows, whole_rows ? 1 : p.queries, p.batch};
-    const int64_t q_steps[3] = {rows > 1 ? 2 * row_step : any, whole_rows ? any : 2 * p.q_query_stride,
-                                p.batch > 1 ? 2 * p.q_row_stride : any};
-    CUresult r = encode_map(&maps.q, bf16, p.q, 4, q_dims, q_steps, 1, !whole_rows ? 1 : all <= kHalfRows ? kHalfRows / 2 : kHalfRows);
+    const auto encode_rows = [&](CUtensorMap* map, bool whole) {
+        const int64_t rows = whole ? each : p.heads;
+        const int64_t dims[4] = {kWidth, rows, whole ? 1 : p.queries, p.batch};
+        const int64_t steps[3] = {rows > 1 ? 2 * row_step : any, whole ? any : 2 * p.q_query_stride,
+                                  p.batch > 1 ? 2 * p.q_row_stride : any};
+        return encode_map(map, bf16, p.q, 4, dims, steps, 1, whole ? box : 1);
+    };
+    CUresult r = encode_rows(&maps.q, whole_rows);
+    // The rows of all requests likewise.
+    const bool all_rows = shared && whole_rows && (p.batch == 1 || each == 1 || p.q_row_stride == each * row_step);
+    if (all_rows && r == CUDA_SUCCESS) {
+        const int64_t step = each == 1 ? p.q_row_stride : row_step;
+        const int64_t dims[4] = {kWidth, all, 1, 1}, steps[3] = {all > 1 ? 2 * step : any, any, any};
+        r = encode_map(&maps.all_q, bf16, p.q, 4, dims, steps, 1, box);
+    } else if (shared && r == CUDA_SUCCESS) {
+        const int64_t dims[4] = {kWidth, p.heads, p.queries, p.batch};
+        const int64_t steps[3] = {p.heads > 1 ? 2 * p.q_head_stride : any, p.queries > 1 ? 2 * p.q_query_stride : any,
+                                  p.batch > 1 ? 2 * p.q_row_stride : any};
+        r = encode_map(&maps.all_q, bf16, p.q, 4, dims, steps, 1, 1);
+    }
     const int64_t c_dims[2] = {kWidth, p.num_slots}, c_steps[1] = {2 * p.slot_stride};
     // Pages of 16 slots or more go through the copy engine.
     const bool paged = !p.indices && p.log2_page >= 4;
@@ -1040,21 +1353,31 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const Att
     if (r == CUDA_SUCCESS) r = encode_map(&maps.cache, bf16, p.cache, 2, c_dims, c_steps, 1, box_rows);
     if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "latent attention tensor map");
 
-    const auto kernel = paged ? (bf16 ? latent_kernel<true, true> : latent_kernel<false, true>)
-                              : (bf16 ? latent_kernel<true, false> : latent_kernel<false, false>);
-    static std::atomic<bool> prepared[4][AttendDevice::kMax];
-    cudaError_t e = allow_shared(kernel, kSmem, prepared[2 * paged + bf16][device.index]);
+    const auto kernel = shared ? (paged ? (bf16 ? latent_kernel<true, true, true> : latent_kernel<false, true, true>)
+                                        : (bf16 ? latent_kernel<true, false, true> : latent_kernel<false, false, true>))
+                               : (paged ? (bf16 ? latent_kernel<true, true, false> : latent_kernel<false, true, false>)
+                                        : (bf16 ? latent_kernel<true, false, false> : latent_kernel<false, false, false>));
+    static std::atomic<bool> prepared[8][AttendDevice::kMax];
+    cudaError_t e = allow_shared(kernel, kSmem, prepared[4 * shared + 2 * paged + bf16][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention shared memory");
-    const int64_t groups = (all + kRows - 1) / kRows;
-    const int64_t tiles = p.batch * groups * (p.max_len > kTile ? (p.max_len + int64_t{kTile} - 1) / kTile : 1);
+    const auto tiles_in = [](int64_t n) { return n > kTile ? (n + kTile - 1) / kTile : 1; };
+    int64_t tiles = p.batch * groups_in(each) * tiles_in(p.max_len);
+    if (shared) tiles += groups_in(all) * tiles_in(p.max_shared);
     if (tiles > INT32_MAX) return TOPK_EINVAL;
     const int64_t most = device.sms / 2 < kMaxPairs ? device.sms / 2 : kMaxPairs;
     const int pairs = static_cast<int>(tiles < most ? tiles : most);
     const float scale_log2 = std::fmax(std::fabs(p.scale) * 1.4426950408889634f, FLT_MIN);
     e = launch_early(kernel, dim3(2 * pairs), kThreads, kSmem, stream, p, maps, device.flags, scale_log2, p.scale < 0.f,
-                     whole_rows, box_rows);
+                     whole_rows, all_rows, box_rows);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
-    if (pairs > 1) {
+    if (shared) {
+        const bool wide = all >= 32 * kFewUnits;
+        const int64_t units = (all + 31) / 32 * (wide ? kLatent / 128 : kLatent / 32), blocks = 2 * device.sms;
+        const auto join = wide ? (bf16 ? join_shared_kernel<true, 4> : join_shared_kernel<false, 4>)
+                               : (bf16 ? join_shared_kernel<true, 1> : join_shared_kernel<false, 1>);
+        e = launch_early(join, dim3(static_cast<unsigned>(units < blocks ? units : blocks)), kJoinThreads, 0, stream, p);
+        if (e != cudaSuccess) return api_cuda_fail(e, "shared attention join launch");
+    } else if (pairs > 1) {
         const int units = (pairs - 1) * ((part_rows_of(all) + 31) / 32) * 16, blocks = 2 * device.sms;
         e = launch_early(bf16 ? join_kernel<true> : join_kernel<false>, dim3(units < blocks ? units : blocks), kJoinThreads,
                          0, stream, p, pairs);
