@@ -16,10 +16,11 @@
 // (or 128 rows of it) each; tensor memory holds two tiles of scores, one of
 // them read while the other is computed.
 //
-// Heads are padded to a multiple of 16 columns by the copy engine, with zeros.
-// A chunk holds a power of two of queries (up to 256 columns in each of one or
-// two products), so that the sum of a request's tiles under the causal limit
-// has a closed form.
+// Heads are padded to a power of two of columns, 16 or more, by the copy
+// engine, with zeros: the loops over a query's columns are unrolled, and a chunk
+// holds a power of two of queries (up to 256 columns in each of one or two
+// products), so that the sum of a request's tiles under the causal limit has a
+// closed form.
 //
 // Warps: 0-3 and 4-7 sums of even and odd score tiles, 8 products, 9 keys, 10
 // queries and weights.
@@ -66,7 +67,7 @@ struct ScoreMaps {
 };
 // How the columns are laid out: per query, product, chunk.
 struct Layout {
-    int32_t padded;      // heads, a multiple of 16
+    int32_t padded;      // heads, a power of two
     int32_t log2_queries;  // of a chunk
     int32_t product_queries;
     int32_t places;      // chunks in shared memory: 2 of one product or 1 of two
@@ -225,10 +226,42 @@ struct Walk {
     }
 };
 
-// kStep: columns of scores that a thread takes at a time (it divides a query's).
-template <int kStep>
+// Columns of scores that a thread takes at a time, while the next are on their way.
+constexpr int kStep = 32;
+__device__ __forceinline__ void load_step(uint32_t from, uint32_t* to) {
+#pragma unroll
+    for (int i = 0; i < kStep; i += 32) tc::load32(from + i, to + i);
+}
+
+// Waits for what load_step asked for; nothing of it is used before.
+__device__ __forceinline__ void landed(uint32_t* x) {
+    tc::wait_load();
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) asm volatile("" : "+r"(x[i]));
+}
+
+// sum += w max(x, 0) over kCount columns from `at` on, with the weights in shared
+// memory; pairs of floats in 64 bits.  kFull: every column is a head.  Else
+// those from `heads` on are zeros, but for a key that holds infinities.
+template <int kCount, bool kFull>
+__device__ __forceinline__ void add_part(const uint32_t* x, int at, int heads, uint32_t w_at, uint64_t* sum) {
+    const auto top = [&](int i) {
+        return ptx::fmax_nan(kFull || at + i < heads ? __uint_as_float(x[i]) : 0.f, 0.f);
+    };
+#pragma unroll
+    for (int i = 0; i < kCount; i += 4) {
+        uint64_t w[2];
+        ptx::lds_u64x2(w_at + 4 * i, w);
+        sum[0] = tc::fma2(tc::pair(top(i), top(i + 1)), w[0], sum[0]);
+        sum[1] = tc::fma2(tc::pair(top(i + 2), top(i + 3)), w[1], sum[1]);
+    }
+}
+
+// kHeads: columns of a query.
+template <int kHeads, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1)
     index_scores_kernel(const IndexScoresParams p, const __grid_constant__ ScoreMaps maps, const Layout a, uint32_t* flags) {
+    constexpr int kProductQueries = kColumns / kHeads;
     extern __shared__ uint8_t raw[];
     const uint32_t start = ptx::smem_addr(raw), base = (start + kSlack - 1u) & ~(kSlack - 1u);
     const uint32_t queries = base, keys = queries + kQueryBytes, weights = keys + kStages * kKeyBytes;
@@ -330,18 +363,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kQueryWarp) {
         for (int n = 0; walk.next(s); ++n) {
             const int place = n % a.places, round = n / a.places;
-            if (round > 0 && (!wait.all(&sh.query_empty[place], (round - 1) & 1) || wait.over())) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.query_full[place], s.queries * a.padded * 256);
+            // Weights come to registers, and queries to L2, while the place is still in use.
+            float w[kAllColumns / 32];
+#pragma unroll
+            for (int k = 0; k < kAllColumns / 32; ++k) {
+                const int i = 32 * k + lane, q = i / kHeads, h = i % kHeads;
+                w[k] = q < s.queries && h < p.heads ? p.weights[(s.query + q) * p.weights_stride + h] : 0.f;
+            }
+            if (round > 0) {
+                for (int i = lane; i < 2 * s.queries; i += 32)
+                    tc::prefetch_3d(&maps.q, 64 * (i & 1), 0, s.query + (i >> 1));
+                if (!wait.all(&sh.query_empty[place], (round - 1) & 1) || wait.over()) break;
+            }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.query_full[place], s.queries * kHeads * 256);
             __syncwarp();
             for (int i = lane; i < 2 * s.queries; i += 32)
-                tc::load_3d(queries + place * place_bytes + (i & 1) * (place_columns * 128) + (i >> 1) * (a.padded * 128), &maps.q,
+                tc::load_3d(queries + place * place_bytes + (i & 1) * (place_columns * 128) + (i >> 1) * (kHeads * 128), &maps.q,
                             64 * (i & 1), 0, s.query + (i >> 1), &sh.query_full[place]);
-            const uint32_t to = weights + place * (place_columns * 4);
-            for (int i = lane; i < s.queries * a.padded; i += 32) {
-                const int h = i % a.padded;
-                const float w = h < p.heads ? p.weights[(s.query + i / a.padded) * p.weights_stride + h] : 0.f;
-                ptx::sts_u32(to + 4 * i, __float_as_uint(w));
-            }
+#pragma unroll
+            for (int k = 0; k < kAllColumns / 32; ++k)
+                if (32 * k < place_columns)
+                    ptx::sts_u32(weights + 4 * (place * place_columns + 32 * k + lane), __float_as_uint(w[k]));
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sh.weight_full[place]);
             if (!wait.all(&sh.query_full[place], round & 1)) {
@@ -360,20 +402,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int tile = s.first; tile < s.last; ++tile, ++n) {
                 const int stage = n % kStages;
                 on = wait.all(&sh.key_full[stage], (n / kStages) & 1) && on;
-                for (int first = 0; first < s.queries; first += a.product_queries, ++u) {
+                for (int first = 0; first < s.queries; first += kProductQueries, ++u) {
                     if (u > 1) on = wait.all(&sh.score_empty[u & 1], ((u >> 1) - 1) & 1) && on;
                     tc::fence_after();
                     if (on && tc::elect()) {
-                        const int columns = min(s.queries - first, a.product_queries) * a.padded;
+                        const int columns = min(s.queries - first, kProductQueries) * kHeads;
                         const uint32_t instr = a.instruction | (static_cast<uint32_t>(columns >> 3) << 17);
                         const uint64_t k_at = key_at + stage * (kKeyBytes >> 4);
-                        const uint64_t q_at = query_at + ((place * place_bytes + first * a.padded * 128) >> 4);
+                        const uint64_t q_at = query_at + ((place * place_bytes + first * kHeads * 128) >> 4);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             tc::mma<1>(tmem + kColumns * (u & 1), k_at + (k >> 2) * (kHalfKeys >> 4) + 2 * (k & 3),
                                        q_at + (k >> 2) * (place_columns * 8) + 2 * (k & 3), instr, k > 0);
                         tc::commit<1>(&sh.score_full[u & 1]);
-                        if (first + a.product_queries >= s.queries) {
+                        if (first + kProductQueries >= s.queries) {
                             tc::commit<1>(&sh.key_empty[stage]);
                             if (tile == s.last - 1) tc::commit<1>(&sh.query_empty[place]);
                         }
@@ -389,8 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         const int group = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColumns * group;
-        const int steps = a.padded / kStep;  // of a query
-        const int rest = p.heads - (steps - 1) * kStep;  // heads of the last of them
+        // A unit of columns: a query or more, an even number of steps.
+        constexpr int kUnit = kHeads > 2 * kStep ? kHeads : 2 * kStep, kUnitQueries = kUnit / kHeads;
+        constexpr int kPart = kHeads < kStep ? kHeads : kStep;  // columns of one query in a step
         int n = 0, u = 0;
         // These warps go through all tiles, also after a wait has given up.
         for (int segment = 0; walk.next(s); ++segment) {
@@ -398,54 +441,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t weights_at = weights + place * (place_columns * 4);
             wait.warp(&sh.weight_full[place], (segment / a.places) & 1);
             for (int tile = s.first; tile < s.last; ++tile, ++n) {
-                for (int first = 0; first < s.queries; first += a.product_queries, ++u) {
+                for (int first = 0; first < s.queries; first += kProductQueries, ++u) {
                     if ((u & 1) != group) continue;
                     wait.warp(&sh.mask_full[n % kMasks], (n / kMasks) & 1);
                     wait.warp(&sh.score_full[group], (u >> 1) & 1);
                     tc::fence_after();
                     const bool there = (sh.mask[n % kMasks][r >> 5] >> (r & 31)) & 1;
-                    const int t = tile * kTile + r, count = min(s.queries - first, a.product_queries);
+                    const int t = tile * kTile + r, count = min(s.queries - first, kProductQueries);
                     float* out = p.scores + (s.query + first) * p.scores_stride + t;
-                    int seen = s.seen + first;  // positions that the query sees
-                    uint32_t x[kStep];
-                    const auto load = [&](uint32_t column, uint32_t* to) {
-                        if constexpr (kStep == 32)
-                            tc::load32(lanes + column, to);
-                        else
-                            tc::load16(lanes + column, to);
-                    };
-                    load(0, x);
-                    uint32_t at = 0;  // column of what is loaded
-                    for (int q = 0; q < count; ++q, ++seen, out += p.scores_stride) {
-                        float2 sum[2] = {};
-                        for (int step = 0; step < steps; ++step) {
-                            float f[kStep];
-                            tc::wait_load();
-                            // (not read before, nor overwritten by the next)
+                    const int seen = s.seen + first;  // positions that the first of them sees
+                    uint32_t w_at = weights_at + 4 * first * kHeads;
+                    uint32_t x[2][kStep];
+                    load_step(lanes, x[0]);
+                    for (int q = 0; q < count; q += kUnitQueries, w_at += 4 * kUnit) {
+                        uint64_t sum[2] = {};
 #pragma unroll
-                            for (int i = 0; i < kStep; ++i) {
-                                asm volatile("" : "+r"(x[i]));
-                                f[i] = __uint_as_float(x[i]);
-                            }
-                            const uint32_t w_at = weights_at + 4 * (first * a.padded + at);
-                            at += kStep;
-                            if (at < static_cast<uint32_t>(count * a.padded)) load(at, x);
-                            // Columns behind the last head are zeros, but a key may hold infinities.
-                            if (step == steps - 1 && rest < kStep) {
+                        for (int c = 0; c < kUnit; c += kStep) {
+                            uint32_t* now = x[c / kStep & 1];
+                            landed(now);
+                            // (columns behind the last query's are in this half of tensor memory too)
+                            if (c + kStep < kUnit || q + kUnitQueries < count)
+                                load_step(lanes + q * kHeads + c + kStep, x[(c / kStep + 1) & 1]);
 #pragma unroll
-                                for (int i = 0; i < kStep; ++i)
-                                    if (i >= rest) f[i] = 0.f;
-                            }
-#pragma unroll
-                            for (int i = 0; i < kStep; i += 4) {
-                                const float4 w = ptx::lds_f4(w_at + 4 * i);
-                                sum[0] = tc::fma2(make_float2(ptx::fmax_nan(f[i], 0.f), ptx::fmax_nan(f[i + 1], 0.f)),
-                                                  make_float2(w.x, w.y), sum[0]);
-                                sum[1] = tc::fma2(make_float2(ptx::fmax_nan(f[i + 2], 0.f), ptx::fmax_nan(f[i + 3], 0.f)),
-                                                  make_float2(w.z, w.w), sum[1]);
+                            for (int i = 0; i < kStep; i += kPart) {
+                                add_part<kPart, kFull>(now + i, (c + i) % kHeads, p.heads, w_at + 4 * (c + i), sum);
+                                if ((c + i + kPart) % kHeads != 0) continue;
+                                const int j = q + (c + i) / kHeads;
+                                const float2 a = tc::unpair(sum[0]), b = tc::unpair(sum[1]);
+                                if (j < count && t < seen + j) out[j * p.scores_stride] = there ? (a.x + a.y) + (b.x + b.y) : -INFINITY;
+                                sum[0] = sum[1] = 0;
                             }
                         }
-                        if (t < seen) *out = there ? (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) : -INFINITY;
                     }
                     tc::fence_before();
                     __syncwarp();
@@ -471,14 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream) {
     const bool bf16 = dtype == TOPK_BF16;
     Layout a = {};
-    a.padded = (p.heads + 15) / 16 * 16;
-    int log2 = 0;  // queries of a product
-    while ((2 << log2) * a.padded <= kColumns) ++log2;
-    a.product_queries = 1 << log2;
+    int log2_heads = 4;
+    while ((1 << log2_heads) < p.heads) ++log2_heads;
+    a.padded = 1 << log2_heads;
+    a.product_queries = kColumns / a.padded;
     // Requests of up to one product's queries: the next chunk's come while
     // this one's are used; else each key is read for two products.
     a.places = p.total_q <= static_cast<int64_t>(p.batch) * a.product_queries ? 2 : 1;
-    a.log2_queries = a.places == 2 ? log2 : log2 + 1;
+    a.log2_queries = 8 - log2_heads + (a.places == 2 ? 0 : 1);
     a.box_rows = p.log2_page < 7 ? 1 << p.log2_page : kTile;
     a.instruction = tc::instruction(bf16, kTile, 0, false, false);
 
@@ -491,10 +517,16 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     if (r == CUDA_SUCCESS) r = encode_map(&maps.cache, bf16, p.cache, 2, c_dims, c_steps, 1, a.box_rows);
     if (r != CUDA_SUCCESS) return api_cuda_fail(cudaErrorInvalidValue, "index scores tensor map");
 
-    const bool wide = a.padded % 32 == 0;
-    const auto kernel = wide ? index_scores_kernel<32> : index_scores_kernel<16>;
-    static std::atomic<bool> prepared[2][AttendDevice::kMax];
-    cudaError_t e = allow_shared(kernel, kSmem, prepared[wide][device.index]);
+    using Kernel = decltype(&index_scores_kernel<16, true>);
+    static constexpr Kernel kernels[2][5] = {
+        {index_scores_kernel<16, false>, index_scores_kernel<32, false>, index_scores_kernel<64, false>,
+         index_scores_kernel<128, false>, index_scores_kernel<256, false>},
+        {index_scores_kernel<16, true>, index_scores_kernel<32, true>, index_scores_kernel<64, true>,
+         index_scores_kernel<128, true>, index_scores_kernel<256, true>}};
+    const bool full = p.heads == a.padded;
+    const Kernel kernel = kernels[full][log2_heads - 4];
+    static std::atomic<bool> prepared[2][5][AttendDevice::kMax];
+    cudaError_t e = allow_shared(kernel, kSmem, prepared[full][log2_heads - 4][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "index scores shared memory");
     const int64_t chunks = ((static_cast<int64_t>(p.total_q) + (1 << a.log2_queries) - 1) >> a.log2_queries) + p.batch;
     const int64_t tiles = chunks * ((p.max_len + int64_t{kTile} - 1) / kTile);
