@@ -40,26 +40,29 @@ namespace {
 constexpr int kThreads = 352;
 constexpr int kProductWarp = 8, kKeyWarp = 9, kQueryWarp = 10;
 constexpr int kTile = 128;
-constexpr int kStages = 3;
-constexpr int kMasks = 8;  // tiles whose masks are kept: kStages copied ahead, two scored, and room
+constexpr int kStages = 5, kBuffers = 4;       // tiles of keys and of scores, at most
+constexpr int kMasks = kStages + kBuffers + 1;  // tiles whose masks are kept: those copied ahead and scored, and one
 constexpr int kColumns = 256, kAllColumns = 2 * kColumns;  // of one product; of the queries in shared memory
 constexpr int kHalfKeys = kTile * 128;                     // 64 values of a tile's keys
 constexpr int kKeyBytes = 2 * kHalfKeys, kQueryBytes = 2 * kAllColumns * 128, kWeightBytes = kAllColumns * 4;
+constexpr int kTileBytes = kQueryBytes + 3 * kKeyBytes;  // queries and keys
 
 struct Shared {
     uint64_t query_full[2], query_empty[2], weight_full[2];
     uint64_t key_full[kStages], key_empty[kStages], mask_full[kMasks];
-    uint64_t score_full[2], score_empty[2], end;
+    uint64_t score_full[kBuffers], score_empty[kBuffers], end;
     int64_t total, begin;  // tiles of the whole call; the first of this block's run
-    int64_t scan[kThreads / 32];
-    uint32_t mask[kMasks][4];
+    union {
+        int64_t scan[kThreads / 32];  // until the run is found
+        uint32_t mask[kMasks][4];
+    };
     int32_t row, chunk, tile;  // where the run begins
     uint32_t tmem, gave_up;
 };
 // The structure lies before or behind the tiles, in what their alignment leaves.
 constexpr int kSlack = 1024;
 static_assert(sizeof(Shared) <= kSlack / 2, "barriers fit on one side");
-constexpr int kSmem = kQueryBytes + kStages * kKeyBytes + kWeightBytes + kSlack;
+constexpr int kSmem = kTileBytes + kWeightBytes + kSlack;
 static_assert(kSmem <= 232448, "shared memory of a block");
 
 struct ScoreMaps {
@@ -71,6 +74,9 @@ struct Layout {
     int32_t log2_queries;  // of a chunk
     int32_t product_queries;
     int32_t places;      // chunks in shared memory: 2 of one product or 1 of two
+    int32_t place_columns;  // of each
+    int32_t stages;      // tiles of keys in shared memory
+    int32_t buffers;     // tiles of scores in tensor memory
     int32_t box_rows;    // keys per copy
     uint32_t instruction;  // without N
 };
@@ -261,13 +267,12 @@ __device__ __forceinline__ void add_part(const uint32_t* x, int at, int heads, u
 template <int kHeads, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1)
     index_scores_kernel(const IndexScoresParams p, const __grid_constant__ ScoreMaps maps, const Layout a, uint32_t* flags) {
-    constexpr int kProductQueries = kColumns / kHeads;
     extern __shared__ uint8_t raw[];
     const uint32_t start = ptx::smem_addr(raw), base = (start + kSlack - 1u) & ~(kSlack - 1u);
-    const uint32_t queries = base, keys = queries + kQueryBytes, weights = keys + kStages * kKeyBytes;
+    const int place_columns = a.place_columns, place_bytes = place_columns * 256;
+    const uint32_t queries = base, keys = queries + a.places * place_bytes, weights = base + kTileBytes;
     Shared& sh = *reinterpret_cast<Shared*>(raw + (base - start >= sizeof(Shared) ? 0 : weights + kWeightBytes - start));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int place_columns = kAllColumns / a.places, place_bytes = kQueryBytes / a.places;
 
     if (threadIdx.x == 0) {
         sh.gave_up = p.wait.none;
@@ -275,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&sh.query_full[i], 1);
             ptx::mbar_init(&sh.query_empty[i], 9);  // the products, and each warp that reads the weights
             ptx::mbar_init(&sh.weight_full[i], 1);
+        }
+        for (int i = 0; i < kBuffers; ++i) {
             ptx::mbar_init(&sh.score_full[i], 1);
             ptx::mbar_init(&sh.score_empty[i], 4);
         }
@@ -311,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         fetch();
+        int stage = 0, round = 0, kept = 0;  // the place of tile n, how often it was filled, the mask's place
         while (more) {
             int slot[4];
 #pragma unroll
@@ -324,18 +332,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile = s.first;
             }
             fetch();
-            const int stage = n % kStages;
-            if (n >= kStages && !wait.all(&sh.key_empty[stage], (n / kStages - 1) & 1)) break;
-            // The mask's place was last read for tile n - 8; the copies of tile
-            // n waited for the products of tile n - 3, and those for the sums
-            // two score tiles before.
+            if (round > 0 && !wait.all(&sh.key_empty[stage], (round - 1) & 1)) break;
+            // The mask's place was last read for tile n - kMasks; the copies of
+            // tile n waited for the products of tile n - stages, and those for
+            // the sums of the score tile `buffers` before.
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t bits = __ballot_sync(~0u, slot[i] >= 0);
-                if (lane == 0) sh.mask[n % kMasks][i] = bits;
+                if (lane == 0) sh.mask[kept][i] = bits;
             }
             if (lane == 0) {
-                ptx::mbar_arrive(&sh.mask_full[n % kMasks]);
+                ptx::mbar_arrive(&sh.mask_full[kept]);
                 ptx::mbar_arrive_expect_tx(&sh.key_full[stage], kKeyBytes);
             }
             __syncwarp();
@@ -355,9 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ++n;
+            if (++stage == a.stages) {
+                stage = 0;
+                ++round;
+            }
+            if (++kept == kMasks) kept = 0;
         }
-        for (int i = 0; i < kStages; ++i) {
-            const int copied = (n + kStages - 1 - i) / kStages;  // to this place
+        for (int i = 0; i < a.stages; ++i) {
+            const int copied = (n + a.stages - 1 - i) / a.stages;  // to this place
             if (copied > 0) tc::Waits::drain(&sh.key_full[i], (copied - 1) & 1);
         }
     } else if (warp == kQueryWarp) {
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             64 * (i & 1), 0, s.query + (i >> 1), &sh.query_full[place]);
 #pragma unroll
             for (int k = 0; k < kAllColumns / 32; ++k)
-                if (32 * k < place_columns)
+                if (32 * k + lane < place_columns)
                     ptx::sts_u32(weights + 4 * (place * place_columns + 32 * k + lane), __float_as_uint(w[k]));
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sh.weight_full[place]);
@@ -393,34 +405,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kProductWarp) {
         const uint64_t key_at = tc::operand(keys), query_at = tc::operand(queries);
-        int n = 0, u = 0;
+        const uint32_t buffer_columns = 2 * kColumns / a.buffers;
+        int stage = 0, buffer = 0;
+        uint32_t round = 0, use = 0;  // how often the places were used
         // Given up, nothing is issued or announced any more.
         bool on = true;
         for (int segment = 0; walk.next(s); ++segment) {
             const int place = segment % a.places;
             on = wait.all(&sh.query_full[place], (segment / a.places) & 1) && on;
-            for (int tile = s.first; tile < s.last; ++tile, ++n) {
-                const int stage = n % kStages;
-                on = wait.all(&sh.key_full[stage], (n / kStages) & 1) && on;
-                for (int first = 0; first < s.queries; first += kProductQueries, ++u) {
-                    if (u > 1) on = wait.all(&sh.score_empty[u & 1], ((u >> 1) - 1) & 1) && on;
+            for (int tile = s.first; tile < s.last; ++tile) {
+                on = wait.all(&sh.key_full[stage], round & 1) && on;
+                for (int first = 0; first < s.queries; first += a.product_queries) {
+                    if (use > 0) on = wait.all(&sh.score_empty[buffer], (use - 1) & 1) && on;
                     tc::fence_after();
                     if (on && tc::elect()) {
-                        const int columns = min(s.queries - first, kProductQueries) * kHeads;
+                        const int columns = min(s.queries - first, a.product_queries) * kHeads;
                         const uint32_t instr = a.instruction | (static_cast<uint32_t>(columns >> 3) << 17);
                         const uint64_t k_at = key_at + stage * (kKeyBytes >> 4);
                         const uint64_t q_at = query_at + ((place * place_bytes + first * kHeads * 128) >> 4);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            tc::mma<1>(tmem + kColumns * (u & 1), k_at + (k >> 2) * (kHalfKeys >> 4) + 2 * (k & 3),
+                            tc::mma<1>(tmem + buffer_columns * buffer, k_at + (k >> 2) * (kHalfKeys >> 4) + 2 * (k & 3),
                                        q_at + (k >> 2) * (place_columns * 8) + 2 * (k & 3), instr, k > 0);
-                        tc::commit<1>(&sh.score_full[u & 1]);
-                        if (first + kProductQueries >= s.queries) {
+                        tc::commit<1>(&sh.score_full[buffer]);
+                        if (first + a.product_queries >= s.queries) {
                             tc::commit<1>(&sh.key_empty[stage]);
                             if (tile == s.last - 1) tc::commit<1>(&sh.query_empty[place]);
                         }
                     }
                     __syncwarp();
+                    if (++buffer == a.buffers) {
+                        buffer = 0;
+                        ++use;
+                    }
+                }
+                if (++stage == a.stages) {
+                    stage = 0;
+                    ++round;
                 }
             }
         }
@@ -430,24 +451,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         const int group = warp >> 2, r = threadIdx.x & 127;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColumns * group;
+        const uint32_t buffer_columns = 2 * kColumns / a.buffers;
         // A unit of columns: a query or more, an even number of steps.
         constexpr int kUnit = kHeads > 2 * kStep ? kHeads : 2 * kStep, kUnitQueries = kUnit / kHeads;
         constexpr int kPart = kHeads < kStep ? kHeads : kStep;  // columns of one query in a step
-        int n = 0, u = 0;
+        int kept = 0, buffer = 0;
+        uint32_t round = 0, use = 0;  // of the masks' and the scores' places
         // These warps go through all tiles, also after a wait has given up.
         for (int segment = 0; walk.next(s); ++segment) {
             const int place = segment % a.places;
             const uint32_t weights_at = weights + place * (place_columns * 4);
             wait.warp(&sh.weight_full[place], (segment / a.places) & 1);
-            for (int tile = s.first; tile < s.last; ++tile, ++n) {
-                for (int first = 0; first < s.queries; first += kProductQueries, ++u) {
-                    if ((u & 1) != group) continue;
-                    wait.warp(&sh.mask_full[n % kMasks], (n / kMasks) & 1);
-                    wait.warp(&sh.score_full[group], (u >> 1) & 1);
+            for (int tile = s.first; tile < s.last; ++tile) {
+                for (int first = 0; first < s.queries; first += a.product_queries) {
+                    const int at = buffer;
+                    const uint32_t phase = use & 1;
+                    if (++buffer == a.buffers) {
+                        buffer = 0;
+                        ++use;
+                    }
+                    if ((at & 1) != group) continue;
+                    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + buffer_columns * at;
+                    wait.warp(&sh.mask_full[kept], round & 1);
+                    wait.warp(&sh.score_full[at], phase);
                     tc::fence_after();
-                    const bool there = (sh.mask[n % kMasks][r >> 5] >> (r & 31)) & 1;
-                    const int t = tile * kTile + r, count = min(s.queries - first, kProductQueries);
+                    const bool there = (sh.mask[kept][r >> 5] >> (r & 31)) & 1;
+                    const int t = tile * kTile + r, count = min(s.queries - first, a.product_queries);
                     float* out = p.scores + (s.query + first) * p.scores_stride + t;
                     const int seen = s.seen + first;  // positions that the first of them sees
                     uint32_t w_at = weights_at + 4 * first * kHeads;
@@ -475,7 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&sh.score_empty[group]);
+                    if (lane == 0) ptx::mbar_arrive(&sh.score_empty[at]);
+                }
+                if (++kept == kMasks) {
+                    kept = 0;
+                    ++round;
                 }
             }
             __syncwarp();
@@ -500,11 +533,20 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     int log2_heads = 4;
     while ((1 << log2_heads) < p.heads) ++log2_heads;
     a.padded = 1 << log2_heads;
-    a.product_queries = kColumns / a.padded;
-    // Requests of up to one product's queries: the next chunk's come while
-    // this one's are used; else each key is read for two products.
-    a.places = p.total_q <= static_cast<int64_t>(p.batch) * a.product_queries ? 2 : 1;
-    a.log2_queries = 8 - log2_heads + (a.places == 2 ? 0 : 1);
+    // Requests of few queries each: chunks of as many, the next one's come
+    // while this one's are used, and what room they leave holds more tiles of
+    // keys and of scores.  Else each key is read for two products.
+    const int most = kColumns / a.padded;  // queries of a product
+    int log2 = 0;
+    while ((1 << log2) < most && (int64_t{p.batch} << log2) < p.total_q) ++log2;
+    const bool small = (int64_t{p.batch} << log2) >= p.total_q;
+    a.product_queries = 1 << log2;
+    a.places = small ? 2 : 1;
+    a.log2_queries = small ? log2 : log2 + 1;
+    a.place_columns = a.padded << a.log2_queries;
+    a.buffers = a.padded << log2 <= kColumns / 2 ? kBuffers : 2;
+    a.stages = (kTileBytes - a.places * a.place_columns * 256) / kKeyBytes;
+    if (a.stages > kStages) a.stages = kStages;
     a.box_rows = p.log2_page < 7 ? 1 << p.log2_page : kTile;
     a.instruction = tc::instruction(bf16, kTile, 0, false, false);
 
