@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 352;
 constexpr int kProductWarp = 8, kKeyWarp = 9, kQueryWarp = 10;
-constexpr int kTile = 128;
+constexpr int kTile = 128;  // 2^7
 constexpr int kStages = 5, kBuffers = 4;       // tiles of keys and of scores, at most
 constexpr int kMasks = kStages + kBuffers + 1;  // tiles whose masks are kept: those copied ahead and scored, and one
 constexpr int kColumns = 256, kAllColumns = 2 * kColumns;  // of one product; of the queries in shared memory
@@ -114,10 +114,10 @@ struct Request {
             at += static_cast<int64_t>(first) << log2;
         }
         if (chunk <= first) return 0;
-        const int per_tile = kTile >> log2;
-        const auto sum = [&](int64_t x) {  // of i / per_tile over i < x
-            const int64_t q = x / per_tile;
-            return per_tile * (q * (q - 1) / 2) + (x % per_tile) * q;
+        const int log2_tile = 7 - log2;  // chunks of a tile's length
+        const auto sum = [&](int64_t x) {  // of i >> log2_tile over i < x
+            const int64_t q = x >> log2_tile;
+            return ((q * (q - 1) / 2) << log2_tile) + (x & ((1 << log2_tile) - 1)) * q;
         };
         const int64_t a = at >> log2;
         return sum(a + chunk - first) - sum(a);
@@ -130,6 +130,10 @@ struct Request {
 
 // The run of one of n blocks: as even as can be.
 __device__ __forceinline__ int64_t run_start(int64_t total, int n, int i) {
+    if (total <= INT32_MAX) {  // (a division of 64 bits takes some 100 instructions)
+        const int each = static_cast<int>(total) / n, more = static_cast<int>(total) % n;
+        return static_cast<int64_t>(each) * i + min(i, more);
+    }
     return total / n * i + min(static_cast<int64_t>(i), total % n);
 }
 
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kBuffers; ++i) {
             ptx::mbar_init(&sh.score_full[i], 1);
-            ptx::mbar_init(&sh.score_empty[i], 4);
+            ptx::mbar_init(&sh.score_empty[i], 8);
         }
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(&sh.key_full[i], 1);
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::Waits::drain(&sh.end, 0);
         }
     } else {
-        const int group = warp >> 2, r = threadIdx.x & 127;
+        const int half = warp >> 2, r = threadIdx.x & 127;
         const uint32_t buffer_columns = 2 * kColumns / a.buffers;
         // A unit of columns: a query or more, an even number of steps.
         constexpr int kUnit = kHeads > 2 * kStep ? kHeads : 2 * kStep, kUnitQueries = kUnit / kHeads;
@@ -470,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         buffer = 0;
                         ++use;
                     }
-                    if ((at & 1) != group) continue;
                     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + buffer_columns * at;
                     wait.warp(&sh.mask_full[kept], round & 1);
                     wait.warp(&sh.score_full[at], phase);
@@ -479,18 +482,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int t = tile * kTile + r, count = min(s.queries - first, a.product_queries);
                     float* out = p.scores + (s.query + first) * p.scores_stride + t;
                     const int seen = s.seen + first;  // positions that the first of them sees
-                    uint32_t w_at = weights_at + 4 * first * kHeads;
                     uint32_t x[2][kStep];
-                    load_step(lanes, x[0]);
-                    for (int q = 0; q < count; q += kUnitQueries, w_at += 4 * kUnit) {
+                    const int begin = half * kUnitQueries;
+                    if (begin < count) load_step(lanes + begin * kHeads, x[0]);
+                    for (int q = begin; q < count; q += 2 * kUnitQueries) {
+                        const uint32_t w_at = weights_at + 4 * (first + q) * kHeads;
                         uint64_t sum[2] = {};
 #pragma unroll
                         for (int c = 0; c < kUnit; c += kStep) {
                             uint32_t* now = x[c / kStep & 1];
                             landed(now);
                             // (columns behind the last query's are in this half of tensor memory too)
-                            if (c + kStep < kUnit || q + kUnitQueries < count)
+                            if (c + kStep < kUnit)
                                 load_step(lanes + q * kHeads + c + kStep, x[(c / kStep + 1) & 1]);
+                            else if (q + 2 * kUnitQueries < count)
+                                load_step(lanes + (q + 2 * kUnitQueries) * kHeads, x[(c / kStep + 1) & 1]);
 #pragma unroll
                             for (int i = 0; i < kStep; i += kPart) {
                                 add_part<kPart, kFull>(now + i, (c + i) % kHeads, p.heads, w_at + 4 * (c + i), sum);
