@@ -97,6 +97,7 @@ struct Shared {
     int32_t begin;            // first tile of this pair's run
     int32_t row, tile, length;  // where that lies: row of the batch, tile in the row, the row's length
     int32_t common;           // positions that all rows share
+    int32_t tiles;            // of this pair's run, where runs are cut by cost
     int32_t scan[kThreads / 32];
 };
 constexpr int kSmem = kQueryBytes + kKeyBytes + kValueBytes + kWeightBytes + 1024 + 2048;
@@ -116,6 +117,13 @@ __device__ __forceinline__ int tiles_of(int length) {
     return max(static_cast<int>((static_cast<uint32_t>(length) + kTile - 1) / kTile), 1);
 }
 __device__ __forceinline__ int groups_of(const LatentParams& p) { return (p.queries * p.heads + kRows - 1) / kRows; }
+
+// With shared positions runs are cut by cost.  A group of rows costs its tiles
+// and kBegin more, for its queries' copy and its sums' way out, during which the
+// products wait (3.4 to 4.5 us, a tile 1.75; with runs of equal tiles the pairs
+// that had requests' own positions took 74 us where the others took 60, 64
+// requests behind 32768 positions, and 86 to 48, 32 requests of 4 queries).
+constexpr int kBegin = 2;
 
 // Shared positions (kShared): row 0 of the walk is that prompt, with the
 // (request, query, head) rows of all requests; row 1 + b what request b has of
@@ -142,6 +150,10 @@ struct Row {
         return length <= from ? 0 : static_cast<int>((static_cast<uint32_t>(length - base) + kTile - 1) / kTile);
     }
     __device__ __forceinline__ int groups() const { return (all + kRows - 1) / kRows; }
+    __device__ __forceinline__ int cost() const {  // of a group
+        const int n = tiles();
+        return n > 0 ? n + kBegin : 0;
+    }
 };
 
 // The runs of n pairs over all tiles (both below 2^31), as even as can be: the
@@ -222,17 +234,18 @@ __device__ void locate(const LatentParams& p, int pair, int pairs, Shared& sh) {
     __syncthreads();
 }
 
-// The same with shared positions.
+// The same with shared positions, in units of cost, and how many tiles the run has.
 __device__ void locate_shared(const LatentParams& p, int pair, int pairs, Shared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int common = min(max(*p.shared_len, 0), p.max_shared);
     const int per = (p.batch + kThreads) / kThreads;  // of the batch's rows and row 0
     const int from = min(tid * per, p.batch + 1), to = min(from + per, p.batch + 1);
     int mine = 0;
+    if (tid == 0) sh.tiles = 0;
 #pragma unroll 4
     for (int i = from; i < to; ++i) {
         const Row row(p, i, common);
-        mine += row.tiles() * row.groups();
+        mine += row.cost() * row.groups();
     }
     int upto = mine;
 #pragma unroll
@@ -250,23 +263,29 @@ __device__ void locate_shared(const LatentParams& p, int pair, int pairs, Shared
         total += x;
     }
     before += upto - mine;
-    const int begin = Runs(total, pairs).start(pair);
+    const Runs runs(total, pairs);
+    const int begin = runs.start(pair), end = begin + runs.count(pair);
     if (tid == 0) {
         sh.total = total;
         sh.begin = begin;
         sh.common = common;
     }
-    if (begin >= before && begin < before + mine) {
-        int at = before, i = from;
-        while (true) {
+    // Every thread that has rows in the run counts their tiles.
+    if (begin < before + mine && end > before) {
+        int at = before, tiles = 0;
+        for (int i = from; i < to && at < end; ++i) {
             const Row row(p, i, common);
-            const int n = row.tiles() * row.groups();
-            if (begin < at + n) break;
+            const int cost = row.cost(), n = cost * row.groups();
+            if (begin >= at && begin < at + n) {
+                sh.row = i;
+                sh.tile = begin - at;
+            }
+            // Units of a group up to x, of which the first kBegin are no tiles.
+            const auto tiles_to = [&](int x) { return x / cost * (cost - kBegin) + max(x % cost - kBegin, 0); };
+            if (n > 0) tiles += tiles_to(min(max(end - at, 0), n)) - tiles_to(min(max(begin - at, 0), n));
             at += n;
-            ++i;
         }
-        sh.row = i;
-        sh.tile = begin - at;
+        if (tiles > 0) atomicAdd(&sh.tiles, tiles);
     }
     __syncthreads();
 }
@@ -275,51 +294,60 @@ __device__ void locate_shared(const LatentParams& p, int pair, int pairs, Shared
 struct Segment {
     int row, group, first, last, tiles, length;
     int all, base, from;  // of a Row
+    int start;            // the group's first unit of cost
 };
 template <bool kShared>
 struct Walk {
     const LatentParams& p;
     int left, row, group, first, groups, length;
-    int common, at;  // shared positions; the next tile among all
+    int common, at;  // shared positions; the next unit of cost among all
+    int tiles;       // of the whole run
 
     __device__ __forceinline__ Walk(const LatentParams& p, const Shared& sh, int pair, int pairs)
         : p(p), left(Runs(sh.total, pairs).count(pair)), row(sh.row), groups(groups_of(p)), length(sh.length) {
         if constexpr (kShared) {
             common = sh.common;
             at = sh.begin;
+            tiles = sh.tiles;
             if (left <= 0) return;
-            const int tiles = Row(p, row, common).tiles();
-            group = sh.tile / tiles;
-            first = sh.tile - group * tiles;
+            const int cost = Row(p, row, common).cost();
+            group = sh.tile / cost;
+            first = sh.tile - group * cost;  // in units of cost
         } else {
-            const int tiles = tiles_of(length);
-            group = sh.tile / tiles;
-            first = sh.tile - group * tiles;
+            tiles = left;
+            const int each = tiles_of(length);
+            group = sh.tile / each;
+            first = sh.tile - group * each;
         }
     }
     __device__ __forceinline__ bool next(Segment& s) {
         if (left <= 0) return false;
         if constexpr (kShared) {
-            Row r(p, row, common);
-            while (r.tiles() == 0 && row < p.batch) r = Row(p, ++row, common);
-            if (r.tiles() == 0) return false;
-            s.row = row;
-            s.group = group;
-            s.length = r.length;
-            s.all = r.all;
-            s.base = r.base;
-            s.from = r.from;
-            s.tiles = r.tiles();
-            s.first = first;
-            s.last = min(s.tiles, first + left);
-            left -= s.last - s.first;
-            at += s.last - s.first;
-            first = 0;
-            if (++group == r.groups()) {
-                group = 0;
-                ++row;
+            while (left > 0) {
+                Row r(p, row, common);
+                while (r.tiles() == 0 && row < p.batch) r = Row(p, ++row, common);
+                if (r.tiles() == 0) return false;
+                const int past = min(r.cost(), first + left);
+                s.row = row;
+                s.group = group;
+                s.length = r.length;
+                s.all = r.all;
+                s.base = r.base;
+                s.from = r.from;
+                s.tiles = r.tiles();
+                s.first = max(first - kBegin, 0);
+                s.last = past - kBegin;
+                s.start = at - first;
+                left -= past - first;
+                at += past - first;
+                first = 0;
+                if (++group == r.groups()) {
+                    group = 0;
+                    ++row;
+                }
+                if (s.last > s.first) return true;
             }
-            return true;
+            return false;
         }
         s.row = row;
         s.group = group;
@@ -394,7 +422,7 @@ struct SlotAhead {
     bool more;
 
     __device__ __forceinline__ SlotAhead(const LatentParams& p, Walk<kShared>& walk, Segment& s, int at)
-        : p(p), walk(walk), s(s), at(at), tiles(walk.left), more(walk.next(s)) {
+        : p(p), walk(walk), s(s), at(at), tiles(walk.tiles), more(walk.next(s)) {
         tile = s.first;
         fetch(slot[0]);
         fetch(slot[1]);
@@ -712,9 +740,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // All of them at once: the join goes by them whatever becomes of the sums.
             Walk<kShared> ahead = walk;
             while (ahead.next(s))
-                if (s.first == 0)  // (`at` is past this piece)
+                if (s.first == 0)
                     parts_of(p, s.row, s.group) =
-                        make_int2(pair, Runs(sh.total, pairs).of(ahead.at - s.last + s.tiles - 1) - pair + 1);
+                        make_int2(pair, Runs(sh.total, pairs).of(s.start + kBegin + s.tiles - 1) - pair + 1);
         }
         if (!kShared && lane == 0 && rank == 0 && pair > 0) {
             const Runs runs(sh.total, pairs);
@@ -802,7 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 7) {
         // Tells the first block of each group of pieces that landed here,
         // those of keys and of values as they come.
-        const int tiles = walk.left;
+        const int tiles = walk.tiles;
         int keys_done = 0, values_done = 0, kg = 0, vg = 0;
         const bool more = walk.next(s);
         int tile = s.first;
@@ -865,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // while that runs, the keys' last third of tile n + 1 lands and the
             // softmax of tile n is done (taken as their operands came instead,
             // pages were 2 to 4 % slower).
-            const int tiles = walk.left;
+            const int tiles = walk.tiles;
             int n = 0, segment = 0;
             bool add = false;  // whether the sums of tile n - 1 are added to
             int left = 0;      // its slots, up to the row's end
@@ -1362,7 +1390,7 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const Att
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention shared memory");
     const auto tiles_in = [](int64_t n) { return n > kTile ? (n + kTile - 1) / kTile : 1; };
     int64_t tiles = p.batch * groups_in(each) * tiles_in(p.max_len);
-    if (shared) tiles += groups_in(all) * tiles_in(p.max_shared);
+    if (shared) tiles += groups_in(all) * tiles_in(p.max_shared) + kBegin * all_groups(p.batch, each);
     if (tiles > INT32_MAX) return TOPK_EINVAL;
     const int64_t most = device.sms / 2 < kMaxPairs ? device.sms / 2 : kMaxPairs;
     const int pairs = static_cast<int>(tiles < most ? tiles : most);
