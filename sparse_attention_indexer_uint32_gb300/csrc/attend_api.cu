@@ -169,12 +169,11 @@ topk_status_t topk_index_append(const void* rows, int64_t row_stride, int32_t to
         misaligned(norm_weight_or_null, 16) || misaligned(norm_bias_or_null, 16) || misaligned(cos_sin_or_null, 16) ||
         misaligned(positions_or_null, 4) || misaligned(slots, 4))
         return TOPK_EALIGN;
-    AttendDevice device;
-    const topk_status_t st = attend_device(&device);
+    const topk_status_t st = api_check_device();
     if (st != TOPK_OK || tokens == 0) return st;
     IndexAppendParams p = {rows,          row_stride,        tokens, norm_weight_or_null, norm_bias_or_null, eps, cos_sin_or_null,
                            num_positions, positions_or_null, interleaved != 0, rope_last != 0, slots, cache, slot_stride, num_slots};
-    const cudaError_t e = launch_index_append(p, dtype, device, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_index_append(p, dtype, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "index append launch");
 }
 

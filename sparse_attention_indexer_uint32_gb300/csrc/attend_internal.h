@@ -145,7 +145,7 @@ struct IndexAppendParams {
     int64_t slot_stride;
     int32_t num_slots;
 };
-cudaError_t launch_index_append(const IndexAppendParams& p, topk_dtype_t dtype, const AttendDevice& device, cudaStream_t stream);
+cudaError_t launch_index_append(const IndexAppendParams& p, topk_dtype_t dtype, cudaStream_t stream);
 
 struct IndexScoresParams {
     const void* q;
