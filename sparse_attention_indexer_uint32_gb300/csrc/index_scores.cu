@@ -47,16 +47,20 @@ constexpr int kHalfKeys = kTile * 128;                     // 64 values of a til
 constexpr int kKeyBytes = 2 * kHalfKeys, kQueryBytes = 2 * kAllColumns * 128, kWeightBytes = kAllColumns * 4;
 constexpr int kTileBytes = kQueryBytes + 3 * kKeyBytes;  // queries and keys
 
+struct Span {  // of a request
+    int32_t from, n, length;
+};
 struct Shared {
     uint64_t query_full[2], query_empty[2], weight_full[2];
     uint64_t key_full[kStages], key_empty[kStages], mask_full[kMasks];
     uint64_t score_full[kBuffers], score_empty[kBuffers], end;
-    int64_t total, begin;  // tiles of the whole call; the first of this block's run
+    int64_t total, begin;  // units of cost of the whole call; the first of this block's run
     union {
         int64_t scan[kThreads / 32];  // until the run is found
         uint32_t mask[kMasks][4];
     };
-    int32_t row, chunk, tile;  // where the run begins
+    int32_t row, chunk, unit;  // where the run begins
+    Span span;                 // of that row
     uint32_t tmem, gave_up;
 };
 // The structure lies before or behind the tiles, in what their alignment leaves.
@@ -72,6 +76,7 @@ struct ScoreMaps {
 struct Layout {
     int32_t padded;      // heads, a power of two
     int32_t log2_queries;  // of a chunk
+    int32_t begin_cost;    // of a chunk, in tiles
     int32_t product_queries;
     int32_t places;      // chunks in shared memory: 2 of one product or 1 of two
     int32_t place_columns;  // of each
@@ -81,10 +86,10 @@ struct Layout {
     uint32_t instruction;  // without N
 };
 
-// A request's queries and what its tiles are.
-struct Request {
-    int from, n, length;
-
+// A request's queries and what its tiles are.  Runs are cut by cost: a chunk's
+// tiles and begin_cost more, for the change of queries in shared memory.
+struct Request : Span {
+    __device__ __forceinline__ Request(const Span& x) : Span(x) {}
     __device__ __forceinline__ Request(const IndexScoresParams& p, int b) {
         length = min(max(p.seq_lens[b], 0), p.max_len);
         if (p.cu_q) {
@@ -95,36 +100,36 @@ struct Request {
             from = b * n;
         }
     }
-    __device__ __forceinline__ int chunks(int log2) const { return (n + (1 << log2) - 1) >> log2; }
-    // Positions that the last query of a chunk sees.
-    __device__ __forceinline__ int seen(int chunk, int log2) const {
-        return max(length - n + min(n, (chunk + 1) << log2), 0);
+    __device__ __forceinline__ int chunks(const Layout& a) const {
+        return (n + (1 << a.log2_queries) - 1) >> a.log2_queries;
     }
-    __device__ __forceinline__ int tiles(int chunk, int log2) const {
-        return static_cast<int>((static_cast<uint32_t>(seen(chunk, log2)) + kTile - 1) / kTile);
+    __device__ __forceinline__ int tiles(const Layout& a, int chunk) const {
+        // Positions that the chunk's last query sees.
+        const int seen = max(length - n + min(n, (chunk + 1) << a.log2_queries), 0);
+        return static_cast<int>((static_cast<uint32_t>(seen) + kTile - 1) / kTile);
     }
-    // Tiles of the chunks before `chunk`: whole ones, each sees 2^log2 more
+    __device__ __forceinline__ int cost(const Layout& a, int chunk) const {
+        const int x = tiles(a, chunk);
+        return x > 0 ? x + a.begin_cost : 0;
+    }
+    // Cost of the chunks before `chunk`: whole ones, each sees 2^log2 more
     // than the one before, and 2^log2 divides a tile.
-    __device__ __forceinline__ int64_t before(int chunk, int log2) const {
-        const int step = 1 << log2;
-        int64_t at = static_cast<int64_t>(length) - n + step + kTile - 1;
-        int first = 0;
-        if (at < 0) {
-            first = static_cast<int>((-at + step - 1) >> log2);
-            at += static_cast<int64_t>(first) << log2;
-        }
-        if (chunk <= first) return 0;
+    __device__ __forceinline__ int64_t before(const Layout& a, int chunk) const {
+        const int log2 = a.log2_queries, step = 1 << log2;
+        const int blind = n > length ? (n - length) >> log2 : 0;  // chunks that see nothing
+        if (chunk <= blind) return 0;
+        const int64_t at = static_cast<int64_t>(length) - n + step + kTile - 1 + (static_cast<int64_t>(blind) << log2);
         const int log2_tile = 7 - log2;  // chunks of a tile's length
         const auto sum = [&](int64_t x) {  // of i >> log2_tile over i < x
             const int64_t q = x >> log2_tile;
             return ((q * (q - 1) / 2) << log2_tile) + (x & ((1 << log2_tile) - 1)) * q;
         };
-        const int64_t a = at >> log2;
-        return sum(a + chunk - first) - sum(a);
+        const int64_t i = at >> log2, many = chunk - blind;
+        return sum(i + many) - sum(i) + many * a.begin_cost;
     }
-    __device__ __forceinline__ int64_t all(int log2) const {
-        const int c = chunks(log2);
-        return c > 0 ? before(c - 1, log2) + tiles(c - 1, log2) : 0;
+    __device__ __forceinline__ int64_t all(const Layout& a) const {
+        const int c = chunks(a);
+        return c > 0 ? before(a, c - 1) + cost(a, c - 1) : 0;
     }
 };
 
@@ -137,13 +142,13 @@ __device__ __forceinline__ int64_t run_start(int64_t total, int n, int i) {
     return total / n * i + min(static_cast<int64_t>(i), total % n);
 }
 
-// All threads: the tiles of the call, and where this block's run begins.
+// All threads: the cost of the call, and where this block's run begins.
 __device__ void locate(const IndexScoresParams& p, const Layout& a, Shared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int from = min(tid * per, p.batch), to = min(from + per, p.batch);
     int64_t mine = 0;
-    for (int b = from; b < to; ++b) mine += Request(p, b).all(a.log2_queries);
+    for (int b = from; b < to; ++b) mine += Request(p, b).all(a);
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -169,23 +174,24 @@ __device__ void locate(const IndexScoresParams& p, const Layout& a, Shared& sh) 
         int64_t at = begin - before;
         int b = from;
         while (true) {
-            const int64_t n = Request(p, b).all(a.log2_queries);
+            const int64_t n = Request(p, b).all(a);
             if (at < n) break;
             at -= n;
             ++b;
         }
         const Request r(p, b);
-        int lo = 0, hi = r.chunks(a.log2_queries) - 1;  // the last chunk with before <= at
+        int lo = 0, hi = r.chunks(a) - 1;  // the last chunk with before <= at
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (r.before(mid, a.log2_queries) <= at)
+            if (r.before(a, mid) <= at)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         sh.row = b;
         sh.chunk = lo;
-        sh.tile = static_cast<int>(at - r.before(lo, a.log2_queries));
+        sh.unit = static_cast<int>(at - r.before(a, lo));
+        sh.span = r;
     }
     __syncthreads();
 }
@@ -198,39 +204,36 @@ struct Segment {
 };
 struct Walk {
     const IndexScoresParams& p;
-    int log2;
+    const Layout& a;
     int64_t left;
-    int row, chunk, first;
+    int row, chunk, first;  // (first: in units of cost)
+    Request r;              // of the row
 
     __device__ __forceinline__ Walk(const IndexScoresParams& p, const Layout& a, const Shared& sh)
-        : p(p), log2(a.log2_queries), row(sh.row), chunk(sh.chunk), first(sh.tile) {
+        : p(p), a(a), row(sh.row), chunk(sh.chunk), first(sh.unit), r(sh.span) {
         left = run_start(sh.total, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x) + 1) - sh.begin;
     }
     __device__ __forceinline__ bool next(Segment& s) {
         while (left > 0 && row < p.batch) {
-            const Request r(p, row);
-            const int chunks = r.chunks(log2);
-            // Chunks that see nothing come before those that see something.
-            while (chunk < chunks) {
-                const int tiles = r.tiles(chunk, log2), at = chunk << log2;
+            const int chunks = r.chunks(a);
+            while (chunk < chunks && left > 0) {
+                const int cost = r.cost(a, chunk), at = chunk << a.log2_queries;
+                const int past = static_cast<int>(min(static_cast<int64_t>(cost), first + left));
+                s.first = max(first - a.begin_cost, 0);
+                s.last = past - a.begin_cost;
+                left -= past - first;
+                first = 0;
                 ++chunk;
-                if (first >= tiles) {
-                    first = 0;
-                    continue;
-                }
+                if (s.last <= s.first) continue;
                 s.row = row;
                 s.query = r.from + at;
-                s.queries = min(r.n - at, 1 << log2);
-                s.first = first;
-                s.last = static_cast<int>(min(static_cast<int64_t>(tiles), first + left));
+                s.queries = min(r.n - at, 1 << a.log2_queries);
                 s.seen = r.length - (r.n - 1 - at);
                 s.length = r.length;
-                left -= s.last - s.first;
-                first = 0;
                 return true;
             }
             chunk = 0;
-            ++row;
+            if (++row < p.batch && left > 0) r = Request(p, row);
         }
         return false;
     }
@@ -297,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&sh.end, 1);
         ptx::fence_mbarrier_init();
     }
+    if (warp == kKeyWarp && lane < 2) tc::prefetch_map(lane == 0 ? &maps.q : &maps.cache);
     if (warp == kProductWarp) tc::alloc<1>(ptx::smem_addr(&sh.tmem), 2 * kColumns);
     ptx::grid_dependency_wait();
     tc::fence_before();
@@ -550,6 +554,7 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     a.places = small ? 2 : 1;
     a.log2_queries = small ? log2 : log2 + 1;
     a.place_columns = a.padded << a.log2_queries;
+    a.begin_cost = small ? 0 : 2;
     a.buffers = a.padded << log2 <= kColumns / 2 ? kBuffers : 2;
     a.stages = (kTileBytes - a.places * a.place_columns * 256) / kKeyBytes;
     if (a.stages > kStages) a.stages = kStages;
@@ -577,7 +582,7 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     cudaError_t e = allow_shared(kernel, kSmem, prepared[full][log2_heads - 4][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "index scores shared memory");
     const int64_t chunks = ((static_cast<int64_t>(p.total_q) + (1 << a.log2_queries) - 1) >> a.log2_queries) + p.batch;
-    const int64_t tiles = chunks * ((p.max_len + int64_t{kTile} - 1) / kTile);
+    const int64_t tiles = chunks * ((p.max_len + int64_t{kTile} - 1) / kTile);  // at most
     const unsigned blocks = static_cast<unsigned>(tiles < device.sms ? tiles : device.sms);
     e = launch_early(kernel, dim3(blocks), kThreads, kSmem, stream, p, maps, a, device.flags);
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "index scores launch");
