@@ -67,6 +67,7 @@ _DTYPES = {torch.bfloat16: _lib.TOPK_BF16, torch.float16: _lib.TOPK_FP16}
 _LATENT, _ROPE, _NOPE, _VALUE = _lib.TOPK_LATENT_DIM, _lib.TOPK_ROPE_DIM, _lib.TOPK_NOPE_DIM, _lib.TOPK_VALUE_DIM
 _WIDTH = _LATENT + _ROPE
 _INDEX = _lib.TOPK_INDEX_DIM
+_INDEX_ROW, _VALUES_ROW = (_INDEX,), (_LATENT,)
 _I32, _F32 = torch.int32, torch.float32
 _c = _lib.library()
 
@@ -292,23 +293,41 @@ def index_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     """Runs ``topk_index_append``: the indexer's keys ``rows`` [tokens, 128] to ``slots`` of their ``cache``
     [num_slots, 128], layer-normed by ``norm_weight`` and ``norm_bias`` [128] and, in their first 64 values (the last
     with ``rope_last``), rotated by ``cos_sin`` (as in :func:`cache_append`) at ``positions``, where these are given."""
-    gpu, dtype, shape, places = cache.get_device(), cache.dtype, rows.shape, cache.shape
-    code, tokens, positions_n = _DTYPES.get(dtype), shape[0] if shape else 0, 0 if cos_sin is None else cos_sin.shape[0]
-    if not (gpu >= 0 and code is not None and rows.dtype is dtype and rows.get_device() == gpu and len(shape) == 2
-            and len(places) == 2 and shape[1] == _INDEX == places[1] and rows.stride(1) == 1 == cache.stride(1)
-            and _line(slots, tokens, gpu) and (positions is None or _line(positions, tokens, gpu))
-            and (norm_weight is None or _is(norm_weight, dtype, gpu, (_INDEX,)))
-            and (norm_bias is None or _is(norm_bias, dtype, gpu, (_INDEX,)))
-            and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))
-            and not (_grad_enabled() and (_any_grad(rows, cache, norm_weight, norm_bias)
-                                          or (cos_sin is not None and cos_sin.requires_grad)))):
+    gpu, dtype, shape, places, steps, slot_steps = (cache.get_device(), cache.dtype, rows.shape, cache.shape, rows.stride(),
+                                                    cache.stride())
+    code, tokens, positions_n = _DTYPES.get(dtype), shape[0] if shape else 0, 0
+    line = (tokens,)
+    right = (gpu >= 0 and code is not None and rows.dtype is dtype and rows.get_device() == gpu and len(shape) == 2
+             and len(places) == 2 and shape[1] == _INDEX == places[1] and steps[1] == 1 == slot_steps[1]
+             and slots.dtype is _I32 and slots.shape == line and slots.get_device() == gpu and slots.is_contiguous())
+    if positions is not None:
+        right = (right and positions.dtype is _I32 and positions.shape == line and positions.get_device() == gpu
+                 and positions.is_contiguous())
+        positions_at = positions.data_ptr()
+    else:
+        positions_at = None
+    weight_at = bias_at = turns_at = None
+    if norm_weight is not None:
+        right = (right and norm_weight.dtype is dtype and norm_weight.shape == _INDEX_ROW and norm_weight.get_device() == gpu
+                 and norm_weight.is_contiguous())
+        weight_at = norm_weight.data_ptr()
+    if norm_bias is not None:
+        right = (right and norm_bias.dtype is dtype and norm_bias.shape == _INDEX_ROW and norm_bias.get_device() == gpu
+                 and norm_bias.is_contiguous())
+        bias_at = norm_bias.data_ptr()
+    if cos_sin is not None:
+        turns = cos_sin.shape
+        positions_n = turns[0] if turns else 0
+        right = (right and cos_sin.dtype is _F32 and len(turns) == 2 and turns[1] == _ROPE and cos_sin.get_device() == gpu
+                 and cos_sin.is_contiguous())
+        turns_at = cos_sin.data_ptr()
+    if not right or (_grad_enabled() and (_any_grad(rows, cache, norm_weight, norm_bias)
+                                          or (cos_sin is not None and cos_sin.requires_grad))):
         _check_index_append(rows, slots, cache, norm_weight, norm_bias, cos_sin, positions)
     status = (_c.topk_index_append if _current_device() == gpu else _there(_c.topk_index_append, gpu))(
-        rows.data_ptr(), rows.stride(0) if tokens > 1 else _INDEX, tokens,
-        None if norm_weight is None else norm_weight.data_ptr(), None if norm_bias is None else norm_bias.data_ptr(), eps,
-        None if cos_sin is None else cos_sin.data_ptr(), positions_n, None if positions is None else positions.data_ptr(),
-        interleaved, rope_last, slots.data_ptr(), cache.data_ptr(), cache.stride(0) if places[0] > 1 else _INDEX, places[0],
-        code, _lib.stream_handle(stream, gpu))
+        rows.data_ptr(), steps[0] if tokens > 1 else _INDEX, tokens, weight_at, bias_at, eps, turns_at, positions_n,
+        positions_at, interleaved, rope_last, slots.data_ptr(), cache.data_ptr(), slot_steps[0] if places[0] > 1 else _INDEX,
+        places[0], code, _lib.stream_handle(stream, gpu))
     if status:
         _lib.check("topk_index_append", status)
 
@@ -351,32 +370,40 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, cache: torch.Tensor, se
     max_seq_len rounded up to a multiple of 4), of which each query's row is written up to what it sees: the last
     query of a request ``seq_lens`` positions, each one before it one less."""
     gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
+    w_steps, slot_steps, table_steps = weights.stride(), cache.stride(), page_table.stride()
     code = _DTYPES.get(dtype)
-    most = min(listed[1] * page_size, 2 ** 31 - 1) if max_seq_len is None and len(listed) == 2 else max_seq_len
-    if not (gpu >= 0 and code is not None and len(shape) == 3 and len(listed) == 2 and shape[2] == _INDEX
-            and steps[2] == 1 and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
-            and places[1] == _INDEX and cache.stride(1) == 1 and weights.dtype is _F32 and weights.get_device() == gpu
-            and weights.shape == shape[:2] and (shape[1] <= 1 or weights.stride(1) == 1)
-            and page_table.dtype is _I32 and page_table.get_device() == gpu
-            and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, listed[0], gpu)
-            and (_line(cu_q, listed[0] + 1, gpu) if cu_q is not None else listed[0] > 0 and shape[0] % listed[0] == 0)
-            and most <= listed[1] * page_size
-            and (out is None or (out.dtype is _F32 and out.get_device() == gpu and out.dim() == 2
-                                 and out.shape[0] == shape[0] and out.shape[1] >= most
-                                 and (out.shape[1] <= 1 or out.stride(1) == 1)))
-            and not (_grad_enabled() and _any_grad(q, weights, cache, out))):
+    right = (gpu >= 0 and code is not None and len(shape) == 3 and len(listed) == 2 and shape[2] == _INDEX
+             and steps[2] == 1 and cache.dtype is dtype and cache.get_device() == gpu and len(places) == 2
+             and places[1] == _INDEX and slot_steps[1] == 1 and weights.dtype is _F32 and weights.get_device() == gpu
+             and weights.shape == shape[:2] and (w_steps[1] == 1 or shape[1] <= 1)
+             and page_table.dtype is _I32 and page_table.get_device() == gpu
+             and (table_steps[1] == 1 or listed[1] <= 1) and seq_lens.dtype is _I32 and seq_lens.get_device() == gpu
+             and seq_lens.shape == listed[:1] and seq_lens.is_contiguous()
+             and (_line(cu_q, listed[0] + 1, gpu) if cu_q is not None else listed[0] > 0 and shape[0] % listed[0] == 0))
+    if right:
+        most = listed[1] * page_size
+        if max_seq_len is None:
+            most = min(most, 2 ** 31 - 1)
+        else:
+            right, most = max_seq_len <= most, max_seq_len
+    if right and out is not None:
+        sides, out_steps = out.shape, out.stride()
+        right = (out.dtype is _F32 and out.get_device() == gpu and len(sides) == 2 and sides[0] == shape[0]
+                 and sides[1] >= most and (out_steps[1] == 1 or sides[1] <= 1))
+    if not right or (_grad_enabled() and _any_grad(q, weights, cache, out)):
         _check_index_scores(q, weights, cache, seq_lens, page_table, page_size, cu_q, max_seq_len, out)
     total, heads, _ = shape
     batch, slots = listed[0], places[0]
     if out is None:
         out = _empty((total, (most + 3) // 4 * 4), _F32, q.device, stream)
+        out_steps = out.stride()
     many = total > 1
     status = (_c.topk_index_scores if _current_device() == gpu else _there(_c.topk_index_scores, gpu))(
         q.data_ptr(), steps[0] if many else _INDEX, steps[1] if heads > 1 else _INDEX, weights.data_ptr(),
-        weights.stride(0) if many else heads, cache.data_ptr(), cache.stride(0) if slots > 1 else _INDEX, slots,
-        seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else listed[1], page_size, most,
+        w_steps[0] if many else heads, cache.data_ptr(), slot_steps[0] if slots > 1 else _INDEX, slots,
+        seq_lens.data_ptr(), page_table.data_ptr(), table_steps[0] if batch > 1 else listed[1], page_size, most,
         None if cu_q is None else cu_q.data_ptr(), batch, total, heads, code, out.data_ptr(),
-        out.stride(0) if many else out.shape[1], _lib.stream_handle(stream, gpu))
+        out_steps[0] if many else most, _lib.stream_handle(stream, gpu))
     if status:
         _lib.check("topk_index_scores", status)
     return out
@@ -520,12 +547,18 @@ def attend_shared(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     ``page_table``.  ``seq_lens`` counts both.  Returns ``(out [batch, queries, heads, 512], lse [batch, queries,
     heads], workspace)``."""
     gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
-    code, common = _DTYPES.get(dtype), shared_pages.numel()
-    if not (code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
-            and shape[3] == _WIDTH and steps[3] == 1 and page_table.dtype is _I32 and page_table.get_device() == gpu
-            and (listed[1] <= 1 or page_table.stride(1) == 1) and _line(seq_lens, shape[0], gpu)
-            and _line(shared_pages, common, gpu) and _line(shared_len, 1, gpu)
-            and _fits(q, cache, places, out, lse, gpu, dtype, (shape[0], shape[1], shape[2]))):
+    code, common, slot_steps, table_steps = _DTYPES.get(dtype), shared_pages.numel(), cache.stride(), page_table.stride()
+    right = (gpu >= 0 and code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]
+             and shape[3] == _WIDTH and steps[3] == 1 and cache.dtype is dtype and cache.get_device() == gpu
+             and len(places) == 2 and places[1] == _WIDTH and slot_steps[1] == 1 and page_table.dtype is _I32
+             and page_table.get_device() == gpu and (table_steps[1] == 1 or listed[1] <= 1)
+             and seq_lens.dtype is _I32 and seq_lens.get_device() == gpu and seq_lens.shape == listed[:1]
+             and seq_lens.is_contiguous() and _line(shared_pages, common, gpu) and _line(shared_len, 1, gpu))
+    if right and out is not None:
+        right = out.dtype is dtype and out.get_device() == gpu and out.shape == shape[:3] + _VALUES_ROW and out.is_contiguous()
+    if right and lse is not None:
+        right = lse.dtype is _F32 and lse.get_device() == gpu and lse.shape == shape[:3] and lse.is_contiguous()
+    if not right or (_grad_enabled() and _any_grad(q, cache, out, lse)):
         if q.dim() != 4 or page_table.dim() != 2 or page_table.shape[0] != q.shape[0]:
             raise ValueError(f"q and page_table must be [batch, queries, heads, ..] and [batch, pages]: got "
                              f"{tuple(q.shape)} and {tuple(page_table.shape)}")
@@ -550,8 +583,8 @@ def attend_shared(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     slots = places[0]
     status = (_c.topk_attend_shared if _current_device() == gpu else _there(_c.topk_attend_shared, gpu))(
         q.data_ptr(), steps[0] if batch > 1 else _WIDTH, steps[1] if queries > 1 else _WIDTH,
-        steps[2] if heads > 1 else _WIDTH, cache.data_ptr(), cache.stride(0) if slots > 1 else _WIDTH, slots,
-        seq_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else listed[1],
+        steps[2] if heads > 1 else _WIDTH, cache.data_ptr(), slot_steps[0] if slots > 1 else _WIDTH, slots,
+        seq_lens.data_ptr(), page_table.data_ptr(), table_steps[0] if batch > 1 else listed[1],
         shared_pages.data_ptr(), common, shared_len.data_ptr(), page_size, max_seq_len, batch, queries, heads, scale, code,
         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), room, _lib.stream_handle(stream, gpu))
     if status:
