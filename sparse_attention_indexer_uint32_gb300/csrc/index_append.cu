@@ -5,7 +5,12 @@
 // values in fp32 (the mean first, then the squares of what is left: no
 // difference of two large sums), then the rotation of 64 of them by the angle
 // of the token's position, and one rounding.  Half a warp holds a key, eight
-// values (16 bytes) a lane, so a key is read once and written once.
+// values (16 bytes) a lane, so a key is read once and written once: 256 + 256 +
+// 256 bytes with its cosines and sines, bound by memory at large counts and by the
+// call at small ones.  65536 keys take 12.6 us, 4.0 TB/s (59 % of the measured
+// copy rate; two dependent reads, position and angles, in each of 5 rounds of
+// blocks).  Four keys a half warp at once took 15.7 us, the registers held fewer
+// keys on an SM; 64 keys 7.7 to 8.4 us a call, nearly all of it the host's.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -20,7 +25,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLanes = kIndex / 8;            // lanes of a key
 constexpr int kTurnLanes = kRope / 8;         // of them, those with rotary values
-constexpr int kKeys = kThreads / kLanes;      // keys of a block at a time
+constexpr int kKeys = kThreads / kLanes;      // keys of a block
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) index_append_kernel(const IndexAppendParams p) {
