@@ -442,8 +442,8 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
  * and the rest are as in topk_attend_paged: seq_lens counts the shared
  * positions, and a request shorter than shared_len sees as many as it has.
  *   shared_pages      device int32[num_shared_pages] (may be a row of the
- *                     page table); the entries of the rows below shared_len /
- *                     page_size are not read.
+ *                     page table); the rows' entries below shared_len /
+ *                     page_size are not used, whatever they hold.
  *   shared_len        device int32[1]; values outside [0,
  *                     min(num_shared_pages * page_size, max_seq_len)] are
  *                     clamped to it.  It may end inside a page.
@@ -506,9 +506,9 @@ topk_status_t topk_attend_prompt(const void* q, int64_t q_token_stride, int64_t 
  * bounded device wait of some call since the last clearing gave up and that
  * call's output is void (a wait may span the work on one row or piece: calls
  * that take seconds need a higher wait_limit_us).  clear != 0 resets the word
- * afterwards.  The first
- * call of an attention entry point on a device looks up the word's address;
- * make it before any stream capture.
+ * afterwards.  topk_index_scores notes its waits here too.  The first call of an
+ * attention entry point or of topk_index_scores on a device looks up the word's
+ * address; make it before any stream capture.
  */
 topk_status_t topk_read_attend_flags(uint32_t* flags_host, int32_t clear, topk_stream_t stream);
 

@@ -162,6 +162,39 @@ def test_what_is_not_seen_may_be_anything(api, dtype, page):
     x.check(out, lse)
 
 
+@pytest.mark.parametrize("page,shared", [(64, 192), (64, 200), (16, 208), (8, 100), (256, 300)])
+def test_entries_below_the_prompt_may_be_anything(api, page, shared):
+    x = Batch([shared + 70, shared + 1, shared, 500], shared, 1, 16, page, torch.bfloat16)
+    out, lse, _ = x.run(api)
+    x.check(out, lse)
+    below = shared // page
+    for value in (0, x.cache.shape[0] // page, 2 ** 31 - 1, -2 ** 31):
+        x.table[:, :below] = value
+        again, again_lse, _ = x.run(api)
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
+def test_no_positions_at_all(api):
+    x = Batch([5, 70], 64, 2, 16, 64, torch.bfloat16)
+    out, lse, _ = x.run(api, max_seq_len=0)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    x.shared.zero_()
+    x.lens.zero_()
+    out, lse, _ = x.run(api)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    x.pages = x.pages[:0]  # no list: nothing is shared, and every position is a row's own
+    x.lens.copy_(i32([5, 70]))
+    x.table = i32(torch.arange(4).reshape(2, 2))
+    x.shared.fill_(64)
+    out, lse, _ = x.run(api)
+    for r, n in enumerate((5, 70)):
+        for i in range(2):
+            kv = x.cache[x.table[r, 0] * 64:][: n - 1 + i]
+            o, l, ob, lb = attend(x.q[r, i], kv, kv[:, :LATENT], SCALE, x.q.dtype)
+            check(out[r, i], o, ob, f"request {r}, query {i}")
+            check(lse[r, i], l, lb, f"request {r}, query {i}")
+
+
 def test_large_scores_on_either_side(api):
     """The maximum in the prompt for some rows, far above or below what is their own."""
     x = Batch([600, 700, 640], 512, 1, 64, 64, torch.bfloat16)

@@ -251,6 +251,17 @@ def test_scores_offsets_that_are_not_in_order(api):
     run(api, randn(2, 9, 8, INDEX), randn(3, 9, 8, dtype=torch.float32), cache, i32([100, 128, 60, 77]), table, 16, cu=i32([-4, 3, 9, 5, 5]))
 
 
+@pytest.mark.parametrize("heads", [7, 16, 64])
+def test_scores_of_infinite_keys(api, heads):
+    """Infinities in a key go to its own score, and padding columns add nothing to them."""
+    cache, table = paged(1, 1, 4, 64, torch.bfloat16)
+    q, weights = randn(2, 2, heads, INDEX).abs(), randn(3, 2, heads, dtype=torch.float32).abs() + 1
+    at = table[0].long()[:, None].mul(64).add(torch.arange(64, device="cuda")).flatten()
+    cache[at[3], 7], cache[at[9], 8] = math.inf, -math.inf  # (no query value is zero)
+    out = run(api, q, weights, cache, i32([200]), table, 64)
+    assert (out[:, 3] == math.inf).all() and (out[:, 9] == 0).all() and not out[:, :199].isnan().any()
+
+
 def test_scores_replayed_with_other_lengths(api):
     page, b = 32, 3
     cache, table = paged(1, b, 40, page, torch.bfloat16)
