@@ -175,6 +175,21 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
+def _load_tensor_calls():
+    if not os.path.exists(os.path.join(_PKG, "_tensor_calls.so")):
+        raise ImportError(f"{_PKG}/_tensor_calls.so is missing: build it with "
+                          "`python -m sparse_attention_indexer_uint32_gb300.build`")
+    from . import _tensor_calls
+
+    _tensor_calls.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+        "topk_index_append", "topk_index_scores", "topk_attend_shared", "topk_attend_shared_workspace_bytes")))
+    return _tensor_calls
+
+
+#: The calls that are made straight from tensors (csrc/tensor_calls.cpp).
+tensor_calls = _load_tensor_calls()
+
+
 def library() -> ctypes.CDLL:
     return _lib
 

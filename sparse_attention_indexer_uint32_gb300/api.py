@@ -70,6 +70,7 @@ _INDEX = _lib.TOPK_INDEX_DIM
 _INDEX_ROW, _VALUES_ROW = (_INDEX,), (_LATENT,)
 _I32, _F32 = torch.int32, torch.float32
 _c = _lib.library()
+_calls = _lib.tensor_calls
 
 
 # The calls below look their arguments over twice at most: one condition that
@@ -78,7 +79,10 @@ _c = _lib.library()
 # where gradients are being recorded, tensors that require one are refused.  The
 # attention calls do not wait for their kernels: topk_read_attend_flags of the
 # binding says afterwards whether a bounded wait of one gave up, which makes
-# that call's output void.
+# that call's output void.  The index calls and attention behind a shared prompt
+# are tried by a compiled module first, which returns whether it made the call:
+# what it does not take (results to allocate, another GPU than the current one,
+# arguments that are wrong) goes on here.
 
 
 def _same(dtype: torch.dtype, device: torch.device, **tensors) -> None:
@@ -293,6 +297,9 @@ def index_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     """Runs ``topk_index_append``: the indexer's keys ``rows`` [tokens, 128] to ``slots`` of their ``cache``
     [num_slots, 128], layer-normed by ``norm_weight`` and ``norm_bias`` [128] and, in their first 64 values (the last
     with ``rope_last``), rotated by ``cos_sin`` (as in :func:`cache_append`) at ``positions``, where these are given."""
+    if _calls.index_append(rows, slots, cache, norm_weight, norm_bias, eps, cos_sin, positions, interleaved, rope_last,
+                           None if stream is None else _lib.stream_handle(stream, 0)):
+        return
     gpu, dtype, shape, places, steps, slot_steps = (cache.get_device(), cache.dtype, rows.shape, cache.shape, rows.stride(),
                                                     cache.stride())
     code, tokens, positions_n = _DTYPES.get(dtype), shape[0] if shape else 0, 0
@@ -369,6 +376,9 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, cache: torch.Tensor, se
     tokens (None: as many for each).  Returns ``out`` [tokens, max_seq_len or more] (float32; new memory has
     max_seq_len rounded up to a multiple of 4), of which each query's row is written up to what it sees: the last
     query of a request ``seq_lens`` positions, each one before it one less."""
+    if out is not None and _calls.index_scores(q, weights, cache, seq_lens, page_table, page_size, cu_q, max_seq_len, out,
+                                               None if stream is None else _lib.stream_handle(stream, 0)):
+        return out
     gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
     w_steps, slot_steps, table_steps = weights.stride(), cache.stride(), page_table.stride()
     code = _DTYPES.get(dtype)
@@ -546,6 +556,10 @@ def attend_shared(q: torch.Tensor, cache: torch.Tensor, seq_lens: torch.Tensor, 
     same, which are read once for all through ``shared_pages`` [pages]; those after them through each request's row of
     ``page_table``.  ``seq_lens`` counts both.  Returns ``(out [batch, queries, heads, 512], lse [batch, queries,
     heads], workspace)``."""
+    if workspace is not None and out is not None and _calls.attend_shared(
+            q, cache, seq_lens, page_table, shared_pages, shared_len, page_size, scale, max_seq_len, out, lse, workspace,
+            None if stream is None else _lib.stream_handle(stream, 0)):
+        return out, lse, workspace
     gpu, dtype, shape, listed, places, steps = q.get_device(), q.dtype, q.shape, page_table.shape, cache.shape, q.stride()
     code, common, slot_steps, table_steps = _DTYPES.get(dtype), shared_pages.numel(), cache.stride(), page_table.stride()
     right = (gpu >= 0 and code is not None and len(shape) == 4 and len(listed) == 2 and listed[0] == shape[0]

@@ -1,8 +1,10 @@
-"""Builds ``libtopkidx.so`` (the CUDA library) in-tree with nvcc for sm_103a.
+"""Builds ``libtopkidx.so`` (the CUDA library) in-tree with nvcc for sm_103a, and
+``_tensor_calls.so``, which makes some of its calls straight from tensors.
 
 Usage: ``python -m sparse_attention_indexer_uint32_gb300.build [--verbose]``.
-The translation units are compiled in parallel and linked into one shared
-library next to this file.  Nothing is installed into site-packages.
+The translation units are compiled in parallel, those of the library linked
+into one shared library next to this file.  Nothing is installed into
+site-packages.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libtopkidx.so")
+TENSOR_CALLS = os.path.join(PKG, "_tensor_calls.so")
 SOURCES = ["topk_kernels.cu", "topk_stream.cu", "topk_warp.cu", "topk_split.cu", "topkidx_api.cu", "topk_noalloc.cu",
            "serve_tables.cu", "serve_append.cu", "index_append.cu", "index_scores.cu",
            "attend_latent.cu", "attend_prompt.cu", "attend_api.cu"]
@@ -36,8 +40,28 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_tensor_calls() -> None:
+    """The CPython module, against the headers and libraries of the torch that imports it."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    include = os.path.join(root, "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = TENSOR_CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", include,
+           "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(cuda, "include"), os.path.join(CSRC, "tensor_calls.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for tensor_calls.cpp:\n{res.stderr}")
+    os.replace(tmp, TENSOR_CALLS)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    if not force and os.path.exists(LIBRARY) and os.path.getmtime(LIBRARY) >= _deps_mtime():
+    built = (LIBRARY, TENSOR_CALLS)
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in built):
         return LIBRARY
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -55,8 +79,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_tensor_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls.result()
     tmp = LIBRARY + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     res = subprocess.run(cmd, capture_output=True, text=True)

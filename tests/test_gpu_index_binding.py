@@ -90,3 +90,44 @@ def test_parameters_without_recording(api, off):
         api.index_append(rows, at, place, norm_weight=weight)
         got = api.index_scores(q, w, cache, i32([9, 9]), i32([[0], [0]]), 16)
     assert torch.equal(place, kept) and torch.equal(got[:, :9], want[:, :9])
+
+
+def test_right_calls_are_made_from_tensors(lib, api):
+    """The compiled module makes a right call and leaves a wrong one, or one elsewhere, to the checks."""
+    calls = lib.tensor_calls
+    rows, cache, slots = randn(4, 192)[:, :128], randn(64, 128), i32([0, 3, 5, 8])
+    turn, positions, w = torch.randn(10, 64, device="cuda"), i32([1, 2, 3, 0]), randn(128)
+    assert calls.index_append(rows, slots, cache, w, w, 1e-6, turn, positions, True, False, None) is True
+    assert calls.index_append(rows, slots, cache, None, None, 1, None, None, 0, 1, torch.cuda.current_stream().cuda_stream) is True
+    assert calls.index_append(rows, slots, cache, None, w, 1e-6, None, None, False, False, None) is False  # a bias alone
+    assert calls.index_append(rows, slots, cache, w, w, float("nan"), None, None, False, False, None) is False
+    assert calls.index_append(rows, slots, cache, w, w, "x", None, None, False, False, None) is False
+    assert calls.index_append(rows, slots.long(), cache, w, w, 1e-6, None, None, False, False, None) is False
+    assert calls.index_append(rows, slots[:3], cache, w, w, 1e-6, None, None, False, False, None) is False
+    assert calls.index_append(rows.half(), slots, cache, w, w, 1e-6, None, None, False, False, None) is False
+    assert calls.index_append(rows, slots.cpu(), cache, w, w, 1e-6, None, None, False, False, None) is False
+    assert calls.index_append(rows, slots, cache, w, w.float(), 1e-6, None, None, False, False, None) is False
+    assert calls.index_append(rows, slots, cache, w, w[::2], 1e-6, None, None, False, False, None) is False
+    assert calls.index_append(rows, slots, cache, w, w, 1e-6, turn[:, :32], positions, False, False, None) is False
+    parameter = torch.nn.Parameter(w.clone())
+    assert calls.index_append(rows, slots, cache, parameter, None, 1e-6, None, None, False, False, None) is False
+    with torch.no_grad():
+        assert calls.index_append(rows, slots, cache, parameter, None, 1e-6, None, None, False, False, None) is True
+    q, hw, lens, table, out = randn(4, 3, 128), torch.randn(4, 3, device="cuda"), i32([30, 16]), i32([[0, 1], [2, 3]]), torch.zeros(4, 32, device="cuda")
+    scores = lambda q=q, hw=hw, cache=cache, lens=lens, table=table, page=16, cu=None, most=None, out=out: calls.index_scores(  # noqa: E731
+        q, hw, cache, lens, table, page, cu, most, out, None)
+    assert scores() is True and scores(cu=i32([0, 1, 4]), most=20, out=torch.zeros(4, 20, device="cuda")) is True
+    for bad in (dict(page=0), dict(page=12), dict(page=1 << 70), dict(most=33), dict(most=-1), dict(out=out[:, :31]), dict(out=out.t()),
+                dict(cu=i32([0, 1])), dict(hw=hw.half()), dict(q=q[:3], hw=hw[:3], out=out[:3]), dict(lens=lens[:1]),
+                dict(table=table.float()), dict(out=None), dict(q=q.float()), dict(cache=cache[:, :64])):
+        assert scores(**bad) is False, bad
+    x, latent, pages, common = randn(2, 1, 3, 576), randn(64, 576), i32([3]), i32([16])
+    to, lse = randn(2, 1, 3, 512), torch.zeros(2, 1, 3, device="cuda")
+    room = torch.zeros(lib.topk_attend_shared_workspace_bytes(2, 1, 3), dtype=torch.uint8, device="cuda")
+    shared = lambda x=x, latent=latent, lens=lens, table=table, pages=pages, common=common, page=16, scale=0.1, most=None, to=to, lse=lse, room=room: (  # noqa: E731
+        calls.attend_shared(x, latent, lens, table, pages, common, page, scale, most, to, lse, room, None))
+    assert shared() is True and shared(most=20) is True and shared(pages=pages[:0]) is True
+    for bad in (dict(room=room[:-1]), dict(room=None), dict(lse=None), dict(lse=lse.double()), dict(to=to[:, :, :2]), dict(most=33),
+                dict(common=i32([1, 2])), dict(common=16), dict(pages=pages.long()), dict(scale=None), dict(page=24),
+                dict(x=x[..., :512]), dict(latent=latent.half()), dict(lens=i32([1, 2, 3]))):
+        assert shared(**bad) is False, bad
