@@ -1267,19 +1267,25 @@ template <bool kBf16, int kColumns>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_shared_kernel(const LatentParams p) {
     constexpr int kParts = 8 / kColumns;  // looked at a time
     constexpr int kPerUnit = kLatent / (4 * kColumns) / (kJoinThreads / 32);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int each = p.queries * p.heads, rows = p.batch * each;  // (at most 2^30)
+    const int units = (rows + 31) / 32 * kPerUnit;
+    int unit = static_cast<int>(blockIdx.x);
+    const auto row_at = [&] { return unit / kPerUnit * 32 + lane; };
+    const auto length_at = [&] { return row_at() < rows ? length_of(p, row_at() / each) : 0; };
+    // The lengths are there before the sums: the first kernel has read them when
+    // this one is placed.
+    const int common = min(max(*p.shared_len, 0), p.max_shared);
+    int length = length_at();
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int each = p.queries * p.heads, common = min(max(*p.shared_len, 0), p.max_shared);
-    const int64_t rows = static_cast<int64_t>(p.batch) * each, units = (rows + 31) / 32 * kPerUnit;
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t at = unit / kPerUnit * 32 + lane;
-        const int c = static_cast<int>(unit % kPerUnit * (kJoinThreads / 32) + warp) * kColumns;
+    for (; unit < units; unit += static_cast<int>(gridDim.x), length = length_at()) {
+        const int at = row_at(), c = (unit % kPerUnit * (kJoinThreads / 32) + warp) * kColumns;
         if (at >= rows) continue;
-        const int b = static_cast<int>(at / each), m = static_cast<int>(at - static_cast<int64_t>(b) * each);
-        const int prompt_group = static_cast<int>(at / kRows), group = m / kRows;
-        const int2 prompt = common > 0 ? parts_of(p, 0, prompt_group) : make_int2(0, 0);
-        const int2 own = length_of(p, b) > common ? parts_of(p, b + 1, group) : make_int2(0, 0);
+        const int b = at / each, m = at - b * each, prompt_group = at / kRows, group = m / kRows;
+        int2 prompt = parts_of(p, 0, prompt_group), own = parts_of(p, b + 1, group);
+        if (common <= 0) prompt = make_int2(0, 0);  // (not written)
+        if (length <= common) own = make_int2(0, 0);
         const int prompt_rows = part_rows_of(rows), own_rows = part_rows_of(each);
         float top = -INFINITY, l = 0.f;
         float4 o[kColumns] = {};
@@ -1294,7 +1300,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_shared_kernel(const Late
                     const int i = of_prompt ? i0 + k : i0 + k - prompt.y;
                     const int2 parts = of_prompt ? prompt : own;
                     const int n = of_prompt ? prompt_rows : own_rows;
-                    const int r = of_prompt ? static_cast<int>(at % kRows) : m % kRows;
+                    const int r = of_prompt ? at % kRows : m % kRows;
                     const float* part = parts.y > 1 ? run_of(p, 2 * (parts.x + i) + (i == 0 ? 1 : 0))
                                         : of_prompt ? whole_of(p, 0, prompt_group)
                                                     : whole_of(p, b + 1, group);
@@ -1331,7 +1337,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_shared_kernel(const Late
             w[2 * v] = tc::pack<kBf16>(o[v].x * by, o[v].y * by);
             w[2 * v + 1] = tc::pack<kBf16>(o[v].z * by, o[v].w * by);
         }
-        uint16_t* out = static_cast<uint16_t*>(p.out) + at * kLatent + 4 * c;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(at) * kLatent + 4 * c;
         if constexpr (kColumns == 4)
             tc::store_v8(out, w);
         else

@@ -563,16 +563,25 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     // key is read for two products (for one: 4096 queries 297 us in place of
     // 281), and a chunk that begins costs two tiles (2.8 us; with runs of equal
     // tiles 8 pieces of prompts took 39.8 us in place of 28.7).
-    const int most = kColumns / a.padded;  // queries of a product
+    const int most = 8 - log2_heads;  // log2 of a product's queries
     int log2 = 0;
-    while ((1 << log2) < most && (int64_t{p.batch} << log2) < p.total_q) ++log2;
-    const bool small = (int64_t{p.batch} << log2) >= p.total_q;
-    a.product_queries = 1 << log2;
+    while (log2 <= most && (int64_t{p.batch} << log2) < p.total_q) ++log2;
+    // Little work in all: smaller chunks, until there are tiles for one and a
+    // half rounds of blocks (300 queries of 24 heads on 500 to 800 keys 14.7 ->
+    // 11.1 us, 100 of 4 heads on 4100 keys 11.5 -> 10.0; for two rounds the first
+    // took 11.9, for four 13.4).
+    const int64_t key_tiles = (p.max_len + int64_t{kTile} - 1) / kTile;
+    const auto tiles_of = [&](int x) {  // at most
+        return (((static_cast<int64_t>(p.total_q) + (1 << x) - 1) >> x) + (x > 0 ? p.batch : 0)) * key_tiles;
+    };
+    while (log2 > 0 && 2 * tiles_of(log2) < 3 * device.sms) --log2;
+    const bool small = log2 <= most;
+    a.log2_queries = log2;
+    a.product_queries = 1 << (small ? log2 : most);
     a.places = small ? 2 : 1;
-    a.log2_queries = small ? log2 : log2 + 1;
     a.place_columns = a.padded << a.log2_queries;
-    a.begin_cost = small ? 0 : 2;
-    a.buffers = a.padded << log2 <= kColumns / 2 ? kBuffers : 2;
+    a.begin_cost = small ? 1 : 2;
+    a.buffers = a.product_queries * a.padded <= kColumns / 2 ? kBuffers : 2;
     a.stages = (kTileBytes - a.places * a.place_columns * 256) / kKeyBytes;
     if (a.stages > kStages) a.stages = kStages;
     a.box_rows = p.log2_page < 7 ? 1 << p.log2_page : kTile;
@@ -598,8 +607,7 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     static std::atomic<bool> prepared[2][5][AttendDevice::kMax];
     cudaError_t e = allow_shared(kernel, kSmem, prepared[full][log2_heads - 4][device.index]);
     if (e != cudaSuccess) return api_cuda_fail(e, "index scores shared memory");
-    const int64_t chunks = ((static_cast<int64_t>(p.total_q) + (1 << a.log2_queries) - 1) >> a.log2_queries) + p.batch;
-    const int64_t tiles = chunks * ((p.max_len + int64_t{kTile} - 1) / kTile);  // at most
+    const int64_t tiles = tiles_of(log2);
     const unsigned blocks = static_cast<unsigned>(tiles < device.sms ? tiles : device.sms);
     e = launch_early(kernel, dim3(blocks), kThreads, kSmem, stream, p, maps, a, device.flags);
     return e == cudaSuccess ? TOPK_OK : api_cuda_fail(e, "index scores launch");
