@@ -83,7 +83,7 @@ def source_digest() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "sparse_attention_indexer_uint32_gb300", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if name.startswith(("attend_", "serve_", "tc.", "tensor_map.")):
+        if name.startswith(("attend_", "serve_", "index_", "tc.", "tensor_map.", "tensor_calls.", "two_byte.")):
             continue
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             text = f.read()

@@ -22,7 +22,7 @@
 namespace topkidx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kLanes = kIndex / 8;            // lanes of a key
 constexpr int kTurnLanes = kRope / 8;         // of them, those with rotary values
 constexpr int kKeys = kThreads / kLanes;      // keys of a block

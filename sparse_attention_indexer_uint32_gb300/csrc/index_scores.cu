@@ -277,7 +277,7 @@ __device__ __forceinline__ void add_part(const uint32_t* x, int at, int heads, u
 #pragma unroll
     for (int i = 0; i < kCount; i += 4) {
         uint64_t w[2];
-        ptx::lds_u64x2(w_at + 4 * i, w);
+        tc::load_pairs(w_at + 4 * i, w);
         sum[0] = tc::fma2(tc::pair(top(i), top(i + 1)), w[0], sum[0]);
         sum[1] = tc::fma2(tc::pair(top(i + 2), top(i + 3)), w[1], sum[1]);
     }

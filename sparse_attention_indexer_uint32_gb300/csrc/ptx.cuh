@@ -68,9 +68,6 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
                  : "memory");
     return v;
 }
-__device__ __forceinline__ void lds_u64x2(uint32_t a, uint64_t* v) {
-    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(a) : "memory");
-}
 __device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }

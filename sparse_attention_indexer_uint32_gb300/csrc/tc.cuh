@@ -227,7 +227,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
-// The same for pairs that stay in 64 bits.
+// The same for pairs that stay in 64 bits, from shared memory two at a time.
+__device__ __forceinline__ void load_pairs(uint32_t addr, uint64_t* v) {
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
