@@ -1149,8 +1149,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256;
 constexpr int kFewParts = 4;
 // Units of 32 rows from which on a warp of the join behind shared positions
-// takes 16 values of each.
-constexpr int kFewUnits = 64;
+// takes 16, or 8, values of each, two or four parts at a time (4 of eight parts
+// otherwise): 2048 rows 65.0 us with 16, 68.4 with 4; 1024 rows 72.4 with 8, 74.5
+// with 4; 960 rows 19.9 and 21.6; 512 rows 22.3 and 21.2.
+constexpr int kManyUnits = 64, kSomeUnits = 24;
 
 // Values 4 c.. 4 (c + kColumns) of one row; kParts parts at a time.
 template <bool kBf16, int kColumns, int kParts>
@@ -1340,6 +1342,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_shared_kernel(const Late
         uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(at) * kLatent + 4 * c;
         if constexpr (kColumns == 4)
             tc::store_v8(out, w);
+        else if constexpr (kColumns == 2)
+            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
         else
             *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
         if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
@@ -1415,10 +1419,11 @@ topk_status_t launch_latent(const LatentParams& p, topk_dtype_t dtype, const Att
                      whole_rows, all_rows, box_rows);
     if (e != cudaSuccess) return api_cuda_fail(e, "latent attention launch");
     if (shared) {
-        const bool wide = all >= 32 * kFewUnits;
-        const int64_t units = (all + 31) / 32 * (wide ? kLatent / 128 : kLatent / 32), blocks = 2 * device.sms;
-        const auto join = wide ? (bf16 ? join_shared_kernel<true, 4> : join_shared_kernel<false, 4>)
-                               : (bf16 ? join_shared_kernel<true, 1> : join_shared_kernel<false, 1>);
+        const int columns = all >= 32 * kManyUnits ? 4 : all >= 32 * kSomeUnits ? 2 : 1;
+        const int64_t units = (all + 31) / 32 * (kLatent / 32 / columns), blocks = 2 * device.sms;
+        const auto join = columns == 4   ? (bf16 ? join_shared_kernel<true, 4> : join_shared_kernel<false, 4>)
+                          : columns == 2 ? (bf16 ? join_shared_kernel<true, 2> : join_shared_kernel<false, 2>)
+                                         : (bf16 ? join_shared_kernel<true, 1> : join_shared_kernel<false, 1>);
         e = launch_early(join, dim3(static_cast<unsigned>(units < blocks ? units : blocks)), kJoinThreads, 0, stream, p);
         if (e != cudaSuccess) return api_cuda_fail(e, "shared attention join launch");
     } else if (pairs > 1) {
