@@ -64,7 +64,7 @@ struct Span {  // of a request
     int32_t from, n, length;
 };
 struct Shared {
-    uint64_t query_full[2], query_empty[2], weight_full[2];
+    uint64_t query_full[2], query_empty[2], weight_full[2];  // (full: by place; in one place by product)
     uint64_t key_full[kStages], key_empty[kStages], mask_full[kMasks];
     uint64_t score_full[kBuffers], score_empty[kBuffers], end;
     int64_t total, begin;  // units of cost of the whole call; the first of this block's run
@@ -394,8 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (copied > 0) tc::Waits::drain(&sh.key_full[i], (copied - 1) & 1);
         }
     } else if (warp == kQueryWarp) {
+        uint32_t seconds = 0;  // second products so far
         for (int n = 0; walk.next(s); ++n) {
             const int place = n % a.places, round = n / a.places;
+            // The first product begins without the second's queries.
+            const int firsts = min(s.queries, a.product_queries), rest = s.queries - firsts;
             // Weights come to registers, and queries to L2, while the place is still in use.
             float w[kAllColumns / 32];
 #pragma unroll
@@ -408,27 +411,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::prefetch_3d(&maps.q, 64 * (i & 1), 0, s.query + (i >> 1));
                 if (!wait.all(&sh.query_empty[place], (round - 1) & 1) || wait.over()) break;
             }
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.query_full[place], s.queries * kHeads * 256);
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(&sh.query_full[place], firsts * kHeads * 256);
+                if (rest > 0) ptx::mbar_arrive_expect_tx(&sh.query_full[1], rest * kHeads * 256);
+            }
             __syncwarp();
             for (int i = lane; i < 2 * s.queries; i += 32)
                 tc::load_3d(queries + place * place_bytes + (i & 1) * (place_columns * 128) + (i >> 1) * (kHeads * 128), &maps.q,
-                            64 * (i & 1), 0, s.query + (i >> 1), &sh.query_full[place]);
+                            64 * (i & 1), 0, s.query + (i >> 1), &sh.query_full[(i >> 1) < firsts ? place : 1]);
 #pragma unroll
             for (int k = 0; k < kAllColumns / 32; ++k)
                 if (32 * k + lane < place_columns)
                     ptx::sts_u32(weights + 4 * (place * place_columns + 32 * k + lane), __float_as_uint(w[k]));
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sh.weight_full[place]);
-            if (!wait.all(&sh.query_full[place], round & 1)) {
+            bool landed = wait.all(&sh.query_full[place], round & 1);
+            if (rest > 0) landed = wait.all(&sh.query_full[1], seconds & 1) && landed;
+            if (!landed) {
                 tc::Waits::drain(&sh.query_full[place], round & 1);
+                if (rest > 0) tc::Waits::drain(&sh.query_full[1], seconds & 1);
                 break;
             }
+            if (rest > 0) ++seconds;
         }
     } else if (warp == kProductWarp) {
         const uint64_t key_at = tc::operand(keys), query_at = tc::operand(queries);
         const uint32_t buffer_columns = 2 * kColumns / a.buffers;
         int stage = 0, buffer = 0;
-        uint32_t round = 0, use = 0;  // how often the places were used
+        uint32_t round = 0, use = 0, seconds = 0;  // how often the places were used; second products
         // Given up, nothing is issued or announced any more.
         bool on = true;
         for (int segment = 0; walk.next(s); ++segment) {
@@ -437,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int tile = s.first; tile < s.last; ++tile) {
                 on = wait.all(&sh.key_full[stage], round & 1) && on;
                 for (int first = 0; first < s.queries; first += a.product_queries) {
+                    if (first > 0 && tile == s.first) on = wait.all(&sh.query_full[1], seconds++ & 1) && on;
                     if (use > 0) on = wait.all(&sh.score_empty[buffer], (use - 1) & 1) && on;
                     tc::fence_after();
                     if (on && tc::elect()) {
