@@ -48,9 +48,9 @@
 // products that one request's heads alone fill to an eighth, and the prompt's
 // rows are read once for 128 rows in place of once a request.  Every piece
 // leaves fp32 sums, joined by row: 64 requests of 16 heads behind 32768
-// positions with 1024 of their own on average 75 to 78 us (0.97 to 1.0 PFLOP/s;
-// 66 us of it here, 1.75 a tile), 16 requests of 128 heads, 8192 and 8192, 65 us,
-// 32 requests of 4 queries and 16 heads behind 16000 70 us.
+// positions with 1024 of their own on average 72 to 76 us (0.99 to 1.04 PFLOP/s;
+// 66 us of it here, 1.75 a tile), 16 requests of 128 heads, 8192 and 8192, 62 to 68
+// us, 32 requests of 4 queries and 16 heads behind 16000 67 to 70 us.
 //
 // Warps of each block: 0-3 softmax and results (thread t: row t & 63, half t >> 6
 // of the tile's slots, values 256 (t >> 6).. of the sums), 4 products (first

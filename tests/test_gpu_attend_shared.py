@@ -265,6 +265,27 @@ def test_replayed_with_other_lengths(api):
         x.check(out, lse)
 
 
+def test_two_graphs_share_a_workspace(api):
+    """Replayed in turn on one stream, with other shapes each."""
+    sets = [Batch([900, 700, 650], 640, 1, 64, 64, torch.bfloat16), Batch([300] * 9, 200, 2, 16, 32, torch.float16, seed=9)]
+    first = [x.run(api) for x in sets]
+    workspace = max((w for _, _, w in first), key=lambda w: w.numel())
+    outs = [(torch.empty_like(o), torch.empty_like(l)) for o, l, _ in first]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for x, (out, lse) in zip(sets, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            x.run(api, out=out, lse=lse, workspace=workspace)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (o, l, _), (out, lse) in zip(first, outs):
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_on_two_streams(api):
     sets = [Batch([900, 1290, 700], 640, 1, 16, 64, torch.bfloat16, seed=s) for s in (0, 50)]
     streams = [torch.cuda.Stream() for _ in sets]

@@ -101,6 +101,30 @@ def test_append_nothing_and_special_rows(api):
     assert cache[1:3].isnan().all() and torch.equal(cache[4:], before[4:])
 
 
+def test_append_replayed_and_on_another_stream(api):
+    tokens, n = 300, 400
+    rows, slots, cos_sin = randn(1, tokens, INDEX), perm(2, n)[:tokens].clone(), turns(500)
+    positions, weight, bias = i32(torch.arange(tokens)), 1 + randn(3, INDEX) / 8, randn(4, INDEX) / 8
+    more = dict(norm_weight=weight, norm_bias=bias, cos_sin=cos_sin, positions=positions)
+    cache, other = torch.zeros(n, INDEX, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, INDEX, dtype=torch.bfloat16, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    api.index_append(rows, slots, other, stream=stream, **more)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        api.index_append(rows, slots, cache, **more)
+    for seed in (7, 8):
+        rows.copy_(randn(seed, tokens, INDEX))
+        slots.copy_(perm(seed, n)[:tokens])
+        positions.copy_(perm(seed + 10, 500)[:tokens])
+        graph.replay()
+        torch.cuda.synchronize()
+        want, bound = append(rows, weight, bias, 1e-6, cos_sin, positions, False, False)
+        check(cache[slots.long()], want, bound, "rows")
+    assert other.any()
+
+
 def paged(seed, batch, width, page, dtype, spare=3, slot_room=INDEX):
     cache = randn(seed, (batch * width + spare) * page, slot_room, dtype=dtype)[:, :INDEX]
     return cache, perm(seed + 1, batch * width + spare)[: batch * width].reshape(batch, width)
@@ -298,6 +322,22 @@ def test_scores_on_two_streams(api):
     torch.cuda.synchronize()
     for (q, w), out in zip(sets, outs):
         check_scores(q, w, cache, lens, table, page, out, torch.full_like(out, 7.0))
+
+
+def test_scores_into_new_memory_on_another_stream(api):
+    page = 64
+    cache, table = paged(1, 3, 10, page, torch.float16)
+    q, w, lens = randn(2, 6, 24, INDEX, dtype=torch.float16), randn(3, 6, 24, dtype=torch.float32), i32([600, 1, 77])
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (stream, stream.cuda_stream, None):
+        out = api.index_scores(q, w, cache, lens, table, page, max_seq_len=630, stream=s)
+        torch.cuda.synchronize()
+        assert out.shape == (6, 632)
+        before = out.clone()
+        for i in range(6):  # (what is not seen is whatever the memory held)
+            before[i, : int(lens[i // 2]) - (1 - i % 2)] = 0
+        check_scores(q, w, cache, lens, table, page, out, before, max_len=630)
 
 
 def test_scores_equal_calls_give_equal_bits(api):
