@@ -31,7 +31,8 @@
 // scores.  (Products of 128 columns and four tiles: 347 us, bound by shared
 // memory; 16 warps of sums: 288; a tile given back as soon as its last columns
 // are in registers, or the next tile's columns asked for then: 299 and 327;
-// chunks of one product with two places: 297.)  4 requests of 8192 keys take 5 us
+// chunks of one product with two places: 297; pairs of blocks with half of the
+// queries each: 287.)  4 requests of 8192 keys take 5 us
 // on the GPU, of which 1.7 pass until a block knows its run and 2.2 more until
 // its queries are there.
 //
