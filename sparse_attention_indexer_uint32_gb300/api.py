@@ -42,12 +42,14 @@ def topk_transform(scores: torch.Tensor, seq_lens: torch.Tensor, page_table: tor
     """Plans (unless a planned ``workspace`` is given) and runs the transform.
 
     ``scores``: float32 cuda [batch, row_stride] (row-contiguous); ``seq_lens``:
-    int32 cuda [batch]; ``page_table``: int32 cuda [batch, pages].  Returns
-    ``(out, raw_or_None, workspace)``.
+    int32 cuda [batch]; ``page_table``: int32 cuda [batch, pages].  Without
+    ``max_seq_len`` a row has what its scores and its pages both hold: rows of
+    scores may be padded past the last page.  Returns ``(out, raw_or_None,
+    workspace)``.
     """
     batch, row_stride = scores.shape
     if max_seq_len is None:
-        max_seq_len = row_stride
+        max_seq_len = min(row_stride, page_table.shape[1] * page_size)
     if scores.stride(1) != 1 or page_table.stride(1) != 1:
         raise ValueError("scores and page_table rows must be contiguous")
     if workspace is None:
@@ -375,7 +377,8 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, cache: torch.Tensor, se
     requests, through ``page_table`` [batch, pages].  ``cu_q`` [batch + 1]: the requests' queries, their newest
     tokens (None: as many for each).  Returns ``out`` [tokens, max_seq_len or more] (float32; new memory has
     max_seq_len rounded up to a multiple of 4), of which each query's row is written up to what it sees: the last
-    query of a request ``seq_lens`` positions, each one before it one less."""
+    query of a request ``seq_lens`` positions, each one before it one less.  Where lengths may be above a
+    ``max_seq_len`` given here, the selection is given it too."""
     if out is not None and _calls.index_scores(q, weights, cache, seq_lens, page_table, page_size, cu_q, max_seq_len, out,
                                                None if stream is None else _lib.stream_handle(stream, 0)):
         return out
