@@ -478,9 +478,9 @@ __device__ __forceinline__ float* part_of(const LatentParams& p, int rows, int p
 
 // Workspace of a call with shared positions: for each group of rows (those of
 // the prompt first, then by request) the pair whose run begins it and how many
-// runs it is in; then a place for two partial sums of each run, as above, with
-// as many rows as any group has; then one for each group, for those that are
-// in one run only.
+// runs it is in, none for a group of a row without positions; then a place for
+// two partial sums of each run, as above, with as many rows as any group has;
+// then one for each group, for those that are in one run only.
 __host__ __device__ __forceinline__ int64_t groups_in(int64_t rows) { return (rows + kRows - 1) / kRows; }
 __host__ __device__ __forceinline__ int64_t place_floats(int64_t rows) {
     return static_cast<int64_t>(part_rows_of(rows)) * (kLatent + 2);
@@ -505,6 +505,19 @@ __device__ __forceinline__ float* whole_of(const LatentParams& p, int row, int g
     if (row == 0) return at + group * place_floats(p.batch * each);
     at += groups_in(p.batch * each) * place_floats(p.batch * each);
     return at + ((row - 1) * groups_in(each) + group) * place_floats(each);
+}
+
+// Threads i of n: the records of the groups that no run has.  With them every
+// record is written in each call, and the join needs nothing else to know which
+// parts there are.
+__device__ __forceinline__ void note_empty(const LatentParams& p, int common, int i, int n) {
+    const int each = p.queries * p.heads;
+    const int of_prompt = static_cast<int>(groups_in(int64_t{p.batch} * each)), of_row = static_cast<int>(groups_in(each));
+    const int64_t groups = all_groups(p.batch, each);
+    for (int64_t g = i; g < groups; g += n) {
+        const int row = g < of_prompt ? 0 : static_cast<int>(g - of_prompt) / of_row + 1;
+        if (Row(p, row, common).tiles() == 0) static_cast<int2*>(p.workspace)[g] = make_int2(0, 0);
+    }
 }
 
 template <bool kBf16, bool kPaged, bool kShared>
@@ -567,6 +580,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const tc::Waits wait{&sh.gave_up, p.wait.ns};
     Walk<kShared> walk(p, sh, pair, pairs);
     Segment s = {};
+    // By the softmax warps, which have nothing to do yet.
+    if (kShared && warp < 4)
+        note_empty(p, sh.common, static_cast<int>(blockIdx.x) * 128 + threadIdx.x, static_cast<int>(gridDim.x) * 128);
 
     if (!kPaged && (warp == 5 || warp == 8)) {
         // Selected slots, first product: 32 of the block's 64 slots of each
@@ -1272,22 +1288,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_shared_kernel(const Late
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int each = p.queries * p.heads, rows = p.batch * each;  // (at most 2^30)
     const int units = (rows + 31) / 32 * kPerUnit;
-    int unit = static_cast<int>(blockIdx.x);
-    const auto row_at = [&] { return unit / kPerUnit * 32 + lane; };
-    const auto length_at = [&] { return row_at() < rows ? length_of(p, row_at() / each) : 0; };
-    // The lengths are there before the sums: the first kernel has read them when
-    // this one is placed.
-    const int common = min(max(*p.shared_len, 0), p.max_shared);
-    int length = length_at();
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    for (; unit < units; unit += static_cast<int>(gridDim.x), length = length_at()) {
-        const int at = row_at(), c = (unit % kPerUnit * (kJoinThreads / 32) + warp) * kColumns;
+    for (int unit = static_cast<int>(blockIdx.x); unit < units; unit += static_cast<int>(gridDim.x)) {
+        const int at = unit / kPerUnit * 32 + lane, c = (unit % kPerUnit * (kJoinThreads / 32) + warp) * kColumns;
         if (at >= rows) continue;
         const int b = at / each, m = at - b * each, prompt_group = at / kRows, group = m / kRows;
-        int2 prompt = parts_of(p, 0, prompt_group), own = parts_of(p, b + 1, group);
-        if (common <= 0) prompt = make_int2(0, 0);  // (not written)
-        if (length <= common) own = make_int2(0, 0);
+        const int2 prompt = parts_of(p, 0, prompt_group), own = parts_of(p, b + 1, group);
         const int prompt_rows = part_rows_of(rows), own_rows = part_rows_of(each);
         float top = -INFINITY, l = 0.f;
         float4 o[kColumns] = {};
