@@ -8,9 +8,12 @@ library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
+
+from .build import tensor_calls_path
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_PKG, "libtopkidx.so")
@@ -176,14 +179,16 @@ _lib = _load()
 
 
 def _load_tensor_calls():
-    if not os.path.exists(os.path.join(_PKG, "_tensor_calls.so")):
-        raise ImportError(f"{_PKG}/_tensor_calls.so is missing: build it with "
+    path = tensor_calls_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with "
                           "`python -m sparse_attention_indexer_uint32_gb300.build`")
-    from . import _tensor_calls
-
-    _tensor_calls.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+    spec = importlib.util.spec_from_file_location(f"{__package__}._tensor_calls", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
         "topk_index_append", "topk_index_scores", "topk_attend_shared", "topk_attend_shared_workspace_bytes")))
-    return _tensor_calls
+    return module
 
 
 #: The calls that are made straight from tensors (csrc/tensor_calls.cpp).

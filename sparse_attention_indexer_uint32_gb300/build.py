@@ -1,5 +1,5 @@
 """Builds ``libtopkidx.so`` (the CUDA library) in-tree with nvcc for sm_103a, and
-``_tensor_calls.so``, which makes some of its calls straight from tensors.
+the module ``_tensor_calls``, which makes some of its calls straight from tensors.
 
 Usage: ``python -m sparse_attention_indexer_uint32_gb300.build [--verbose]``.
 The translation units are compiled in parallel, those of the library linked
@@ -21,7 +21,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libtopkidx.so")
-TENSOR_CALLS = os.path.join(PKG, "_tensor_calls.so")
 SOURCES = ["topk_kernels.cu", "topk_stream.cu", "topk_warp.cu", "topk_split.cu", "topkidx_api.cu", "topk_noalloc.cu",
            "serve_tables.cu", "serve_append.cu", "index_append.cu", "index_scores.cu",
            "attend_latent.cu", "attend_prompt.cu", "attend_api.cu"]
@@ -40,6 +39,17 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def tensor_calls_path() -> str:
+    """The module ``_tensor_calls`` for the running torch and Python.
+
+    It reads their objects where this version has them, so the file is named by
+    both: one that was built for another version is not found, and not loaded.
+    """
+    import torch
+
+    return os.path.join(PKG, f"_tensor_calls.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
+
+
 def _build_tensor_calls() -> None:
     """The CPython module, against the headers and libraries of the torch that imports it."""
     import torch
@@ -47,7 +57,8 @@ def _build_tensor_calls() -> None:
     root = os.path.dirname(torch.__file__)
     include = os.path.join(root, "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = TENSOR_CALLS + ".tmp"
+    path = tensor_calls_path()
+    tmp = path + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", include,
            "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
@@ -56,13 +67,10 @@ def _build_tensor_calls() -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for tensor_calls.cpp:\n{res.stderr}")
-    os.replace(tmp, TENSOR_CALLS)
+    os.replace(tmp, path)
 
 
-def build(verbose: bool = False, force: bool = False) -> str:
-    built = (LIBRARY, TENSOR_CALLS)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in built):
-        return LIBRARY
+def _build_library(verbose: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
@@ -79,16 +87,25 @@ def build(verbose: bool = False, force: bool = False) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        calls = ex.submit(_build_tensor_calls)
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        calls.result()
     tmp = LIBRARY + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIBRARY)
+
+
+def build(verbose: bool = False, force: bool = False) -> str:
+    changed = _deps_mtime()
+    old = [force or not os.path.exists(f) or os.path.getmtime(f) < changed for f in (LIBRARY, tensor_calls_path())]
+    with concurrent.futures.ThreadPoolExecutor(1) as ex:
+        calls = ex.submit(_build_tensor_calls) if old[1] else None
+        if old[0]:
+            _build_library(verbose)
+        if calls:
+            calls.result()
     return LIBRARY
 
 
