@@ -3,13 +3,16 @@
 Every function has the C name.  Tensors are passed as raw device pointers;
 the stream defaults to PyTorch's current stream on the tensors' device.  A
 non-OK status raises :class:`TopkError`.  There is no fallback: if the CUDA
-library is missing, importing this module raises.
+library is missing, importing this module raises.  Three of the calls of ``api``
+are made by a compiled module, where it is built, and through here otherwise.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
 import os
+import types
+import warnings
 
 import torch
 
@@ -178,20 +181,27 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
+_TENSOR_CALLS = ("topk_index_append", "topk_index_scores", "topk_attend_shared", "topk_attend_shared_workspace_bytes")
+
+
 def _load_tensor_calls():
+    """The module, or, with a warning, what stands for it where it was not built: then every call goes through ctypes."""
     path = tensor_calls_path()
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with "
-                          "`python -m sparse_attention_indexer_uint32_gb300.build`")
-    spec = importlib.util.spec_from_file_location(f"{__package__}._tensor_calls", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
-        "topk_index_append", "topk_index_scores", "topk_attend_shared", "topk_attend_shared_workspace_bytes")))
+    try:
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._tensor_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"index_append, index_scores and attend_shared take some 2 us more a call: {e}; build the module "
+                      "with `python -m sparse_attention_indexer_uint32_gb300.build`", RuntimeWarning, stacklevel=2)
+        return types.SimpleNamespace(**{name.removeprefix("topk_"): lambda *args: False for name in _TENSOR_CALLS[:3]})
+    module.bind(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in _TENSOR_CALLS))
     return module
 
 
-#: The calls that are made straight from tensors (csrc/tensor_calls.cpp).
+#: The calls that are made straight from tensors (csrc/tensor_calls.cpp).  Each returns whether it made the call.
 tensor_calls = _load_tensor_calls()
 
 

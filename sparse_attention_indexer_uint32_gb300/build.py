@@ -50,14 +50,20 @@ def tensor_calls_path() -> str:
     return os.path.join(PKG, f"_tensor_calls.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
-def _build_tensor_calls() -> None:
+def _old(path: str, force: bool) -> bool:
+    return force or not os.path.exists(path) or os.path.getmtime(path) < _deps_mtime()
+
+
+def _build_tensor_calls(force: bool) -> None:
     """The CPython module, against the headers and libraries of the torch that imports it."""
+    path = tensor_calls_path()
+    if not _old(path, force):
+        return
     import torch
 
     root = os.path.dirname(torch.__file__)
     include = os.path.join(root, "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    path = tensor_calls_path()
     tmp = path + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", include,
@@ -98,14 +104,12 @@ def _build_library(verbose: bool) -> None:
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    changed = _deps_mtime()
-    old = [force or not os.path.exists(f) or os.path.getmtime(f) < changed for f in (LIBRARY, tensor_calls_path())]
+    """The library's path; what fails in the module is raised once the library, which works without it, is there."""
     with concurrent.futures.ThreadPoolExecutor(1) as ex:
-        calls = ex.submit(_build_tensor_calls) if old[1] else None
-        if old[0]:
+        calls = ex.submit(_build_tensor_calls, force)
+        if _old(LIBRARY, force):
             _build_library(verbose)
-        if calls:
-            calls.result()
+        calls.result()
     return LIBRARY
 
 
