@@ -49,3 +49,33 @@ def test_rows_padded_past_the_last_page(api, pages, page):
     for k in (3, 64):
         slots, raw, _ = api.topk_transform(out, i32(lens), table, page, k, want_raw=True)
         check(out, lens, table, page, k, slots, raw)
+
+
+@pytest.mark.parametrize("page", [2, 64])
+def test_several_queries_a_request(api, page):
+    """The selection takes a length and a row of pages for each row of scores: those of the row's request, and what
+    its query sees."""
+    new, past = [5, 1, 0, 130, 3], [400, 77, 20, 0, 0]
+    lens, pages = [a + b for a, b in zip(new, past)], -(-407 // page)
+    q, weights, cache, table = inputs(2, 5, sum(new), 16, pages, page)
+    cu = torch.tensor([0] + new).cumsum(0)
+    out = api.index_scores(q, weights, cache, i32(lens), table, page, cu_q=i32(cu))
+    # As a program has it, on the GPU and without a host read of lengths.
+    of = torch.repeat_interleave(torch.arange(5, device="cuda"), i32(new), output_size=sum(new))
+    seen = (i32(lens) - i32(cu[1:]))[of] + torch.arange(1, sum(new) + 1, device="cuda", dtype=torch.int32)
+    rows = table[of]
+    slots, raw, _ = api.topk_transform(out, seen, rows, page, 50, want_raw=True)
+    expected = [n - m + 1 + i for n, m in zip(lens, new) for i in range(m)]
+    assert seen.tolist() == expected
+    check(out, expected, rows, page, 50, slots, raw)
+
+
+def test_a_length_of_its_own(api):
+    """Lengths above a max_seq_len that both calls are given: nothing past it is looked at."""
+    q, weights, cache, table = inputs(3, 3, 3, 8, 10, 64)
+    lens = [640, 70, 69]
+    out = api.index_scores(q, weights, cache, i32(lens), table, 64, max_seq_len=70)
+    assert out.shape == (3, 72)
+    out[:, 70:] = float("inf")
+    slots, raw, _ = api.topk_transform(out, i32(lens), table, 64, 80, max_seq_len=70, want_raw=True)
+    check(out, [70, 70, 69], table, 64, 80, slots, raw)
