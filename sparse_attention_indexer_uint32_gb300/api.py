@@ -235,6 +235,13 @@ def block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     return out
 
 
+def _check_angles(cos_sin):
+    # (an empty table has no address: the library would take it for none)
+    if cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.shape[0] < 1 or cos_sin.shape[1] != _ROPE
+                                or not cos_sin.is_contiguous()):
+        raise ValueError(f"cos_sin must be contiguous [1 position or more, {_ROPE}]: got {tuple(cos_sin.shape)}")
+
+
 def _check_append(rows, slots, cache, norm_weight, cos_sin, positions):
     dev = cache.device
     _dtype(cache, "cache")
@@ -245,8 +252,7 @@ def _check_append(rows, slots, cache, norm_weight, cos_sin, positions):
         raise ValueError(f"rows and cache must be [.., {_WIDTH}]: got {tuple(rows.shape)} and {tuple(cache.shape)}")
     _whole((rows.shape[0],), slots=slots, positions=positions)
     _whole((_LATENT,), norm_weight=norm_weight)
-    if cos_sin is not None:
-        _whole((cos_sin.shape[0], _ROPE), cos_sin=cos_sin)
+    _check_angles(cos_sin)
     _no_grad(rows=rows, cache=cache, norm_weight=norm_weight, cos_sin=cos_sin)
     _on_gpu(cache)
 
@@ -258,12 +264,13 @@ def cache_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     ``cache`` [num_slots, 576], normed by ``norm_weight`` [512] and rotated by ``cos_sin`` (float32
     [num_positions, 64]: cosines, sines) at ``positions``, where these are given."""
     gpu, dtype, shape, places = cache.get_device(), cache.dtype, rows.shape, cache.shape
-    code, tokens, positions_n = _DTYPES.get(dtype), shape[0] if shape else 0, 0 if cos_sin is None else cos_sin.shape[0]
+    code, tokens = _DTYPES.get(dtype), shape[0] if shape else 0
+    positions_n = cos_sin.shape[0] if cos_sin is not None and cos_sin.dim() else 0
     if not (gpu >= 0 and code is not None and rows.dtype is dtype and rows.get_device() == gpu and len(shape) == 2
             and len(places) == 2 and shape[1] == _WIDTH == places[1] and rows.stride(1) == 1 == cache.stride(1)
             and _line(slots, tokens, gpu) and (positions is None or _line(positions, tokens, gpu))
             and (norm_weight is None or _is(norm_weight, dtype, gpu, (_LATENT,)))
-            and (cos_sin is None or _is(cos_sin, _F32, gpu, (positions_n, _ROPE)))
+            and (cos_sin is None or (positions_n > 0 and _is(cos_sin, _F32, gpu, (positions_n, _ROPE))))
             and not (_grad_enabled() and _any_grad(rows, cache, norm_weight, cos_sin))):
         _check_append(rows, slots, cache, norm_weight, cos_sin, positions)
     status = (_c.topk_cache_append if _current_device() == gpu else _there(_c.topk_cache_append, gpu))(
@@ -286,8 +293,7 @@ def _check_index_append(rows, slots, cache, norm_weight, norm_bias, cos_sin, pos
         raise ValueError(f"rows and cache must be [.., {_INDEX}]: got {tuple(rows.shape)} and {tuple(cache.shape)}")
     _whole((rows.shape[0],), slots=slots, positions=positions)
     _whole((_INDEX,), norm_weight=norm_weight, norm_bias=norm_bias)
-    if cos_sin is not None:
-        _whole((cos_sin.shape[0], _ROPE), cos_sin=cos_sin)
+    _check_angles(cos_sin)
     _no_grad(rows=rows, cache=cache, norm_weight=norm_weight, norm_bias=norm_bias, cos_sin=cos_sin)
     _on_gpu(cache)
 
@@ -327,8 +333,8 @@ def index_append(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
     if cos_sin is not None:
         turns = cos_sin.shape
         positions_n = turns[0] if turns else 0
-        right = (right and cos_sin.dtype is _F32 and len(turns) == 2 and turns[1] == _ROPE and cos_sin.get_device() == gpu
-                 and cos_sin.is_contiguous())
+        right = (right and cos_sin.dtype is _F32 and len(turns) == 2 and positions_n > 0 and turns[1] == _ROPE
+                 and cos_sin.get_device() == gpu and cos_sin.is_contiguous())
         turns_at = cos_sin.data_ptr()
     if not right or (_grad_enabled() and (_any_grad(rows, cache, norm_weight, norm_bias)
                                           or (cos_sin is not None and cos_sin.requires_grad))):

@@ -117,6 +117,7 @@ PyObject* index_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             c.rows(turns, at::kFloat, 2, TOPK_ROPE_DIM);
             c.need(c.right && turns->is_contiguous());
             if (c.right) angles = turns->size(0);
+            c.need(angles > 0);  // (an empty table has no address)
         }
         const double eps = PyFloat_AsDouble(a[5]);
         const int interleaved = PyObject_IsTrue(a[8]), rope_last = PyObject_IsTrue(a[9]);
