@@ -414,7 +414,7 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, cache: torch.Tensor, se
     total, heads, _ = shape
     batch, slots = listed[0], places[0]
     if out is None:
-        out = _empty((total, (most + 3) // 4 * 4), _F32, q.device, stream)
+        out = _empty((total, max(most + 3, 0) // 4 * 4), _F32, q.device, stream)  # (what is below 0 the library refuses)
         out_steps = out.stride()
     many = total > 1
     status = (_c.topk_index_scores if _current_device() == gpu else _there(_c.topk_index_scores, gpu))(
