@@ -64,3 +64,13 @@ def test_a_piece_among_single_queries(api):  # noqa: F811
     cache, table = paged(1, 61, 50, 64, torch.bfloat16)
     run(api, randn(2, 260, 64, INDEX), randn(3, 260, 64, dtype=torch.float32), cache, i32([a + b for a, b in zip(new, past)]),
         table, 64, cu=i32([0] + torch.tensor(new).cumsum(0).tolist()))
+
+
+@pytest.mark.parametrize("heads", [5, 64, 256])
+def test_more_queries_than_positions(api, heads):  # noqa: F811
+    """A request's first queries see nothing, whole chunks of them; others beside it see what they see."""
+    new, lens = [700, 40, 3, 300, 90], [100, 7, 3000, 0, 2900]
+    cache, table = paged(1, 5, 48, 64, torch.bfloat16)
+    total = sum(new)
+    run(api, randn(2, total, heads, INDEX), randn(3, total, heads, dtype=torch.float32), cache, i32(lens), table, 64,
+        cu=i32([0] + torch.tensor(new).cumsum(0).tolist()))
