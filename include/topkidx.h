@@ -340,10 +340,14 @@ topk_status_t topk_index_append(const void* rows, int64_t row_stride, int32_t to
  * tokens: the last sees t < seq_lens[b] (values above max_seq_len count as
  * max_seq_len, negative ones as 0), each one before it one position less.
  * Positions that a query does not see, and queries of no request, are left as
- * they were (the selection reads a row up to its length only); a position
- * whose slot is outside [0, num_slots) scores -inf.  A NaN among a key's
- * products goes to that position's score; what other slots hold is not used.
+ * they were; a position whose slot is outside [0, num_slots) scores -inf.  A NaN
+ * among a key's products goes to that position's score; what other slots hold is
+ * not used.
  * Products of two-byte values are exact and summed in fp32.
+ * topk_transform takes a length and a row of pages for each row of scores, and
+ * reads the row up to that length only: where a request has several queries,
+ * the seq_lens[b] - (cu_q[b + 1] - 1 - i) positions that query i sees and a copy
+ * of its request's row of pages.
  *   q                 device [total_q][q_token_stride], head h at h * q_head_stride
  *                     (strides of at least 128 where there is more than one).
  *   weights           device float[total_q][weights_stride], heads used per row.
@@ -450,9 +454,14 @@ topk_status_t topk_attend_paged(const void* q, int64_t q_row_stride, int64_t q_q
  * What slots past a request's length hold is not used, nor what the page at
  * which its own positions begin holds before them; the shared positions and
  * the rows of its own newest tokens must be finite.
+ * The prompt's products are shared as well as its reading, while a request has
+ * fewer than 128 (query, head) rows: with about 100 or more of them
+ * topk_attend_paged is as fast or faster.
  *   workspace         of topk_attend_shared_workspace_bytes(batch, queries,
  *                     heads) bytes, 16-byte aligned, contents free; calls that
- *                     may run at the same time need one each.
+ *                     may run at the same time need one each.  About 40 MB (less
+ *                     below 128 rows in all), and 4 KB for each of the
+ *                     batch * queries * heads rows, whose sums it takes.
  * Errors: TOPK_EINVAL, TOPK_EALIGN, TOPK_ENOSPACE, TOPK_EDEVICE, TOPK_ECUDA.
  */
 size_t topk_attend_shared_workspace_bytes(int32_t batch, int32_t queries, int32_t heads);

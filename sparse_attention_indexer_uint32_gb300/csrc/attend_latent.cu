@@ -50,7 +50,10 @@
 // leaves fp32 sums, joined by row: 64 requests of 16 heads behind 32768
 // positions with 1024 of their own on average 72 to 76 us (0.99 to 1.04 PFLOP/s;
 // 66 us of it here, 1.75 a tile), 16 requests of 128 heads, 8192 and 8192, 62 to 68
-// us, 32 requests of 4 queries and 16 heads behind 16000 67 to 70 us.
+// us, 32 requests of 4 queries and 16 heads behind 16000 67 to 70 us.  Requests
+// with 128 rows each fill the products alone, and the sums' way through memory is
+// left as a loss: 64 requests behind 8192 with 1024 of their own take 39 us with
+// 16 heads (whole rows: 91), 74 with 64 (98), 108 with 100 (112), 128 with 128 (118).
 //
 // Warps of each block: 0-3 softmax and results (thread t: row t & 63, half t >> 6
 // of the tile's slots, values 256 (t >> 6).. of the sums), 4 products (first

@@ -7,10 +7,12 @@
 // of the token's position, and one rounding.  Half a warp holds a key, eight
 // values (16 bytes) a lane, so a key is read once and written once: 256 + 256 +
 // 256 bytes with its cosines and sines, bound by memory at large counts and by the
-// call at small ones.  65536 keys take 12.0 to 12.5 us, 4.1 to 4.2 TB/s (60 to 62 % of the
-// measured copy rate; two dependent reads, position and angles, in each of 5 rounds of
-// blocks).  Four keys a half warp at once took 15.7 us, the registers held fewer
-// keys on an SM; 64 keys 2.9 us a call, the host's 2.8 of them.
+// call at small ones.  65536 keys take 12.0 to 12.5 us in fp16, 4.1 to 4.2 TB/s (60 to
+// 62 % of the measured copy rate), and 13.3 to 13.9 in bf16, 3.7 to 3.8 TB/s: two
+// dependent reads, position and angles, in each round of blocks, 4.5 rounds with
+// fp16's 40 registers and 5.4 with bf16's 48.  Four keys a half warp at once took
+// 15.7 us, the registers held fewer keys on an SM; 64 keys 2.9 us a call, the
+// host's 2.8 of them.
 #include <cuda_runtime.h>
 
 #include <cstdint>

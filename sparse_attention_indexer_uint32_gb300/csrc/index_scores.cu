@@ -9,9 +9,10 @@
 // columns.  One query of 64 heads takes 16 K operations on 260 bytes and is
 // bound by memory, 16 of them together by the products.
 //
-// Work is cut in equal runs of tiles (128 keys by one chunk of a request's
-// queries), one block an SM: the host does not know the lengths.  Tiles are
-// independent, so nothing is joined.  A chunk's queries stay in shared memory
+// Work is cut in runs of equal cost, one block an SM: the host does not know the
+// lengths.  A tile (128 keys by one chunk of a request's queries) costs one, the
+// beginning of a chunk one more where it is one product and two where it is
+// two.  Tiles are independent, so nothing is joined.  A chunk's queries stay in shared memory
 // while its keys pass through a ring of three to five places, by tiled copies of
 // a page (or 128 rows of it) each; tensor memory holds two or four tiles of
 // scores, some of them read while another is computed.
@@ -20,21 +21,23 @@
 // engine, with zeros: the loops over a query's columns are unrolled (a loop with
 // its ends tested at run time took 1.5 times as long), and a chunk holds a power
 // of two of queries, so that the cost of a request's tiles under the causal
-// limit has a closed form.  Odd numbers of heads pay for the next power of two.
+// limit has a closed form.  Other numbers of heads pay for the next power of two,
+// and for the test that keeps a padding column's infinity out of the sum: 4096
+// queries on 4096 to 8192 keys take 325 us with 24 heads and 167 with 32, 2048 on
+// 2048 to 4096 213 with 100 and 155 with 128.  (Where keys are finite a caller may
+// pad the heads with zeros, of queries and of weights.)
 //
 // Measured: 128 requests of 1024 to 32768 keys, 64 heads, 89.9 us, 6.3 TB/s (92 %
 // of the measured copy rate); one of 1048576 keys 47.4 us, 5.8 TB/s; 4096 queries
 // of 64 heads on 4096 to 8192 keys 280 us alone, 297 in a row, 1.40 to 1.49
-// PFLOP/s (82 to 87 % of the sustained rate of a library product): the products
-// of 256 columns take 1024 cycles, their sums 1200 on two groups of warps, the
-// maximum at half rate, and the two wait for one another through two tiles of
-// scores.  (Products of 128 columns and four tiles: 347 us, bound by shared
-// memory; 16 warps of sums: 288; a tile given back as soon as its last columns
-// are in registers, or the next tile's columns asked for then: 299 and 327;
-// chunks of one product with two places: 297; pairs of blocks with half of the
-// queries each: 287.)  4 requests of 8192 keys take 5 us
-// on the GPU, of which 1.7 pass until a block knows its run and 2.2 more until
-// its queries are there.
+// PFLOP/s (82 to 87 % of the sustained rate of a library product): products and
+// sums wait for one another through two tiles of scores, and the tensor pipe is
+// busy 60 % of the time.  (Products of 128 columns and four tiles: 347 us, bound
+// by shared memory; 16 warps of sums: 288; a tile given back as soon as its last
+// columns are in registers, or the next tile's columns asked for then: 299 and
+// 327; chunks of one product with two places: 297; pairs of blocks with half of
+// the queries each: 287.)  4 requests of 8192 keys take 5 us on the GPU, of which
+// 1.7 pass until a block knows its run and 2.2 more until its queries are there.
 //
 // Warps: 0-3 and 4-7 every other unit of a tile's columns, 8 products, 9 keys, 10
 // queries and weights.
@@ -571,10 +574,13 @@ topk_status_t launch_index_scores(const IndexScoresParams& p, topk_dtype_t dtype
     // Requests of few queries each: chunks of as many, the next one's come
     // while this one's are used, and what room they leave holds more tiles of
     // keys and of scores (three and two of them: one request of 1M keys 48.9
-    // us in place of 47.3, 128 ragged ones 92.9 in place of 89.9).  Else each
-    // key is read for two products (for one: 4096 queries 297 us in place of
-    // 281), and a chunk that begins costs two tiles (2.8 us; with runs of equal
-    // tiles 8 pieces of prompts took 39.8 us in place of 28.7).
+    // us in place of 47.3, 128 ragged ones 92.9 in place of 89.9).  The mean
+    // decides: the host does not know how queries are spread (255 requests of one
+    // query and one of 256, 4096 keys: 50.0 us, as two calls 52.8; 63 and one of
+    // 512, 8192 keys: 77.1 and 71.1).  Else each key is read for two products (for
+    // one: 4096 queries 297 us in place of 281), and a chunk that begins costs two
+    // tiles (2.8 us; with runs of equal tiles 8 pieces of prompts took 39.8 us in
+    // place of 28.7).
     const int most = 8 - log2_heads;  // log2 of a product's queries
     int log2 = 0;
     while (log2 <= most && (int64_t{p.batch} << log2) < p.total_q) ++log2;
